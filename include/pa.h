@@ -67,6 +67,7 @@ typedef enum pa_dtype { PA_F32 = 0, PA_BF16 = 1 } pa_dtype;
 #define PA_DEVERR_BAD_LENGTH 2    /* context length < 0 or beyond its table      */
 #define PA_DEVERR_BAD_SLOT 4      /* slot outside the pool                       */
 #define PA_DEVERR_TIMEOUT 8       /* a bounded pipeline wait expired             */
+#define PA_DEVERR_BAD_POSITION 16 /* position beyond the cos / sin table         */
 
 /* Human-readable text of a status code (static storage, never NULL). */
 const char* pa_get_error_string(int status);
@@ -302,6 +303,94 @@ int pa_decode_fp8(void* out, const void* q, const void* k_cache, const void* v_c
                   int num_q_heads, int head_dim, int block_size, int num_blocks,
                   int max_blocks_per_seq, int max_context_len, int chunk_tokens, void* workspace,
                   size_t workspace_bytes, int32_t* device_errors, void* stream);
+
+/*
+ * Append with rotary positions.  The cache write of pa_reshape_and_cache with the
+ * position rotation of q and k on the way: one pass over a step's rows instead of
+ * one that rotates and one that writes.  For every token t with position
+ * pos = positions[t] >= 0, the first rot_dim columns of each head of q and k turn by
+ * the angles of table row cos_sin[pos] = [cos (rot_dim / 2) | sin (rot_dim / 2)]:
+ *     a' = a cos_i - b sin_i,   b' = b cos_i + a sin_i,   i < rot_dim / 2,
+ * where (a, b) are columns (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved
+ * is non-zero; the other columns stay.  The arithmetic is float32 (each product and
+ * each sum rounded), then
+ *     q_out[t] = q',  and for slot = slot_mapping[t] >= 0 the slot's K row = k' and
+ *     its V row = v (bytes), as in pa_reshape_and_cache,
+ * rounded once to the element type.  A negative position marks a padding token:
+ * nothing of it is read or written, its row of q_out included.  A negative slot
+ * keeps the token out of the cache (q is still rotated).  A position at or beyond
+ * max_position sets PA_DEVERR_BAD_POSITION and the token is skipped like padding; a
+ * slot beyond the pool sets PA_DEVERR_BAD_SLOT and only q is written.
+ *
+ * q [num_tokens][num_q_heads][head_dim], k and v [num_tokens][num_kv_heads][head_dim]
+ * have token strides q_stride, k_stride, v_stride in elements (multiples of 16 bytes;
+ * heads and columns contiguous), so they may be slices of one matrix; q_out is
+ * contiguous, and may be q itself when q is.  num_q_heads 0: q and q_out are not used.
+ * cos_sin: device float32, 16-byte aligned.  rot_dim: a multiple of 16 up to head_dim,
+ * or 0 for no rotation (then num_q_heads is 0, positions and cos_sin may be null, and
+ * every token is live).  slot_mapping and positions are device int64 arrays.
+ *
+ * pa_rope_and_cache_fp8: the pools hold e4m3 codes with a scale per kv head, as for
+ * pa_reshape_and_cache_fp8 (q, k, v bf16, head_dim 128): k' and v are divided by
+ * their head's scale in float32 and stored as the nearest code.
+ */
+int pa_rope_and_cache(void* q_out, const void* q, const void* k, const void* v, void* k_cache,
+                      void* v_cache, const int64_t* slot_mapping, const int64_t* positions,
+                      const float* cos_sin, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                      int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                      int rot_dim, int interleaved, int max_position, int block_size,
+                      int num_blocks, pa_dtype dtype, int32_t* device_errors, void* stream);
+int pa_rope_and_cache_fp8(void* q_out, const void* q, const void* k, const void* v, void* k_cache,
+                          void* v_cache, const int64_t* slot_mapping, const int64_t* positions,
+                          const float* cos_sin, const float* k_scale, const float* v_scale,
+                          int64_t q_stride, int64_t k_stride, int64_t v_stride, int num_tokens,
+                          int num_q_heads, int num_kv_heads, int head_dim, int rot_dim,
+                          int interleaved, int max_position, int block_size, int num_blocks,
+                          int32_t* device_errors, void* stream);
+
+/*
+ * e4m3 pools with a scale for each page and head.  k_scales and v_scales are device
+ * float32 [num_blocks][num_kv_heads]: the K element of page p, head h is
+ * code * k_scales[p][h], likewise V.  Unlike the scale per kv head they need no
+ * calibration: the append finds them.
+ *
+ * pa_rope_and_cache_fp8_block: pa_rope_and_cache into such pools (q, k, v bf16,
+ * head_dim 128).  For each page and head that receives rows, amax being the largest
+ * finite magnitude of these rows (k after its rotation) and 2^k the least power of
+ * two with amax <= 448 2^k, k >= -100:
+ *   - when the page's first slot is among the written ones the page begins anew: its
+ *     scale is 2^k;
+ *   - otherwise its scale is max(old scale, 2^k), and when it grew, the page's other
+ *     rows are re-encoded: code' = e4m3(code * old / new).
+ * The rows are stored as e4m3(x / scale) (float32 division, nearest, ties to even,
+ * magnitudes above 448 and infinities saturate, NaN stores a NaN code).  The tokens
+ * that one call puts into a page must stand one after another in the batch (as a
+ * sequence's tokens do) and have distinct slots; more of them than the page has
+ * slots set PA_DEVERR_BAD_SLOT, and those past the page's size are dropped.
+ *
+ * pa_decode_fp8_block: decode over such pools for q_len new tokens per sequence,
+ * causal among them, with the window and sinks of pa_decode_window (0, 0 for none);
+ * q and out bf16, head_dim 128; scales positive and finite.  Logits and sums are
+ * float32; q enters the products as two e4m3 parts (exact for bf16 elements down to
+ * 2^-10 of their row's largest), and so do the probabilities times V's scale (about
+ * the precision of bf16).
+ *
+ * pa_copy_scales: the scale rows of copied pages, dst[d] = src[s] for each pair
+ * (s, d) of pa_copy_blocks (src and dst then the same arrays) or pa_swap_blocks
+ * (either side device memory or pinned host memory).  Same rules for the pairs.
+ */
+int pa_rope_and_cache_fp8_block(void* q_out, const void* q, const void* k, const void* v,
+                                void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                                const int64_t* positions, const float* cos_sin, float* k_scales,
+                                float* v_scales, int64_t q_stride, int64_t k_stride,
+                                int64_t v_stride, int num_tokens, int num_q_heads,
+                                int num_kv_heads, int head_dim, int rot_dim, int interleaved,
+                                int max_position, int block_size, int num_blocks,
+                                int32_t* device_errors, void* stream);
+int pa_copy_scales(const float* src_k_scales, const float* src_v_scales, float* dst_k_scales,
+                   float* dst_v_scales, const int64_t* src_dst_pairs, int num_pairs,
+                   int num_kv_heads, int num_src_blocks, int num_dst_blocks,
+                   int32_t* device_errors, void* stream);
 
 /*
  * Test hook for the failure path.  Every pipeline wait of the decode kernels

@@ -12,6 +12,8 @@ Contents, each written from the pages (cited in the modules):
   * ``copy_blocks``        -- byte copy of whole pages for copy-on-write.
   * ``e4m3_encode`` / ``decode_kv8_f64`` / ``reshape_and_cache_fp8`` -- the same
                               path with float8 e4m3 pools and per-kv-head scales.
+  * ``rotate_f64`` / ``rotate_f32`` / ``page_scale_append`` -- rotary positions and the
+                              append into e4m3 pools with a scale per page and head.
   * ``RefBlockManager``    -- the teaching allocator of "PagedAttention原理" §3.3.4
                               with the reference counts of §3.3.3, copy-on-write and
                               swapping whole sequences to a host pool.
@@ -21,11 +23,14 @@ from ._decode import (build, decode_f64, decode_kv8_f64, decode_multi_f64, libra
                       max_threads, widen)
 from ._cache_ops import (copy_blocks, copy_pages, e4m3_encode, e4m3_value, reshape_and_cache,
                          reshape_and_cache_fp8)
+from ._rope import (E4M3_VALUES, page_scale_append, power_of_two_scale, rotate_f32,
+                    rotate_f64)
 from .ref_block_manager import OutOfBlocks, RefBlockManager, Swapped
 
 __all__ = [
     "build", "decode_f64", "decode_kv8_f64", "decode_multi_f64", "library_path", "max_threads",
     "widen",
     "copy_blocks", "copy_pages", "e4m3_encode", "e4m3_value", "reshape_and_cache",
-    "reshape_and_cache_fp8", "OutOfBlocks", "RefBlockManager", "Swapped",
+    "reshape_and_cache_fp8", "E4M3_VALUES", "page_scale_append", "power_of_two_scale",
+    "rotate_f32", "rotate_f64", "OutOfBlocks", "RefBlockManager", "Swapped",
 ]

@@ -15,6 +15,7 @@ PA_OK = 0
 PA_ERR_OUT_OF_BLOCKS = -3
 PA_ERR_SWAPPED = -8
 PA_DEVERR_BAD_BLOCK, PA_DEVERR_BAD_LENGTH, PA_DEVERR_BAD_SLOT, PA_DEVERR_TIMEOUT = 1, 2, 4, 8
+PA_DEVERR_BAD_POSITION = 16
 
 # Every function include/pa.h declares (checked by the tests).
 EXPORTED_SYMBOLS = [
@@ -22,7 +23,8 @@ EXPORTED_SYMBOLS = [
     "pa_decode_workspace_size", "pa_decode", "pa_decode_noalloc", "pa_debug_set_wait_limit",
     "pa_read_device_errors", "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_swap_blocks",
     "pa_decode_multi", "pa_decode_cascade", "pa_decode_cascade_workspace_size",
-    "pa_cascade_groups",
+    "pa_cascade_groups", "pa_rope_and_cache", "pa_rope_and_cache_fp8",
+    "pa_rope_and_cache_fp8_block", "pa_copy_scales",
     "pa_bm_create", "pa_bm_destroy", "pa_bm_add_seq", "pa_bm_append_slot", "pa_bm_fork",
     "pa_bm_free", "pa_bm_block_table", "pa_bm_refcount", "pa_bm_num_free", "pa_bm_free_list",
     "pa_bm_stats", "pa_bm_append_slots", "pa_bm_build_block_tables", "pa_bm_enable_swap",
@@ -61,6 +63,10 @@ _SIGNATURES = {
     "pa_decode_cascade_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32]),
     "pa_cascade_groups": (_i32, [_pi32, _pi32, _i32, _i32, _i32, _pi32, _pi32,
                                  ctypes.POINTER(_i32)]),
+    "pa_rope_and_cache": (_i32, [_vp] * 9 + [_i64] * 3 + [_i32] * 10 + [_vp, _vp]),
+    "pa_rope_and_cache_fp8": (_i32, [_vp] * 11 + [_i64] * 3 + [_i32] * 9 + [_vp, _vp]),
+    "pa_rope_and_cache_fp8_block": (_i32, [_vp] * 11 + [_i64] * 3 + [_i32] * 9 + [_vp, _vp]),
+    "pa_copy_scales": (_i32, [_vp] * 5 + [_i32] * 4 + [_vp, _vp]),
     "pa_debug_set_wait_limit": (_i32, [_i32]),
     "pa_read_device_errors": (_i32, [_vp, _pi32, _i32, _vp]),
     "pa_bm_create": (_i32, [_i32, _i32, _pi32, ctypes.POINTER(_vp)]),
@@ -484,6 +490,170 @@ def pa_decode_fp8(out, q, k_cache, v_cache, block_tables, context_lens, scale, k
         return call
     call()
     return out
+
+
+# ------------------------------------------------------------- rotating appends
+def _rows(name, t, dtype, tokens, head_dim):
+    """Checks [tokens, heads, head_dim] rows whose heads and columns are contiguous;
+    returns (heads, token stride)."""
+    if not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, head_dim]")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    n, heads, d = t.shape
+    if n != tokens or d != head_dim:
+        raise ValueError(f"{name} must have {tokens} tokens of head_dim {head_dim}")
+    st, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (heads > 1 and sh != d):
+        raise ValueError(f"{name}: heads and columns must be contiguous")
+    return heads, (st if n > 1 else heads * d)
+
+
+def _run_on(device, call, prepare):
+    """Issue the call with its tensors' device current (or hand it back)."""
+    if prepare:
+        return call
+    import torch
+    if device.index == torch.cuda.current_device():
+        call()
+    else:
+        with torch.cuda.device(device):
+            call()
+
+
+def _same_device(device, tensors):
+    for name, t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the pools on {device}")
+
+
+def _rope_append(name, row_dtype, pool_args, last, q_out, q, k, v, k_cache, v_cache, slot_mapping,
+                 positions, cos_sin, interleaved, device_errors, stream, prepare):
+    import torch
+    NB, Hkv, bs, D = k_cache.shape
+    dev = k_cache.device
+    _need_cuda_contig("k_cache", k_cache)
+    _need_cuda_contig("v_cache", v_cache)
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache differ in shape or type")
+    T = k.shape[0]
+    hk, k_stride = _rows("k", k, row_dtype, T, D)
+    hv, v_stride = _rows("v", v, row_dtype, T, D)
+    if hk != Hkv or hv != Hkv:
+        raise ValueError("k and v must have the pools' kv heads")
+    Hq, q_stride, rot, most = 0, 0, 0, 0
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            raise ValueError("q and q_out go together")
+        Hq, q_stride = _rows("q", q, row_dtype, T, D)
+        if q_out.shape != q.shape or q_out.dtype != row_dtype or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous, of q's shape and type")
+    ints = (("slot_mapping", slot_mapping), ("positions", positions))
+    if (positions is None) != (cos_sin is None):
+        raise ValueError("positions and cos_sin go together")
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+            raise TypeError("cos_sin must be float32 [max_position, rot_dim]")
+        _need_cuda_contig("cos_sin", cos_sin)
+        most, rot = cos_sin.shape
+    for n, t in ints:
+        if t is None:
+            continue
+        _need_cuda_contig(n, t)
+        if t.dtype != torch.int64:
+            raise TypeError(f"{n} must be int64")
+        if t.numel() != T:
+            raise ValueError(f"{n} must have an entry for each token")
+    _same_device(dev, (("q_out", q_out), ("q", q), ("k", k), ("v", v), ("v_cache", v_cache),
+                       ("cos_sin", cos_sin), ("device_errors", device_errors)) + ints)
+    call = PreparedCall(name, (
+        _ptr(q_out), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
+        _ptr(positions), _ptr(cos_sin), *pool_args, q_stride, k_stride, v_stride, T, Hq, Hkv, D,
+        rot, 1 if interleaved else 0, most, bs, NB, *last, _ptr(device_errors),
+        _stream(stream, dev)))
+    return _run_on(dev, call, prepare)
+
+
+def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                      interleaved=False, device_errors=None, stream=None, prepare=False):
+    """Rotate q and k and write k, v into their slots (see pa.h).  q [T, Hq, D], k and v
+    [T, Hkv, D] may be slices of one matrix (any token stride); caches [NB, Hkv, bs, D] of
+    their type; slot_mapping, positions int64 [T]; cos_sin float32 [max_position, rot_dim]
+    (cos of rot_dim / 2 angles, then their sin).  q and q_out may both be None, and
+    positions and cos_sin too (no rotation)."""
+    if k_cache.dtype != k.dtype:
+        raise TypeError("the pools must have the type of k")
+    return _rope_append("pa_rope_and_cache", k.dtype, (), (_dtype_code(k),), q_out, q, k, v,
+                        k_cache, v_cache, slot_mapping, positions, cos_sin, interleaved,
+                        device_errors, stream, prepare)
+
+
+def pa_rope_and_cache_fp8(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                          k_scale, v_scale, interleaved=False, device_errors=None, stream=None,
+                          prepare=False):
+    """pa_rope_and_cache into e4m3 pools with a scale per kv head: k_scale, v_scale
+    float32 [Hkv]; q, k, v bf16 (see pa.h)."""
+    import torch
+    _need_fp8_pool("k_cache", k_cache)
+    _need_fp8_pool("v_cache", v_cache)
+    _need_scales(k_scale, v_scale, k_cache.shape[1])
+    _same_device(k_cache.device, (("k_scale", k_scale), ("v_scale", v_scale)))
+    return _rope_append("pa_rope_and_cache_fp8", torch.bfloat16, (_ptr(k_scale), _ptr(v_scale)),
+                        (), q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                        interleaved, device_errors, stream, prepare)
+
+
+def _need_page_scales(k_cache, k_scales, v_scales):
+    import torch
+    for n, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        _need_cuda_contig(n, t)
+        if t.dtype != torch.float32 or t.shape != k_cache.shape[:2]:
+            raise TypeError(f"{n} must be float32 [num_blocks, num_kv_heads]")
+    _same_device(k_cache.device, (("k_scales", k_scales), ("v_scales", v_scales)))
+
+
+def pa_rope_and_cache_fp8_block(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                                k_scales, v_scales, interleaved=False, device_errors=None,
+                                stream=None, prepare=False):
+    """pa_rope_and_cache into e4m3 pools with a scale for each page and head, which the
+    call finds and updates: k_scales, v_scales float32 [NB, Hkv]; q, k, v bf16 (see pa.h)."""
+    import torch
+    _need_fp8_pool("k_cache", k_cache)
+    _need_fp8_pool("v_cache", v_cache)
+    _need_page_scales(k_cache, k_scales, v_scales)
+    return _rope_append("pa_rope_and_cache_fp8_block", torch.bfloat16,
+                        (_ptr(k_scales), _ptr(v_scales)), (), q_out, q, k, v, k_cache, v_cache,
+                        slot_mapping, positions, cos_sin, interleaved, device_errors, stream,
+                        prepare)
+
+
+def pa_copy_scales(src_k_scales, src_v_scales, dst_k_scales, dst_v_scales, src_dst_pairs,
+                   device_errors=None, stream=None, prepare=False):
+    """The scale rows of copied pages, dst[d] = src[s] for each (s, d) of src_dst_pairs
+    (int64 [P, 2] on the device): after pa_copy_blocks (src and dst the same arrays) or
+    pa_swap_blocks (either side device or pinned host memory); float32 [blocks, Hkv]."""
+    import torch
+    heads = src_k_scales.shape[1]
+    for n, t, like in (("src_k_scales", src_k_scales, src_k_scales),
+                       ("src_v_scales", src_v_scales, src_k_scales),
+                       ("dst_k_scales", dst_k_scales, dst_k_scales),
+                       ("dst_v_scales", dst_v_scales, dst_k_scales)):
+        if not t.is_contiguous() or not (t.is_cuda or t.is_pinned()):
+            raise ValueError(f"{n} must be a contiguous CUDA tensor or pinned host tensor")
+        if t.dtype != torch.float32 or t.dim() != 2 or t.shape[1] != heads or t.shape != like.shape:
+            raise TypeError(f"{n} must be float32 [blocks, num_kv_heads]")
+    _need_cuda_contig("src_dst_pairs", src_dst_pairs)
+    if src_dst_pairs.dtype != torch.int64:
+        raise TypeError("src_dst_pairs must be int64")
+    dev = src_dst_pairs.device
+    _same_device(dev, [(n, t) for n, t in (
+        ("src_k_scales", src_k_scales), ("src_v_scales", src_v_scales),
+        ("dst_k_scales", dst_k_scales), ("dst_v_scales", dst_v_scales)) if t.is_cuda])
+    call = PreparedCall("pa_copy_scales", (
+        _ptr(src_k_scales), _ptr(src_v_scales), _ptr(dst_k_scales), _ptr(dst_v_scales),
+        _ptr(src_dst_pairs), int(src_dst_pairs.shape[0]), int(heads), int(src_k_scales.shape[0]),
+        int(dst_k_scales.shape[0]), _ptr(device_errors), _stream(stream, dev)))
+    return _run_on(dev, call, prepare)
 
 
 def pa_debug_set_wait_limit(polls: int) -> None:

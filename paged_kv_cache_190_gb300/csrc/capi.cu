@@ -6,20 +6,10 @@
 #include <cstdint>
 
 #include "../../include/pa.h"
+#include "pa_host.h"
 #include "pa_internal.h"
 
-namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Bound on each decode pipeline wait, in polls (< 0: the kernels' default).
-std::atomic<int64_t> g_wait_limit{-1};
-
-bool supported_shape(int head_dim, int block_size) {
-  return (head_dim == 64 || head_dim == 128) && (block_size == 16 || block_size == 32);
-}
-
-int elt_size(pa_dtype dt) { return dt == PA_BF16 ? 2 : (dt == PA_F32 ? 4 : 0); }
+namespace pa {
 
 // SM count of the current device (cached per device id).
 int current_sm_count() {
@@ -35,6 +25,23 @@ int current_sm_count() {
   if (dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_relaxed);
   return n;
 }
+
+}  // namespace pa
+
+namespace {
+
+using pa::current_sm_count;
+
+using pa::aligned16;
+
+// Bound on each decode pipeline wait, in polls (< 0: the kernels' default).
+std::atomic<int64_t> g_wait_limit{-1};
+
+bool supported_shape(int head_dim, int block_size) {
+  return (head_dim == 64 || head_dim == 128) && (block_size == 16 || block_size == 32);
+}
+
+int elt_size(pa_dtype dt) { return dt == PA_BF16 ? 2 : (dt == PA_F32 ? 4 : 0); }
 
 // Split size: halve 512 until the (sequence, kv head, chunk) items give every
 // SM a few, but never below 64 tokens; at most 32 pages per chunk.
@@ -53,6 +60,10 @@ bool valid_chunk(int chunk, int block_size) {
 }
 
 }  // namespace
+
+namespace pa {
+int64_t wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+}  // namespace pa
 
 extern "C" {
 
