@@ -305,6 +305,39 @@ int pa_decode_fp8(void* out, const void* q, const void* k_cache, const void* v_c
                   size_t workspace_bytes, int32_t* device_errors, void* stream);
 
 /*
+ * Decode attention with a sliding window and a few first tokens that stay visible
+ * ("sinks"), for q_len new tokens per sequence, causal among them as in
+ * pa_decode_multi: new token j of sequence b sits at position p = L_b - q_len + j and
+ * attends to the positions t <= p with p - t < window or t < sinks,
+ *     out[b][j][i] = softmax_t(scale q[b][j][i] . K_t) V_t.
+ * window 0 (sinks then 0 too) is no window: all positions up to p.  The cost is that of
+ * the visible tokens: table entries of pages of which no new token sees a position are
+ * not read (the pages may have been given back), and what stands in positions that none
+ * sees does not matter, NaN and infinities included.  (A NaN or infinity in the V row of
+ * a position that some new token of the sequence sees reaches every row of that kv head
+ * in bf16 and e4m3 pools, as in pa_decode_multi.)
+ *
+ * q and out are [num_seqs][q_len][num_q_heads][head_dim] ([num_seqs][num_q_heads]
+ * [head_dim] for q_len 1) in the pools' type, PA_F32 or PA_BF16;
+ * q_len * (num_q_heads / num_kv_heads) must be 1, 2, 4 or 8.  context_lens,
+ * max_context_len, block_tables, device_errors and rows without a visible token as in
+ * pa_decode_multi.  workspace: device scratch of pa_decode_window_workspace_size bytes
+ * (num_q_heads there counts the rows of all new tokens, q_len * num_q_heads; it does not
+ * grow with the batch or the context), 256-byte aligned; it carries no state between
+ * calls, but two calls in flight at once must not share it.  The results do not depend
+ * on what else runs, bit for bit.
+ */
+size_t pa_decode_window_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                                       int head_dim, int block_size, int max_context_len,
+                                       int window, int sinks);
+int pa_decode_window(void* out, const void* q, const void* k_cache, const void* v_cache,
+                     const int32_t* block_tables, const int32_t* context_lens, float scale,
+                     int num_kv_heads, int num_seqs, int num_q_heads, int q_len, int head_dim,
+                     int block_size, int num_blocks, int max_blocks_per_seq, int max_context_len,
+                     int window, int sinks, pa_dtype dtype, void* workspace,
+                     size_t workspace_bytes, int32_t* device_errors, void* stream);
+
+/*
  * Append with rotary positions.  The cache write of pa_reshape_and_cache with the
  * position rotation of q and k on the way: one pass over a step's rows instead of
  * one that rotates and one that writes.  For every token t with position
@@ -370,7 +403,8 @@ int pa_rope_and_cache_fp8(void* q_out, const void* q, const void* k, const void*
  *
  * pa_decode_fp8_block: decode over such pools for q_len new tokens per sequence,
  * causal among them, with the window and sinks of pa_decode_window (0, 0 for none);
- * q and out bf16, head_dim 128; scales positive and finite.  Logits and sums are
+ * q and out bf16, head_dim 128; scales positive and finite; workspace of
+ * pa_decode_window_workspace_size.  Logits and sums are
  * float32; q enters the products as two e4m3 parts (exact for bf16 elements down to
  * 2^-10 of their row's largest), and so do the probabilities times V's scale (about
  * the precision of bf16).
@@ -387,6 +421,13 @@ int pa_rope_and_cache_fp8_block(void* q_out, const void* q, const void* k, const
                                 int num_kv_heads, int head_dim, int rot_dim, int interleaved,
                                 int max_position, int block_size, int num_blocks,
                                 int32_t* device_errors, void* stream);
+int pa_decode_fp8_block(void* out, const void* q, const void* k_cache, const void* v_cache,
+                        const int32_t* block_tables, const int32_t* context_lens, float scale,
+                        const float* k_scales, const float* v_scales, int num_kv_heads,
+                        int num_seqs, int num_q_heads, int q_len, int head_dim, int block_size,
+                        int num_blocks, int max_blocks_per_seq, int max_context_len, int window,
+                        int sinks, void* workspace, size_t workspace_bytes,
+                        int32_t* device_errors, void* stream);
 int pa_copy_scales(const float* src_k_scales, const float* src_v_scales, float* dst_k_scales,
                    float* dst_v_scales, const int64_t* src_dst_pairs, int num_pairs,
                    int num_kv_heads, int num_src_blocks, int num_dst_blocks,

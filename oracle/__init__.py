@@ -14,6 +14,8 @@ Contents, each written from the pages (cited in the modules):
                               path with float8 e4m3 pools and per-kv-head scales.
   * ``rotate_f64`` / ``rotate_f32`` / ``page_scale_append`` -- rotary positions and the
                               append into e4m3 pools with a scale per page and head.
+  * ``decode_window_f64``  -- decode with a sliding window and first tokens that stay
+                              visible, and what its error bars are made of.
   * ``RefBlockManager``    -- the teaching allocator of "PagedAttention原理" §3.3.4
                               with the reference counts of §3.3.3, copy-on-write and
                               swapping whole sequences to a host pool.
@@ -25,6 +27,7 @@ from ._cache_ops import (copy_blocks, copy_pages, e4m3_encode, e4m3_value, resha
                          reshape_and_cache_fp8)
 from ._rope import (E4M3_VALUES, page_scale_append, power_of_two_scale, rotate_f32,
                     rotate_f64)
+from ._window import decode_window_f64, seen
 from .ref_block_manager import OutOfBlocks, RefBlockManager, Swapped
 
 __all__ = [
@@ -32,5 +35,5 @@ __all__ = [
     "widen",
     "copy_blocks", "copy_pages", "e4m3_encode", "e4m3_value", "reshape_and_cache",
     "reshape_and_cache_fp8", "E4M3_VALUES", "page_scale_append", "power_of_two_scale",
-    "rotate_f32", "rotate_f64", "OutOfBlocks", "RefBlockManager", "Swapped",
+    "decode_window_f64", "seen", "rotate_f32", "rotate_f64", "OutOfBlocks", "RefBlockManager", "Swapped",
 ]

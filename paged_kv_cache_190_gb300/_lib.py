@@ -24,7 +24,8 @@ EXPORTED_SYMBOLS = [
     "pa_read_device_errors", "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_swap_blocks",
     "pa_decode_multi", "pa_decode_cascade", "pa_decode_cascade_workspace_size",
     "pa_cascade_groups", "pa_rope_and_cache", "pa_rope_and_cache_fp8",
-    "pa_rope_and_cache_fp8_block", "pa_copy_scales",
+    "pa_rope_and_cache_fp8_block", "pa_copy_scales", "pa_decode_window_workspace_size",
+    "pa_decode_window", "pa_decode_fp8_block",
     "pa_bm_create", "pa_bm_destroy", "pa_bm_add_seq", "pa_bm_append_slot", "pa_bm_fork",
     "pa_bm_free", "pa_bm_block_table", "pa_bm_refcount", "pa_bm_num_free", "pa_bm_free_list",
     "pa_bm_stats", "pa_bm_append_slots", "pa_bm_build_block_tables", "pa_bm_enable_swap",
@@ -67,6 +68,10 @@ _SIGNATURES = {
     "pa_rope_and_cache_fp8": (_i32, [_vp] * 11 + [_i64] * 3 + [_i32] * 9 + [_vp, _vp]),
     "pa_rope_and_cache_fp8_block": (_i32, [_vp] * 11 + [_i64] * 3 + [_i32] * 9 + [_vp, _vp]),
     "pa_copy_scales": (_i32, [_vp] * 5 + [_i32] * 4 + [_vp, _vp]),
+    "pa_decode_window_workspace_size": (_sz, [_i32] * 8),
+    "pa_decode_window": (_i32, [_vp] * 6 + [ctypes.c_float] + [_i32] * 12 + [_vp, _sz, _vp, _vp]),
+    "pa_decode_fp8_block": (_i32, [_vp] * 6 + [ctypes.c_float, _vp, _vp] + [_i32] * 11 +
+                            [_vp, _sz, _vp, _vp]),
     "pa_debug_set_wait_limit": (_i32, [_i32]),
     "pa_read_device_errors": (_i32, [_vp, _pi32, _i32, _vp]),
     "pa_bm_create": (_i32, [_i32, _i32, _pi32, ctypes.POINTER(_vp)]),
@@ -654,6 +659,91 @@ def pa_copy_scales(src_k_scales, src_v_scales, dst_k_scales, dst_v_scales, src_d
         _ptr(src_dst_pairs), int(src_dst_pairs.shape[0]), int(heads), int(src_k_scales.shape[0]),
         int(dst_k_scales.shape[0]), _ptr(device_errors), _stream(stream, dev)))
     return _run_on(dev, call, prepare)
+
+
+# ------------------------------------------- windowed and page-scaled decode
+def pa_decode_window_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                    max_context_len, window=0, sinks=0) -> int:
+    """Bytes of workspace of pa_decode_window and pa_decode_fp8_block; num_q_heads counts
+    the rows of all new tokens (q_len * Hq)."""
+    return int(library().pa_decode_window_workspace_size(
+        int(num_seqs), int(num_q_heads), int(num_kv_heads), int(head_dim), int(block_size),
+        int(max_context_len), int(window), int(sinks)))
+
+
+def _span_decode(name, scales, out, q, k_cache, v_cache, block_tables, context_lens, scale,
+                 num_kv_heads, max_context_len, window, sinks, workspace, device_errors, stream,
+                 prepare):
+    import torch
+    for n, t in (("out", out), ("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
+                 ("block_tables", block_tables), ("context_lens", context_lens)):
+        _need_cuda_contig(n, t)
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    if q.dim() == 3:
+        B, Hq, D = q.shape
+        q_len = 1
+    elif q.dim() == 4:
+        B, q_len, Hq, D = q.shape
+    else:
+        raise ValueError("q must be [B, Hq, D] or [B, q_len, Hq, D]")
+    NB, Hkv, bs, Dc = k_cache.shape
+    if Hkv != num_kv_heads:
+        raise ValueError("num_kv_heads does not match the cache shape")
+    if Dc != D or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("the pools differ in shape or type, or have another head_dim than q")
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and type")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.numel() != B:
+        raise ValueError("block_tables and context_lens must have a row for each sequence")
+    dev = q.device
+    _same_device(dev, (("out", out), ("k_cache", k_cache), ("v_cache", v_cache),
+                       ("block_tables", block_tables), ("context_lens", context_lens),
+                       ("workspace", workspace), ("device_errors", device_errors)))
+    if workspace is None:
+        with torch.cuda.device(dev):
+            nbytes = pa_decode_window_workspace_size(B, q_len * Hq, Hkv, D, bs, max_context_len,
+                                                     window, sinks)
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    head = (_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+            _ptr(context_lens), scale)
+    sizes = (Hkv, B, Hq, q_len, D, bs, NB, block_tables.shape[1], max_context_len, window, sinks)
+    kind = () if scales else (_dtype_code(q),)
+    call = PreparedCall(name, head + scales + sizes + kind + (
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(device_errors),
+        _stream(stream, dev)))
+    return call if prepare else (_run_on(dev, call, False), out)[1]
+
+
+def pa_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads,
+                     max_context_len, window, sinks=0, workspace=None, device_errors=None,
+                     stream=None, prepare=False):
+    """Decode with a sliding window and ``sinks`` first tokens that stay visible (window 0:
+    none): out, q [B, Hq, D], or [B, q_len, Hq, D] for q_len new tokens per sequence;
+    caches [NB, Hkv, bs, D] of their type; block_tables int32 [B, max_blocks];
+    context_lens int32 [B] (see pa.h).  ``workspace``: a uint8 CUDA tensor of at least
+    pa_decode_window_workspace_size() bytes; allocated here when None."""
+    if k_cache.dtype != q.dtype:
+        raise TypeError("the pools must have the type of q")
+    return _span_decode("pa_decode_window", (), out, q, k_cache, v_cache, block_tables,
+                        context_lens, scale, num_kv_heads, max_context_len, window, sinks,
+                        workspace, device_errors, stream, prepare)
+
+
+def pa_decode_fp8_block(out, q, k_cache, v_cache, block_tables, context_lens, scale, k_scales,
+                        v_scales, num_kv_heads, max_context_len, window=0, sinks=0,
+                        workspace=None, device_errors=None, stream=None, prepare=False):
+    """pa_decode_window over e4m3 pools with a scale for each page and head: out, q bf16;
+    caches one-byte [NB, Hkv, bs, 128]; k_scales, v_scales float32 [NB, Hkv] (see pa.h)."""
+    import torch
+    _need_fp8_pool("k_cache", k_cache)
+    _need_fp8_pool("v_cache", v_cache)
+    _need_page_scales(k_cache, k_scales, v_scales)
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q and out must be bf16")
+    return _span_decode("pa_decode_fp8_block", (_ptr(k_scales), _ptr(v_scales)), out, q, k_cache,
+                        v_cache, block_tables, context_lens, scale, num_kv_heads,
+                        max_context_len, window, sinks, workspace, device_errors, stream, prepare)
 
 
 def pa_debug_set_wait_limit(polls: int) -> None:

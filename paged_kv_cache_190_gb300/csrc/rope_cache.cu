@@ -29,6 +29,9 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// (No load here goes through the read-only path: the kernels start before the one ahead
+// of them in the stream has ended, and wait for its writes on the device.)
+
 // 16 bytes of a row as floats and back.  E: float or uint16_t (bf16 bits).
 template <typename E>
 struct Vec;
@@ -95,8 +98,8 @@ struct Angles {
         const int i = (k ? lc.c1 : lc.c0) * (N / 2);
 #pragma unroll
         for (int e = 0; e < N / 2; e += 2) {
-          const float2 cc = on ? __ldg(reinterpret_cast<const float2*>(row + i + e)) : make_float2(1.f, 1.f);
-          const float2 ss = on ? __ldg(reinterpret_cast<const float2*>(row + half + i + e)) : make_float2(0.f, 0.f);
+          const float2 cc = on ? *reinterpret_cast<const float2*>(row + i + e) : make_float2(1.f, 1.f);
+          const float2 ss = on ? *reinterpret_cast<const float2*>(row + half + i + e) : make_float2(0.f, 0.f);
           c[k * N / 2 + e] = cc.x; c[k * N / 2 + e + 1] = cc.y;
           s[k * N / 2 + e] = ss.x; s[k * N / 2 + e + 1] = ss.y;
         }
@@ -105,8 +108,8 @@ struct Angles {
       const int i = lc.c0 * N;
 #pragma unroll
       for (int e = 0; e < N; e += 4) {
-        const float4 cc = __ldg(reinterpret_cast<const float4*>(row + i + e));
-        const float4 ss = __ldg(reinterpret_cast<const float4*>(row + half + i + e));
+        const float4 cc = *reinterpret_cast<const float4*>(row + i + e);
+        const float4 ss = *reinterpret_cast<const float4*>(row + half + i + e);
         c[e] = cc.x; c[e + 1] = cc.y; c[e + 2] = cc.z; c[e + 3] = cc.w;
         s[e] = ss.x; s[e + 1] = ss.y; s[e + 2] = ss.z; s[e + 3] = ss.w;
       }
@@ -167,8 +170,8 @@ struct Place {
 };
 __device__ __forceinline__ Place place(const RopeArgs& a, int t, bool speak) {
   Place p;
-  p.pos = a.positions ? __ldg(a.positions + t) : 0;
-  p.slot = __ldg(a.slots + t);
+  p.pos = a.positions ? a.positions[t] : 0;
+  p.slot = a.slots[t];
   p.rotate = p.pos >= 0;
   p.write = p.rotate && p.slot >= 0;
   if (a.positions && p.pos >= a.max_position) {
@@ -229,7 +232,7 @@ __device__ __forceinline__ void rows_of_token(const RopeArgs& a, int t, Kind kin
       dst[lc.c0] = Vec<E>::pack(x0);
       dst[lc.c1] = Vec<E>::pack(x1);
     } else if constexpr (FP8) {
-      const float s = __ldg((kind == kK ? a.k_scale : a.v_scale) + h);
+      const float s = (kind == kK ? a.k_scale : a.v_scale)[h];
       const bool pow2 = is_pow2(s);
       const float inv = pow2 ? pow2_reciprocal(s) : 0.f;
       uint2* dst = reinterpret_cast<uint2*>(kind == kK ? a.k_cache : a.v_cache) +
@@ -334,7 +337,7 @@ __device__ __forceinline__ void append_run(const RopeArgs& a, int t0, int n, uin
     if (turned) {
       const int r = min(i * kRowsPerPass + row, n - 1);
       Angles<N, D, INTER> an;
-      an.load(a.cos_sin + __ldg(a.positions + t0 + r) * a.rot_dim, a.rot_dim / 2, lc);
+      an.load(a.cos_sin + a.positions[t0 + r] * a.rot_dim, a.rot_dim / 2, lc);
       rotate<N, D, INTER>(x0, x1, lc, an);
     }
   };
@@ -377,7 +380,7 @@ __device__ __forceinline__ void append_run(const RopeArgs& a, int t0, int n, uin
     if (r < n) {
       float x0[N], x1[N];
       values(i, x0, x1);
-      const int off = static_cast<int>(__ldg(a.slots + t0 + r) - page * BS);
+      const int off = static_cast<int>(a.slots[t0 + r] - page * BS);
       uint2* dst = reinterpret_cast<uint2*>(base + off * D);
       dst[lc.c0] = e4m3x8(x0, s, pow2, inv);
       dst[lc.c1] = e4m3x8(x1, s, pow2, inv);
@@ -440,7 +443,7 @@ __global__ void __launch_bounds__(kThreads) rope_and_cache_page_scale_kernel(
       n = BS;                                              // more tokens than slots: refused
       if (lane == 0) report(a.device_errors, PA_DEVERR_BAD_SLOT);
     }
-    const uint32_t bit = lane < n ? 1u << static_cast<uint32_t>(__ldg(a.slots + tt) - pg * BS) : 0u;
+    const uint32_t bit = lane < n ? 1u << static_cast<uint32_t>(a.slots[tt] - pg * BS) : 0u;
     const uint32_t offsets = __reduce_or_sync(0xffffffffu, bit);
     for (; k < items; k += warps_per_tile)
       append_run<INTER, BS>(a, s, n, offsets, pg, offsets & 1u, k >> 1, k & 1);

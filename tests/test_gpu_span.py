@@ -1,0 +1,329 @@
+"""The windowed decode and the decode over page-scaled e4m3 pools on the GPU against the
+oracle; span_cases.Decode.bar has the error bars."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import paged_kv_cache_190_gb300 as pa
+from gpu_helpers import DEV, out_as_f64, to_dev
+from span_cases import Decode
+
+pytestmark = pytest.mark.gpu
+
+
+class Dev:
+    def __init__(self, c):
+        self.c = c
+        bf = c.dtype != "f32"
+        q = c.q if c.q_len > 1 else c.q[:, 0]
+        self.q = to_dev(q, bf)
+        self.kc, self.vc = (to_dev(x, c.dtype == "bf16") for x in (c.k_cache, c.v_cache))
+        self.tables, self.lens = to_dev(c.tables), to_dev(c.lens)
+        self.scales = tuple(to_dev(s) for s in c.scales)
+        self.out = torch.full(self.q.shape, float("nan"), dtype=self.q.dtype, device=DEV)
+        self.errs = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def call(self, out=None, **kw):
+        c = self.c
+        out = self.out if out is None else out
+        kw = dict(max_context_len=int(c.lens.max()), window=c.window, sinks=c.sinks, device_errors=self.errs) | kw
+        if c.dtype == "fp8":
+            return pa.pa_decode_fp8_block(out, self.q, self.kc, self.vc, self.tables, self.lens, c.scale,
+                                          *self.scales, c.hkv, **kw)
+        return pa.pa_decode_window(out, self.q, self.kc, self.vc, self.tables, self.lens, c.scale, c.hkv, **kw)
+
+    def errors(self):
+        return pa.pa_read_device_errors(self.errs)
+
+
+def check(c, got, rows=None):
+    want, parts = c.want()
+    got = out_as_f64(got).reshape(want.shape)
+    bar = c.bar(want, parts)
+    if rows is not None:
+        got, want, bar = got[rows], want[rows], bar[rows]
+    worst = np.max(np.abs(got - want) / bar)
+    assert np.all(np.abs(got - want) <= bar), f"error {worst:.2f} of its bar"
+
+
+# (dtype, q_len, Hq, Hkv, D, bs)
+KINDS = [("bf16", 1, 8, 8, 128, 16), ("bf16", 1, 8, 2, 128, 32), ("bf16", 2, 8, 2, 64, 16), ("bf16", 1, 6, 3, 64, 32),
+         ("bf16", 8, 2, 2, 128, 16), ("f32", 1, 8, 8, 64, 16), ("f32", 1, 8, 1, 128, 16), ("f32", 4, 2, 1, 64, 32),
+         ("f32", 2, 3, 3, 128, 32), ("fp8", 1, 32, 8, 128, 16), ("fp8", 1, 3, 3, 128, 32), ("fp8", 2, 8, 2, 128, 16),
+         ("fp8", 8, 4, 4, 128, 32), ("fp8", 1, 8, 1, 128, 16)]
+WINDOWS = [(0, 0), (1, 0), (1, 1), (16, 4), (33, 0), (64, 17), (100, 70), (5000, 2)]
+
+
+@pytest.mark.parametrize("dtype,q_len,hq,hkv,d,bs", KINDS)
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+def test_small_calls(dtype, q_len, hq, hkv, d, bs, window, sinks):
+    lens = [q_len, q_len + 1, 15 + q_len, 16 + q_len, 33 + q_len, 97, 131, 300]
+    c = Decode(len(dtype) + q_len + hq + bs + window, dtype, lens, q_len, hq, hkv, d, bs, window, sinks, spread=3)
+    dv = Dev(c)
+    dv.call()
+    assert dv.errors() == 0
+    check(c, dv.out)
+
+
+@pytest.mark.parametrize("dtype,q_len,hq,hkv,d,bs", [
+    ("bf16", 1, 16, 8, 128, 16), ("bf16", 2, 8, 2, 128, 32), ("bf16", 1, 3, 3, 64, 16), ("f32", 1, 8, 8, 64, 16),
+    ("f32", 8, 1, 1, 128, 16), ("fp8", 1, 16, 8, 128, 16), ("fp8", 1, 16, 16, 128, 16), ("fp8", 2, 8, 2, 128, 32),
+    ("fp8", 8, 1, 1, 128, 16)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 4), (90, 33)])
+def test_large_calls_in_shares(dtype, q_len, hq, hkv, d, bs, window, sinks):
+    """Enough work that it goes out in equal shares, with sequences cut anywhere, several
+    in a share, and one that spans many shares."""
+    r = np.random.default_rng(hq + d)
+    lens = [int(x) for x in r.integers(q_len, 400, 37)] + [6000, q_len, 3000]
+    c = Decode(hq + hkv + bs, dtype, lens, q_len, hq, hkv, d, bs, window, sinks, spread=2)
+    dv = Dev(c)
+    # the bound that the caller gives may be far above the lengths
+    width = 120000 // bs
+    tables = torch.full((len(lens), width), -1, dtype=torch.int32, device=DEV)
+    tables[:, :dv.tables.shape[1]] = dv.tables
+    dv.tables = tables
+    dv.call(max_context_len=120000, window=window or 0)
+    assert dv.errors() == 0
+    check(c, dv.out)
+    again = torch.empty_like(dv.out)
+    dv.call(again, max_context_len=120000, workspace=torch.full((64 << 20,), 0x7F, dtype=torch.uint8, device=DEV))
+    assert torch.equal(again.view(torch.int16), dv.out.view(torch.int16)), "not the same bits twice"
+
+
+def test_one_long_sequence_over_all_shares():
+    c = Decode(3, "fp8", [50000], 1, 8, 8, 128, 16, spread=1)
+    dv = Dev(c)
+    dv.call()
+    assert dv.errors() == 0
+    check(c, dv.out)
+    c = Decode(4, "bf16", [40001, 7], 1, 2, 2, 64, 32, window=39000, sinks=5)
+    dv = Dev(c)
+    dv.call()
+    assert dv.errors() == 0
+    check(c, dv.out)
+
+
+@pytest.mark.parametrize("big", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+def test_empty_sequences_and_refused_lengths(dtype, big):
+    d = 128
+    lens = [0, 40, 0, 3, 70] + [0] * 9
+    c = Decode(5, dtype, lens, 1, 4, 2, d, 16, window=30, sinks=2)
+    dv = Dev(c)
+    most = 200000 if big else 80
+    if big:
+        dv.tables = torch.nn.functional.pad(dv.tables, (0, 200000 // 16 - dv.tables.shape[1]), value=-1)
+    else:
+        dv.tables = torch.nn.functional.pad(dv.tables, (0, 6), value=-1)
+    kw = dict(max_context_len=most, window=30 if not big else 30)
+    dv.call(**kw)
+    assert dv.errors() == 0
+    check(c, dv.out)
+    assert bool((dv.out[[0, 2]] == 0).all())
+    dv.lens[0] = -5
+    dv.call(**kw)
+    assert dv.errors() == pa.PA_DEVERR_BAD_LENGTH
+    check(c, dv.out)
+
+
+def test_length_past_the_bound_is_flagged_and_cut():
+    c = Decode(6, "bf16", [48, 48], 1, 2, 2, 64, 16)
+    dv = Dev(c)
+    dv.lens[1] = 100
+    dv.call(max_context_len=48)
+    assert dv.errors() == pa.PA_DEVERR_BAD_LENGTH
+    check(c, dv.out)
+
+
+def test_fewer_tokens_than_new_ones():
+    c = Decode(7, "bf16", [2, 40], 4, 2, 2, 128, 16, window=9)
+    dv = Dev(c)
+    dv.call()
+    assert dv.errors() == pa.PA_DEVERR_BAD_LENGTH
+    assert bool((dv.out[0, :2] == 0).all())
+    check(c, dv.out)
+
+
+@pytest.mark.parametrize("dtype,bs", [("bf16", 16), ("f32", 16), ("fp8", 16), ("fp8", 32)])
+def test_missing_pages_are_flagged_and_left_out(dtype, bs):
+    """A bad entry inside the window: its tokens drop out as if they were not there."""
+    c = Decode(8, dtype, [200, 200, 64], 1, 4, 2, 128, bs, window=100, sinks=3)
+    bad = 150 // bs
+    dv = Dev(c)
+    dv.tables[1, bad] = c.nb + 3
+    dv.call()
+    assert dv.errors() == pa.PA_DEVERR_BAD_BLOCK
+    check(c, dv.out, rows=[0, 2])
+    got = out_as_f64(dv.out)[1]
+    page = [p for p in range(200) if p < 3 or (p >= 100 and p // bs != bad)]
+    from rope_cases import values
+    if dtype == "fp8":
+        k, v = (oracle.E4M3_VALUES[x] * s[:, :, None, None].astype(np.float64)
+                for x, s in zip((c.k_cache, c.v_cache), c.scales))
+    else:
+        k, v = (values(x).astype(np.float64) for x in (c.k_cache, c.v_cache))
+    for i in range(4):
+        kk, vv = (np.stack([x[c.tables[1, p // bs], i // 2, p % bs] for p in page]) for x in (k, v))
+        s = c.scale * kk @ values(c.q)[1, 0, i].astype(np.float64)
+        w = np.exp(s - s.max())
+        w /= w.sum()
+        assert np.max(np.abs(got[i] - w @ vv)) <= (1e-5 if dtype == "f32" else 2e-2)
+
+
+def test_no_window_agrees_with_the_full_decode():
+    c = Decode(9, "bf16", [700, 33, 1], 1, 16, 4, 128, 16)
+    dv = Dev(c)
+    dv.call()
+    full = torch.empty_like(dv.out)
+    pa.pa_decode(full, dv.q, dv.kc, dv.vc, dv.tables, dv.lens, c.scale, c.hkv, 700, device_errors=dv.errs)
+    assert dv.errors() == 0
+    check(c, dv.out)
+    check(c, full)
+
+
+@pytest.mark.parametrize("norm", [1e-30, 2.0 ** -20, 2.0 ** 12, 0.0])
+def test_first_pages_with_values_of_another_size(norm):
+    """V rows of the first page far smaller (as first tokens' are) or larger than the rest."""
+    c = Decode(10, "fp8", [16, 20, 333], 1, 8, 2, 128, 16, first_norm=norm)
+    dv = Dev(c)
+    dv.call()
+    assert dv.errors() == 0
+    check(c, dv.out)
+
+
+def test_wide_scores():
+    for dtype in ("bf16", "f32", "fp8"):
+        c = Decode(11, dtype, [400, 77], 1, 8, 4, 128, 16, window=150, sinks=4, std=4.0)
+        dv = Dev(c)
+        dv.call()
+        check(c, dv.out)
+
+
+@pytest.mark.parametrize("dtype,lens", [("bf16", [300, 900]), ("fp8", [300, 900]), ("f32", [300, 900]),
+                                        ("bf16", [3000] * 60), ("fp8", [5000] * 60)])
+@pytest.mark.parametrize("polls", [0, 40])
+def test_expired_waits_report_and_leave_the_context_usable(dtype, lens, polls):
+    B, hkv, d, bs = len(lens), 8, 128, 16
+    r = torch.Generator(device=DEV).manual_seed(1)
+    width = -(-max(lens) // bs)
+    nb = 512
+    tables = torch.randint(0, nb, (B, width), generator=r, device=DEV, dtype=torch.int32)
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    q = torch.randn(B, 8, d, generator=r, device=DEV).to(dt)
+    kc = torch.randn(nb, hkv, bs, d, generator=r, device=DEV)
+    vc = torch.randn(nb, hkv, bs, d, generator=r, device=DEV)
+    kc, vc = (x.to(torch.float8_e4m3fn) if dtype == "fp8" else x.to(dt) for x in (kc, vc))
+    one = torch.ones(nb, hkv, device=DEV)
+    errs = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def call():
+        out = torch.empty_like(q)
+        if dtype == "fp8":
+            pa.pa_decode_fp8_block(out, q, kc, vc, tables, n, d ** -0.5, one, one, hkv, max(lens), device_errors=errs)
+        else:
+            pa.pa_decode_window(out, q, kc, vc, tables, n, d ** -0.5, hkv, max(lens), 0, device_errors=errs)
+        return out
+
+    want = call()
+    assert pa.pa_read_device_errors(errs) == 0
+    try:
+        pa.pa_debug_set_wait_limit(polls)
+        call()
+        flags = pa.pa_read_device_errors(errs)
+    finally:
+        pa.pa_debug_set_wait_limit(-1)
+    assert flags == pa.PA_DEVERR_TIMEOUT if polls == 0 else flags & ~pa.PA_DEVERR_TIMEOUT == 0
+    assert torch.equal(call().view(torch.int16), want.view(torch.int16))
+    assert pa.pa_read_device_errors(errs) == 0
+
+
+def test_pools_past_32_bit_offsets():
+    """Pages at the far end of pools of more than 2^32 bytes."""
+    hkv, bs, d = 32, 16, 128
+    nb = (1 << 32) // (hkv * bs * d) + 9
+    kc = torch.zeros(nb, hkv, bs, d, dtype=torch.uint8, device=DEV)
+    vc = torch.zeros_like(kc)
+    ks = torch.full((nb, hkv), float("nan"), device=DEV)
+    vs = ks.clone()
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x = torch.randn(2, 40, hkv, d, generator=g, device=DEV).to(torch.bfloat16)
+    page = torch.tensor([nb - 1, nb - 5, nb - 3], device=DEV)
+    slots = (page[:, None] * bs + torch.arange(bs, device=DEV)).flatten()[:40]
+    errs = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pa.pa_rope_and_cache_fp8_block(None, None, x[0], x[1], kc, vc, slots, None, None, ks, vs, device_errors=errs)
+    q = torch.randn(1, hkv, d, generator=g, device=DEV).to(torch.bfloat16)
+    out = torch.empty_like(q)
+    pa.pa_decode_fp8_block(out, q, kc, vc, page.int()[None], torch.tensor([40], dtype=torch.int32, device=DEV),
+                           d ** -0.5, ks, vs, hkv, 48, device_errors=errs)
+    assert pa.pa_read_device_errors(errs) == 0
+    s = torch.einsum("hd,thd->ht", q[0].double(), x[0].double()) * d ** -0.5
+    want = torch.einsum("ht,thd->hd", s.softmax(-1), x[1].double())
+    # e4m3 keys and values: 2^-4 of each V element, and of each key's product
+    dots = torch.einsum("hd,thd->ht", q[0].double().abs(), x[0].double().abs()).amax(-1) * d ** -0.5 * 2.0 ** -4
+    mag = torch.einsum("ht,thd->hd", s.softmax(-1), x[1].double().abs())
+    assert bool(((out[0].double() - want).abs() <= (2.0 ** -4 + 2.0 ** -7 + 2 * dots[:, None]) * mag + 2.0 ** -8).all())
+
+
+def test_other_stream_and_captured_graphs():
+    """Calls on a stream of their own, captured with a workspace each, replayed with other
+    lengths, in turn and against eager calls."""
+    cs = [Decode(12 + i, dt, [300, 45, 200], 1, 8, 4, 128, 16, window=64, sinks=4)
+          for i, dt in enumerate(("bf16", "fp8", "f32"))]
+    dvs = [Dev(c) for c in cs]
+    for dv in dvs:
+        dv.call()
+    eager = [dv.out.clone() for dv in dvs]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(side):
+        for dv in dvs:
+            dv.ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+            dv.call(workspace=dv.ws)
+        side.synchronize()
+        for dv in dvs:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                dv.call(workspace=dv.ws)
+            graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        for dv in dvs:
+            dv.out.fill_(float("nan"))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for dv, e in zip(dvs, eager):
+            assert torch.equal(dv.out.view(torch.int16), e.view(torch.int16))
+    # other inputs in the same buffers
+    for dv in dvs:
+        dv.q.copy_(dv.q.flip(0))
+        dv.lens[1] = 44
+    for g in reversed(graphs):
+        g.replay()
+    torch.cuda.synchronize()
+    for dv in dvs:
+        replayed = dv.out.clone()
+        dv.call()
+        assert torch.equal(dv.out.view(torch.int16), replayed.view(torch.int16))
+        assert dv.errors() == 0
+
+
+def test_refusals_of_the_python_call():
+    c = Decode(15, "bf16", [20, 20], 1, 4, 2, 128, 16)
+    dv = Dev(c)
+    ok = dict(out=dv.out, q=dv.q, k_cache=dv.kc, v_cache=dv.vc, block_tables=dv.tables, context_lens=dv.lens,
+              scale=1.0, num_kv_heads=2, max_context_len=20, window=4)
+    pa.pa_decode_window(**ok)
+    small = torch.empty(256, dtype=torch.uint8, device=DEV)
+    for over, kind in ((dict(q=dv.q.float()), (TypeError, ValueError)), (dict(out=dv.out[:1]), ValueError),
+                       (dict(k_cache=dv.kc.float()), TypeError), (dict(v_cache=dv.vc[:1]), ValueError),
+                       (dict(num_kv_heads=4), ValueError), (dict(context_lens=dv.lens[:1]), ValueError),
+                       (dict(block_tables=dv.tables.long()), TypeError), (dict(window=-1), pa.PaError),
+                       (dict(window=0, sinks=3), pa.PaError), (dict(workspace=small), pa.PaError),
+                       (dict(max_context_len=10 ** 6), pa.PaError),
+                       (dict(block_tables=dv.tables.t()), ValueError), (dict(context_lens=dv.lens.cpu()), ValueError)):
+        with pytest.raises(kind):
+            pa.pa_decode_window(**{**ok, **over})
