@@ -4,19 +4,24 @@ Each CUDA translation unit is compiled by nvcc in parallel with
 ``-gencode arch=compute_103a,code=sm_103a``; the host block manager by g++; the
 objects are linked by nvcc into ``paged_kv_cache_190_gb300/libpagedattn.so``
 (CUDA runtime linked statically, so the library loads on a machine without a
-GPU driver and its block manager works there).
+GPU driver and its block manager works there).  The per-step calls have a C++
+binding for Python, ``_step.so`` beside it, compiled by g++ against torch's headers and
+linked to libpagedattn.so.
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedattn.so")
+BINDING = os.path.join(PKG, "_step.so")
+BINDING_SOURCE = os.path.join(CSRC, "step_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CU_SOURCES = ["capi.cu", "cache_ops.cu", "decode_launch.cu", "decode_bf16.cu", "decode_f32.cu",
               "decode_fp8.cu", "decode_noalloc.cu", "cascade.cu", "rope_cache.cu", "capi_rope.cu",
@@ -44,6 +49,25 @@ def _headers():
     return hs
 
 
+def _binding_command(obj: str):
+    """g++ over the binding's source, with the headers of the torch it will be used with."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    return ["g++", "-O2", "-std=c++17", "-fPIC", f"-I{root}/include",
+            f"-I{root}/include/torch/csrc/api/include", f"-I{cuda}/include",
+            f"-I{sysconfig.get_paths()['include']}",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-c", BINDING_SOURCE, "-o", obj]
+
+
+def _binding_link(obj: str, out: str):
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-shared", "-o", out, obj, f"-L{PKG}", "-l:libpagedattn.so", f"-L{lib}", "-lc10",
+            "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link; returns the library path.  Skips up-to-date objects."""
     os.makedirs(OUT_DIR, exist_ok=True)
@@ -64,6 +88,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(o)
         if force or _newer(o, [s] + headers):
             jobs.append(["g++", "-O2", "-std=c++17", "-fPIC", "-c", s, "-o", o])
+    binding_obj = os.path.join(OUT_DIR, "step_binding.cpp.o")
+    if force or _newer(binding_obj, [BINDING_SOURCE] + headers):
+        jobs.insert(0, _binding_command(binding_obj))          # the longest of them first
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -81,6 +108,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    if force or _newer(BINDING, [binding_obj]):
+        tmp = BINDING + f".tmp{os.getpid()}"
+        run(_binding_link(binding_obj, tmp))
+        os.replace(tmp, BINDING)
     return LIB
 
 

@@ -497,86 +497,34 @@ def pa_decode_fp8(out, q, k_cache, v_cache, block_tables, context_lens, scale, k
     return out
 
 
-# ------------------------------------------------------------- rotating appends
-def _rows(name, t, dtype, tokens, head_dim):
-    """Checks [tokens, heads, head_dim] rows whose heads and columns are contiguous;
-    returns (heads, token stride)."""
-    if not t.is_cuda or t.dim() != 3:
-        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, head_dim]")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    n, heads, d = t.shape
-    if n != tokens or d != head_dim:
-        raise ValueError(f"{name} must have {tokens} tokens of head_dim {head_dim}")
-    st, sh, sd = t.stride()
-    if (d > 1 and sd != 1) or (heads > 1 and sh != d):
-        raise ValueError(f"{name}: heads and columns must be contiguous")
-    return heads, (st if n > 1 else heads * d)
+# ------------------------------------------------------- per-step calls
+# A serving loop issues these every step on small tensors, so their arguments are checked
+# and passed on by the C++ binding (csrc/step_binding.cpp), which keeps a call at a few us.
+_step = None
 
 
-def _run_on(device, call, prepare):
-    """Issue the call with its tensors' device current (or hand it back)."""
+def _binding():
+    global _step
+    if _step is None:
+        library()
+        try:
+            from . import _step as module
+        except ImportError as e:
+            raise RuntimeError("the per-step binding has not been built for this interpreter: build it "
+                               "with `python -c \"import __graft_entry__ as g; g.build()\"`") from e
+        _step = module
+    return _step
+
+
+def _rope_append(name, kind, q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                 k_scale, v_scale, interleaved, device_errors, stream, prepare):
+    rc = (_step or _binding()).rope_append(
+        kind, q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, k_scale, v_scale,
+        interleaved, device_errors, stream, prepare)
     if prepare:
-        return call
-    import torch
-    if device.index == torch.cuda.current_device():
-        call()
-    else:
-        with torch.cuda.device(device):
-            call()
-
-
-def _same_device(device, tensors):
-    for name, t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the pools on {device}")
-
-
-def _rope_append(name, row_dtype, pool_args, last, q_out, q, k, v, k_cache, v_cache, slot_mapping,
-                 positions, cos_sin, interleaved, device_errors, stream, prepare):
-    import torch
-    NB, Hkv, bs, D = k_cache.shape
-    dev = k_cache.device
-    _need_cuda_contig("k_cache", k_cache)
-    _need_cuda_contig("v_cache", v_cache)
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache differ in shape or type")
-    T = k.shape[0]
-    hk, k_stride = _rows("k", k, row_dtype, T, D)
-    hv, v_stride = _rows("v", v, row_dtype, T, D)
-    if hk != Hkv or hv != Hkv:
-        raise ValueError("k and v must have the pools' kv heads")
-    Hq, q_stride, rot, most = 0, 0, 0, 0
-    if q is not None or q_out is not None:
-        if q is None or q_out is None:
-            raise ValueError("q and q_out go together")
-        Hq, q_stride = _rows("q", q, row_dtype, T, D)
-        if q_out.shape != q.shape or q_out.dtype != row_dtype or not q_out.is_contiguous():
-            raise ValueError("q_out must be contiguous, of q's shape and type")
-    ints = (("slot_mapping", slot_mapping), ("positions", positions))
-    if (positions is None) != (cos_sin is None):
-        raise ValueError("positions and cos_sin go together")
-    if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
-            raise TypeError("cos_sin must be float32 [max_position, rot_dim]")
-        _need_cuda_contig("cos_sin", cos_sin)
-        most, rot = cos_sin.shape
-    for n, t in ints:
-        if t is None:
-            continue
-        _need_cuda_contig(n, t)
-        if t.dtype != torch.int64:
-            raise TypeError(f"{n} must be int64")
-        if t.numel() != T:
-            raise ValueError(f"{n} must have an entry for each token")
-    _same_device(dev, (("q_out", q_out), ("q", q), ("k", k), ("v", v), ("v_cache", v_cache),
-                       ("cos_sin", cos_sin), ("device_errors", device_errors)) + ints)
-    call = PreparedCall(name, (
-        _ptr(q_out), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
-        _ptr(positions), _ptr(cos_sin), *pool_args, q_stride, k_stride, v_stride, T, Hq, Hkv, D,
-        rot, 1 if interleaved else 0, most, bs, NB, *last, _ptr(device_errors),
-        _stream(stream, dev)))
-    return _run_on(dev, call, prepare)
+        return PreparedCall(name, rc)
+    if rc:
+        _check(rc, name)
 
 
 def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin,
@@ -586,11 +534,8 @@ def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions,
     their type; slot_mapping, positions int64 [T]; cos_sin float32 [max_position, rot_dim]
     (cos of rot_dim / 2 angles, then their sin).  q and q_out may both be None, and
     positions and cos_sin too (no rotation)."""
-    if k_cache.dtype != k.dtype:
-        raise TypeError("the pools must have the type of k")
-    return _rope_append("pa_rope_and_cache", k.dtype, (), (_dtype_code(k),), q_out, q, k, v,
-                        k_cache, v_cache, slot_mapping, positions, cos_sin, interleaved,
-                        device_errors, stream, prepare)
+    return _rope_append("pa_rope_and_cache", 0, q_out, q, k, v, k_cache, v_cache, slot_mapping,
+                        positions, cos_sin, None, None, interleaved, device_errors, stream, prepare)
 
 
 def pa_rope_and_cache_fp8(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin,
@@ -598,23 +543,9 @@ def pa_rope_and_cache_fp8(q_out, q, k, v, k_cache, v_cache, slot_mapping, positi
                           prepare=False):
     """pa_rope_and_cache into e4m3 pools with a scale per kv head: k_scale, v_scale
     float32 [Hkv]; q, k, v bf16 (see pa.h)."""
-    import torch
-    _need_fp8_pool("k_cache", k_cache)
-    _need_fp8_pool("v_cache", v_cache)
-    _need_scales(k_scale, v_scale, k_cache.shape[1])
-    _same_device(k_cache.device, (("k_scale", k_scale), ("v_scale", v_scale)))
-    return _rope_append("pa_rope_and_cache_fp8", torch.bfloat16, (_ptr(k_scale), _ptr(v_scale)),
-                        (), q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin,
-                        interleaved, device_errors, stream, prepare)
-
-
-def _need_page_scales(k_cache, k_scales, v_scales):
-    import torch
-    for n, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        _need_cuda_contig(n, t)
-        if t.dtype != torch.float32 or t.shape != k_cache.shape[:2]:
-            raise TypeError(f"{n} must be float32 [num_blocks, num_kv_heads]")
-    _same_device(k_cache.device, (("k_scales", k_scales), ("v_scales", v_scales)))
+    return _rope_append("pa_rope_and_cache_fp8", 1, q_out, q, k, v, k_cache, v_cache, slot_mapping,
+                        positions, cos_sin, k_scale, v_scale, interleaved, device_errors, stream,
+                        prepare)
 
 
 def pa_rope_and_cache_fp8_block(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin,
@@ -622,14 +553,9 @@ def pa_rope_and_cache_fp8_block(q_out, q, k, v, k_cache, v_cache, slot_mapping, 
                                 stream=None, prepare=False):
     """pa_rope_and_cache into e4m3 pools with a scale for each page and head, which the
     call finds and updates: k_scales, v_scales float32 [NB, Hkv]; q, k, v bf16 (see pa.h)."""
-    import torch
-    _need_fp8_pool("k_cache", k_cache)
-    _need_fp8_pool("v_cache", v_cache)
-    _need_page_scales(k_cache, k_scales, v_scales)
-    return _rope_append("pa_rope_and_cache_fp8_block", torch.bfloat16,
-                        (_ptr(k_scales), _ptr(v_scales)), (), q_out, q, k, v, k_cache, v_cache,
-                        slot_mapping, positions, cos_sin, interleaved, device_errors, stream,
-                        prepare)
+    return _rope_append("pa_rope_and_cache_fp8_block", 2, q_out, q, k, v, k_cache, v_cache,
+                        slot_mapping, positions, cos_sin, k_scales, v_scales, interleaved,
+                        device_errors, stream, prepare)
 
 
 def pa_copy_scales(src_k_scales, src_v_scales, dst_k_scales, dst_v_scales, src_dst_pairs,
@@ -638,27 +564,30 @@ def pa_copy_scales(src_k_scales, src_v_scales, dst_k_scales, dst_v_scales, src_d
     (int64 [P, 2] on the device): after pa_copy_blocks (src and dst the same arrays) or
     pa_swap_blocks (either side device or pinned host memory); float32 [blocks, Hkv]."""
     import torch
-    heads = src_k_scales.shape[1]
+    _need_cuda_contig("src_dst_pairs", src_dst_pairs)
+    if src_dst_pairs.dtype != torch.int64 or src_dst_pairs.dim() != 2 or src_dst_pairs.shape[1] != 2:
+        raise TypeError("src_dst_pairs must be int64 [pairs, 2]")
+    dev = src_dst_pairs.device
     for n, t, like in (("src_k_scales", src_k_scales, src_k_scales),
                        ("src_v_scales", src_v_scales, src_k_scales),
                        ("dst_k_scales", dst_k_scales, dst_k_scales),
                        ("dst_v_scales", dst_v_scales, dst_k_scales)):
-        if not t.is_contiguous() or not (t.is_cuda or t.is_pinned()):
-            raise ValueError(f"{n} must be a contiguous CUDA tensor or pinned host tensor")
-        if t.dtype != torch.float32 or t.dim() != 2 or t.shape[1] != heads or t.shape != like.shape:
+        if not t.is_contiguous() or not (t.device == dev or t.is_pinned()):
+            raise ValueError(f"{n} must be contiguous, on the pairs' device or in pinned host memory")
+        if t.dtype != torch.float32 or t.dim() != 2 or t.shape[1] != src_k_scales.shape[1] \
+                or t.shape != like.shape:
             raise TypeError(f"{n} must be float32 [blocks, num_kv_heads]")
-    _need_cuda_contig("src_dst_pairs", src_dst_pairs)
-    if src_dst_pairs.dtype != torch.int64:
-        raise TypeError("src_dst_pairs must be int64")
-    dev = src_dst_pairs.device
-    _same_device(dev, [(n, t) for n, t in (
-        ("src_k_scales", src_k_scales), ("src_v_scales", src_v_scales),
-        ("dst_k_scales", dst_k_scales), ("dst_v_scales", dst_v_scales)) if t.is_cuda])
-    call = PreparedCall("pa_copy_scales", (
-        _ptr(src_k_scales), _ptr(src_v_scales), _ptr(dst_k_scales), _ptr(dst_v_scales),
-        _ptr(src_dst_pairs), int(src_dst_pairs.shape[0]), int(heads), int(src_k_scales.shape[0]),
-        int(dst_k_scales.shape[0]), _ptr(device_errors), _stream(stream, dev)))
-    return _run_on(dev, call, prepare)
+    if device_errors is not None and (device_errors.device != dev or device_errors.dtype != torch.int32):
+        raise ValueError("device_errors must be an int32 tensor on the pairs' device")
+    with torch.cuda.device(dev):
+        call = PreparedCall("pa_copy_scales", (
+            _ptr(src_k_scales), _ptr(src_v_scales), _ptr(dst_k_scales), _ptr(dst_v_scales),
+            _ptr(src_dst_pairs), src_dst_pairs.shape[0], src_k_scales.shape[1],
+            src_k_scales.shape[0], dst_k_scales.shape[0], _ptr(device_errors),
+            _stream(stream, dev)))
+        if prepare:
+            return call
+        call()
 
 
 # ------------------------------------------- windowed and page-scaled decode
@@ -671,48 +600,27 @@ def pa_decode_window_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_di
         int(max_context_len), int(window), int(sinks)))
 
 
-def _span_decode(name, scales, out, q, k_cache, v_cache, block_tables, context_lens, scale,
-                 num_kv_heads, max_context_len, window, sinks, workspace, device_errors, stream,
-                 prepare):
-    import torch
-    for n, t in (("out", out), ("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
-                 ("block_tables", block_tables), ("context_lens", context_lens)):
-        _need_cuda_contig(n, t)
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
-        raise TypeError("block_tables and context_lens must be int32")
-    if q.dim() == 3:
-        B, Hq, D = q.shape
-        q_len = 1
-    elif q.dim() == 4:
-        B, q_len, Hq, D = q.shape
-    else:
-        raise ValueError("q must be [B, Hq, D] or [B, q_len, Hq, D]")
-    NB, Hkv, bs, Dc = k_cache.shape
-    if Hkv != num_kv_heads:
-        raise ValueError("num_kv_heads does not match the cache shape")
-    if Dc != D or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("the pools differ in shape or type, or have another head_dim than q")
-    if out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out must have q's shape and type")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.numel() != B:
-        raise ValueError("block_tables and context_lens must have a row for each sequence")
-    dev = q.device
-    _same_device(dev, (("out", out), ("k_cache", k_cache), ("v_cache", v_cache),
-                       ("block_tables", block_tables), ("context_lens", context_lens),
-                       ("workspace", workspace), ("device_errors", device_errors)))
+def _span_decode(name, fp8, out, q, k_cache, v_cache, block_tables, context_lens, scale, k_scales,
+                 v_scales, num_kv_heads, max_context_len, window, sinks, workspace, device_errors,
+                 stream, prepare):
     if workspace is None:
-        with torch.cuda.device(dev):
-            nbytes = pa_decode_window_workspace_size(B, q_len * Hq, Hkv, D, bs, max_context_len,
-                                                     window, sinks)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-    head = (_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-            _ptr(context_lens), scale)
-    sizes = (Hkv, B, Hq, q_len, D, bs, NB, block_tables.shape[1], max_context_len, window, sinks)
-    kind = () if scales else (_dtype_code(q),)
-    call = PreparedCall(name, head + scales + sizes + kind + (
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(device_errors),
-        _stream(stream, dev)))
-    return call if prepare else (_run_on(dev, call, False), out)[1]
+        import torch
+        if not q.is_cuda:
+            raise ValueError("q must be a contiguous CUDA tensor")
+        rows = q.shape[-2] * (q.shape[1] if q.dim() == 4 else 1)
+        with torch.cuda.device(q.device):
+            nbytes = pa_decode_window_workspace_size(
+                q.shape[0], rows, num_kv_heads, q.shape[-1], k_cache.shape[2], max_context_len,
+                window, sinks)
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+    rc = (_step or _binding()).span_decode(
+        fp8, out, q, k_cache, v_cache, block_tables, context_lens, scale, k_scales, v_scales,
+        num_kv_heads, max_context_len, window, sinks, workspace, device_errors, stream, prepare)
+    if prepare:
+        return PreparedCall(name, rc)
+    if rc:
+        _check(rc, name)
+    return out
 
 
 def pa_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads,
@@ -723,11 +631,9 @@ def pa_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, scale
     caches [NB, Hkv, bs, D] of their type; block_tables int32 [B, max_blocks];
     context_lens int32 [B] (see pa.h).  ``workspace``: a uint8 CUDA tensor of at least
     pa_decode_window_workspace_size() bytes; allocated here when None."""
-    if k_cache.dtype != q.dtype:
-        raise TypeError("the pools must have the type of q")
-    return _span_decode("pa_decode_window", (), out, q, k_cache, v_cache, block_tables,
-                        context_lens, scale, num_kv_heads, max_context_len, window, sinks,
-                        workspace, device_errors, stream, prepare)
+    return _span_decode("pa_decode_window", False, out, q, k_cache, v_cache, block_tables,
+                        context_lens, scale, None, None, num_kv_heads, max_context_len, window,
+                        sinks, workspace, device_errors, stream, prepare)
 
 
 def pa_decode_fp8_block(out, q, k_cache, v_cache, block_tables, context_lens, scale, k_scales,
@@ -735,15 +641,9 @@ def pa_decode_fp8_block(out, q, k_cache, v_cache, block_tables, context_lens, sc
                         workspace=None, device_errors=None, stream=None, prepare=False):
     """pa_decode_window over e4m3 pools with a scale for each page and head: out, q bf16;
     caches one-byte [NB, Hkv, bs, 128]; k_scales, v_scales float32 [NB, Hkv] (see pa.h)."""
-    import torch
-    _need_fp8_pool("k_cache", k_cache)
-    _need_fp8_pool("v_cache", v_cache)
-    _need_page_scales(k_cache, k_scales, v_scales)
-    if q.dtype != torch.bfloat16:
-        raise TypeError("q and out must be bf16")
-    return _span_decode("pa_decode_fp8_block", (_ptr(k_scales), _ptr(v_scales)), out, q, k_cache,
-                        v_cache, block_tables, context_lens, scale, num_kv_heads,
-                        max_context_len, window, sinks, workspace, device_errors, stream, prepare)
+    return _span_decode("pa_decode_fp8_block", True, out, q, k_cache, v_cache, block_tables,
+                        context_lens, scale, k_scales, v_scales, num_kv_heads, max_context_len,
+                        window, sinks, workspace, device_errors, stream, prepare)
 
 
 def pa_debug_set_wait_limit(polls: int) -> None:
