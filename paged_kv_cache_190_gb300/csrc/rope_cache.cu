@@ -19,6 +19,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "pa_device.cuh"
@@ -27,7 +28,11 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+// Heads that a thread takes of one token, when there are rows enough to fill the GPU.
+// Two: the table row serves two rows, and at 40 registers enough threads are resident to
+// keep HBM busy (16384 tokens of 32 + 8 heads: 64.5 us; four heads at 72 registers 80.1).
+constexpr int kHeadsAtOnce = 2;
 
 // (No load here goes through the read-only path: the kernels start before the one ahead
 // of them in the stream has ended, and wait for its writes on the device.)
@@ -143,12 +148,21 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
 }
 
+// Division as a call: a scale that is no power of two is rare (one that the append did
+// not choose itself), and 16 divisions in line are most of a kernel's code.
+__device__ __noinline__ float divide(float x, float s) { return __fdiv_rn(x, s); }
+
 // Eight floats over s (IEEE division) as e4m3 codes.  A power of two divides by a
 // product with its reciprocal, which rounds to the same float.
 __device__ __forceinline__ uint2 e4m3x8(const float* x, float s, bool pow2, float inv) {
   float y[8];
+  if (pow2) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = pow2 ? x[e] * inv : __fdiv_rn(x[e], s);
+    for (int e = 0; e < 8; ++e) y[e] = x[e] * inv;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = divide(x[e], s);
+  }
   return make_uint2(e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16),
                     e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
 }
@@ -282,6 +296,8 @@ __global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const RopeArgs
 // re-encoded when it does.
 constexpr int kLanesPerRow = 8;                            // 128 bf16 columns: 2 chunks a lane
 constexpr int kRowsPerPass = 32 / kLanesPerRow;
+constexpr int kPageThreads = 256;                          // of a block of this kernel
+constexpr int kKeptRows = 16;                              // tokens that a block holds at a time
 
 __device__ __forceinline__ float page_scale(float amax) {
   const uint32_t u = __float_as_uint(amax);
@@ -289,6 +305,12 @@ __device__ __forceinline__ float page_scale(float amax) {
   int k = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
   k = max(k, -100);
   return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+}
+
+// A value's magnitude as ordered bits, 0 for infinities and NaN.
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
+  return u < 0x7f800000u ? u : 0u;
 }
 
 // Codes of a word at a new scale: value * ratio, nearest even.
@@ -304,67 +326,113 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
   return out;
 }
 
-template <bool INTER, int BS>
-__device__ __forceinline__ void append_run(const RopeArgs& a, int t0, int n, uint32_t offsets,
-                                           int64_t page, bool fresh, int h, bool is_v) {
-  constexpr int N = 8, D = 128;
-  constexpr int PASSES = BS / kRowsPerPass;
-  const int lane = threadIdx.x & 31;
-  const int l = lane % kLanesPerRow, row = lane / kLanesPerRow;
-  const uint16_t* src = static_cast<const uint16_t*>(is_v ? a.v : a.k) + static_cast<int64_t>(h) * D;
-  const int64_t stride = is_v ? a.v_stride : a.k_stride;
-  const LaneChunks<N, D, INTER> lc(l, is_v ? 0 : a.rot_dim);
-  const bool turned = !is_v && a.rot_dim > 0;
-  const float old = fresh ? 0.f : (is_v ? a.v_scales : a.k_scales)[page * a.num_kv_heads + h];
+// Tokens around a tile, as its block sees them: token t0 - 1 + i in entry i.
+constexpr int kTile = 16;
+constexpr int kSeenTokens = 1 + kTile + 32;                // one before, a run's length behind
+struct TileTokens {
+  int64_t page[kSeenTokens];                               // -1: not written
+  int64_t pos[kSeenTokens];
+  int off[kSeenTokens];
+  // the runs that start in the tile, in entry j that of token t0 + j: its length (0: no
+  // start); and the starts of the runs of one token and of those of more
+  int length[kTile], ones[kTile], more[kTile];
+  int num_ones, num_more;
+};
 
-  uint4 w[PASSES][2];
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int r = i * kRowsPerPass + row;
-    if (r < n) {
-      const uint4* p = reinterpret_cast<const uint4*>(src + (t0 + static_cast<int64_t>(r)) * stride);
-      w[i][0] = p[lc.c0];
-      w[i][1] = p[lc.c1];
-    }
-  }
-  uint32_t top = 0;                                        // largest magnitude's bits, finite ones only
-  // rotated values replace the raw ones as float32 only while they are coded: the
-  // first pass finds the magnitude, the second rotates again (cheaper than twice
-  // the registers)
-  auto values = [&](int i, float* x0, float* x1) {
-    Vec<uint16_t>::unpack(w[i][0], x0);
-    Vec<uint16_t>::unpack(w[i][1], x1);
+// A copy of 16 bytes to shared memory that nothing waits for until fetched().
+__device__ __forceinline__ void fetch16(void* smem, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// A run of several tokens: the block takes its rows of up to kHeadsPerItem heads, of K or
+// of V.  The rows and the tokens' table rows come into shared memory all at once, which is
+// what has to overlap; the warps go over them there twice, for the magnitude and for the
+// codes.  (Warp by warp straight from HBM, 4 rows in flight a warp, the same work took
+// 26 us for 8190 tokens of 8 heads; rows kept in registers in between, 25.)  Runs of more
+// than kKeptRows tokens come in pieces, the first of them again for its codes.
+constexpr int kHeadsPerItem = 8;
+constexpr int kWarps = kPageThreads / 32;
+constexpr int kRunBytes = kKeptRows * (kHeadsPerItem * 256 + 128 * 4);
+
+template <bool INTER, int BS>
+__device__ __forceinline__ void append_run(const RopeArgs& a, const TileTokens& seen, unsigned char* buf, float* tops,
+                                           int64_t t, int first, int n, uint32_t offsets, int64_t page, int h0,
+                                           bool is_v) {
+  constexpr int N = 8, D = 128;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int l = lane % kLanesPerRow, row = lane / kLanesPerRow;
+  const int heads = min(kHeadsPerItem, a.num_kv_heads - h0);
+  const int wph = kWarps / heads;                          // warps of a head
+  const int hh = warp / wph, sub = warp - hh * wph;
+  const bool active = hh < heads;
+  const bool fresh = offsets & 1u;
+  const bool turned = !is_v && a.rot_dim > 0;
+  const int64_t stride = is_v ? a.v_stride : a.k_stride;
+  const uint16_t* src = static_cast<const uint16_t*>(is_v ? a.v : a.k) + t * stride + static_cast<int64_t>(h0) * D;
+  float* table = reinterpret_cast<float*>(buf + kKeptRows * kHeadsPerItem * 256);
+  const int64_t head_page = page * a.num_kv_heads + h0 + hh;
+  float* scale = (is_v ? a.v_scales : a.k_scales) + head_page;
+  const LaneChunks<N, D, INTER> lc(l, is_v ? 0 : a.rot_dim);
+
+  auto fetch = [&](int r0, int m) {
+    const int cpr = heads * 16, tpr = a.rot_dim / 4;       // 16-byte chunks of a token
+    const int at = threadIdx.x % cpr;
+    if (threadIdx.x < kPageThreads / cpr * cpr)
+      for (int r = threadIdx.x / cpr; r < m; r += kPageThreads / cpr)
+        fetch16(buf + (r * cpr + at) * 16, src + (r0 + r) * stride + at * N);
+    if (turned)
+      for (int i = threadIdx.x; i < m * tpr; i += kPageThreads) {
+        const int r = i / tpr, c = i - r * tpr;
+        fetch16(table + r * a.rot_dim + c * 4, a.cos_sin + seen.pos[first + r0 + r] * a.rot_dim + c * 4);
+      }
+    fetched();
+    __syncthreads();
+  };
+  // this lane's two chunks of row r of the piece, rotated
+  auto values = [&](int r, float* x0, float* x1) {
+    const uint4* p = reinterpret_cast<const uint4*>(buf + (r * heads + hh) * 256);
+    Vec<uint16_t>::unpack(p[lc.c0], x0);
+    Vec<uint16_t>::unpack(p[lc.c1], x1);
     if (turned) {
-      const int r = min(i * kRowsPerPass + row, n - 1);
       Angles<N, D, INTER> an;
-      an.load(a.cos_sin + a.positions[t0 + r] * a.rot_dim, a.rot_dim / 2, lc);
+      an.load(table + r * a.rot_dim, a.rot_dim / 2, lc);
       rotate<N, D, INTER>(x0, x1, lc, an);
     }
   };
+
+  const float old = fresh || !active ? 0.f : *scale;
+  const int last = (n - 1) / kKeptRows * kKeptRows;
+  float top = 0.f;
+  for (int r0 = 0; r0 < n; r0 += kKeptRows) {
+    if (r0 > 0) __syncthreads();
+    const int m = min(n - r0, kKeptRows);
+    fetch(r0, m);
+    if (active)
+#pragma unroll 2
+      for (int r = sub * kRowsPerPass + row; r < m; r += wph * kRowsPerPass) {
+        float x0[N], x1[N];
+        values(r, x0, x1);
 #pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    if (i * kRowsPerPass + row < n) {
-      float x0[N], x1[N];
-      values(i, x0, x1);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const uint32_t u0 = __float_as_uint(x0[e]) & 0x7fffffffu, u1 = __float_as_uint(x1[e]) & 0x7fffffffu;
-        top = max(top, u0 < 0x7f800000u ? u0 : 0u);
-        top = max(top, u1 < 0x7f800000u ? u1 : 0u);
+        for (int e = 0; e < N; ++e) {                      // infinities and NaN do not count
+          const float y0 = fabsf(x0[e]), y1 = fabsf(x1[e]);
+          top = fmaxf(top, fmaxf(y0 < INFINITY ? y0 : 0.f, y1 < INFINITY ? y1 : 0.f));
+        }
       }
-    }
   }
-  top = __reduce_max_sync(0xffffffffu, top);
-  const float need = page_scale(__uint_as_float(top));
-  const float s = fmaxf(old, need);
-  unsigned char* base = static_cast<unsigned char*>(is_v ? a.v_cache : a.k_cache) +
-                        (page * a.num_kv_heads + h) * BS * static_cast<int64_t>(D);
-  if (!fresh && s > old) {
+  top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+  if (wph > 1) {
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+    for (int w = 0; w < wph; ++w) top = fmaxf(top, active ? tops[hh * wph + w] : 0.f);
+  }
+  const float s = fmaxf(old, page_scale(top));
+  unsigned char* base = static_cast<unsigned char*>(is_v ? a.v_cache : a.k_cache) + head_page * BS * D;
+  if (active && !fresh && s > old) {
     // what the page holds, rows of this run aside: 16-byte chunk c of row r
     const float ratio = __fdiv_rn(old, s);
-#pragma unroll
-    for (int i = 0; i < BS * D / 16 / 32; ++i) {
-      const int idx = i * 32 + lane;
+#pragma unroll 2
+    for (int idx = sub * 32 + lane; idx < BS * D / 16; idx += wph * 32) {
       if (!((offsets >> (idx / 8)) & 1u)) {
         uint4* p = reinterpret_cast<uint4*>(base) + idx;
         const uint4 c = *p;
@@ -374,80 +442,177 @@ __device__ __forceinline__ void append_run(const RopeArgs& a, int t0, int n, uin
   }
   const bool pow2 = is_pow2(s);
   const float inv = pow2 ? pow2_reciprocal(s) : 0.f;
+  for (int r0 = last; r0 >= 0; r0 -= kKeptRows) {
+    const int m = min(n - r0, kKeptRows);
+    if (r0 != last) {
+      __syncthreads();
+      fetch(r0, m);
+    }
+    if (active)
+#pragma unroll 2
+      for (int r = sub * kRowsPerPass + row; r < m; r += wph * kRowsPerPass) {
+        float x0[N], x1[N];
+        values(r, x0, x1);
+        uint2* dst = reinterpret_cast<uint2*>(base + seen.off[first + r0 + r] * D);
+        dst[lc.c0] = e4m3x8(x0, s, pow2, inv);
+        dst[lc.c1] = e4m3x8(x1, s, pow2, inv);
+      }
+  }
+  if (active && sub == 0 && lane == 0) *scale = s;
+  __syncthreads();                                         // the buffer is free
+}
+
+// A run of one token, which is what a decode step's are: lanes 0-15 take the head's K
+// row, lanes 16-31 its V row, a 16-byte chunk each, and get the chunk that theirs rotates
+// with from its lane.  
+template <bool INTER, int BS>
+__device__ __forceinline__ void append_one(const RopeArgs& a, int64_t t, int64_t pos, int off, int64_t page, int h) {
+  constexpr int N = 8, D = 128;
+  const int lane = threadIdx.x & 31, c = lane & 15;
+  const bool is_v = lane >= 16;
+  const bool fresh = off == 0;
+  const uint16_t* src = static_cast<const uint16_t*>(is_v ? a.v : a.k) + t * (is_v ? a.v_stride : a.k_stride) +
+                        static_cast<int64_t>(h) * D;
+  const uint4 w = reinterpret_cast<const uint4*>(src)[c];
+  float* scale = (is_v ? a.v_scales : a.k_scales) + page * a.num_kv_heads + h;
+  const float old = fresh ? 0.f : *scale;
+  float x[N];
+  Vec<uint16_t>::unpack(w, x);
+  if (a.rot_dim > 0) {
+    const bool on = !is_v && c * N < a.rot_dim;
+    const float* row = a.cos_sin + pos * a.rot_dim;
+    const int half = a.rot_dim / 2;
+    if constexpr (INTER) {
+      if (on) {
 #pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int r = i * kRowsPerPass + row;
-    if (r < n) {
-      float x0[N], x1[N];
-      values(i, x0, x1);
-      const int off = static_cast<int>(a.slots[t0 + r] - page * BS);
-      uint2* dst = reinterpret_cast<uint2*>(base + off * D);
-      dst[lc.c0] = e4m3x8(x0, s, pow2, inv);
-      dst[lc.c1] = e4m3x8(x1, s, pow2, inv);
+        for (int e = 0; e < N / 2; ++e) turn(x[2 * e], x[2 * e + 1], row[c * 4 + e], row[half + c * 4 + e]);
+      }
+    } else {
+      const int hc = half / N;                             // chunks of a half
+      const bool second = c >= hc;
+      const int from = on ? (second ? lane - hc : lane + hc) : lane;
+      uint4 o;
+      o.x = __shfl_sync(0xffffffffu, w.x, from);
+      o.y = __shfl_sync(0xffffffffu, w.y, from);
+      o.z = __shfl_sync(0xffffffffu, w.z, from);
+      o.w = __shfl_sync(0xffffffffu, w.w, from);
+      if (on) {
+        float y[N];
+        Vec<uint16_t>::unpack(o, y);
+        const float* cs = row + (second ? c - hc : c) * N;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float xc = __fmul_rn(x[e], cs[e]), ys = __fmul_rn(y[e], cs[half + e]);
+          x[e] = second ? __fadd_rn(xc, ys) : __fsub_rn(xc, ys);
+        }
+      }
     }
   }
-  if (lane == 0) (is_v ? a.v_scales : a.k_scales)[page * a.num_kv_heads + h] = s;
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < N; ++e) top = max(top, finite_bits(x[e]));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float s = fmaxf(old, page_scale(__uint_as_float(top)));
+  unsigned char* base = static_cast<unsigned char*>(is_v ? a.v_cache : a.k_cache) +
+                        (page * a.num_kv_heads + h) * BS * static_cast<int64_t>(D);
+  if (!fresh && s > old) {
+    const float ratio = __fdiv_rn(old, s);
+#pragma unroll 4
+    for (int idx = c; idx < BS * D / 16; idx += 16)        // 16-byte chunks, 8 a row
+      if (idx / 8 != off) {
+        uint4* p = reinterpret_cast<uint4*>(base) + idx;
+        const uint4 q = *p;
+        *p = make_uint4(rescale4(q.x, ratio), rescale4(q.y, ratio), rescale4(q.z, ratio), rescale4(q.w, ratio));
+      }
+  }
+  const bool pow2 = is_pow2(s);
+  reinterpret_cast<uint2*>(base + off * D)[c] = e4m3x8(x, s, pow2, pow2 ? pow2_reciprocal(s) : 0.f);
+  if (c == 0) *scale = s;
 }
 
-// Page of token t >= 0, or -1 where the token is not written.
-__device__ __forceinline__ int64_t page_of(const RopeArgs& a, int t, bool speak) {
-  if (t >= a.num_tokens) return -1;
-  const Place p = place(a, t, speak);
-  return p.write ? p.slot / a.block_size : -1;
-}
-
-// Blocks 0 .. kv_blocks - 1 take TILE tokens each: every run that starts among them,
-// one warp for each (run, head, K or V).  The blocks behind rotate q.
+// A block of a tile: the runs that start among the tile's kTile tokens, a warp for each
+// (token, head) of the runs of one token and the block for each (run, 8 heads, K or V) of
+// the longer ones; the tile's `parts` blocks share these out.  Every block looks its
+// tokens up once, into shared memory.  The blocks behind rotate q.
 template <bool INTER, int BS>
-__global__ void __launch_bounds__(kThreads) rope_and_cache_page_scale_kernel(
-    const RopeArgs a, int tile, int kv_blocks, int warps_per_tile, int64_t q_groups, int uq) {
+__global__ void __launch_bounds__(kPageThreads, 4) rope_and_cache_page_scale_kernel(
+    const RopeArgs a, int parts, int64_t kv_blocks, int64_t q_groups, int uq) {
+  __shared__ TileTokens seen;
+  __shared__ float tops[kWarps];
+  extern __shared__ __align__(16) unsigned char run_buf[];
   wait_prior_grids();
   allow_next_grid();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  if (static_cast<int>(blockIdx.x) >= kv_blocks) {
-    constexpr int HPT = 4;
-    const int64_t g = static_cast<int64_t>(blockIdx.x - kv_blocks) * (kThreads / kLanesPerRow) +
-                      threadIdx.x / kLanesPerRow;
+  const int64_t kv = blockIdx.x;
+  if (kv >= kv_blocks) {
+    const int64_t g = (kv - kv_blocks) * (kPageThreads / kLanesPerRow) + threadIdx.x / kLanesPerRow;
     if (g >= q_groups) return;
     const int t = static_cast<int>(g / uq);
-    rows_of_token<uint16_t, 128, INTER, false, HPT>(a, t, kQ, static_cast<int>(g - static_cast<int64_t>(t) * uq) * HPT,
-                                                    threadIdx.x % kLanesPerRow);
+    rows_of_token<uint16_t, 128, INTER, false, kHeadsAtOnce>(
+        a, t, kQ, static_cast<int>(g - static_cast<int64_t>(t) * uq) * kHeadsAtOnce, threadIdx.x % kLanesPerRow);
     return;
   }
-  const int64_t gw = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp;
-  const int first = static_cast<int>(gw / warps_per_tile) * tile;
-  const int mine = static_cast<int>(gw % warps_per_tile);
-  if (first >= a.num_tokens) return;
-  // starts among the tile's tokens: the page differs from the token's before
-  const int t = first + lane;
-  const bool in = lane < tile && t < a.num_tokens;
-  const int64_t page = in ? page_of(a, t, mine == 0) : -1;
-  const bool start = in && page >= 0 && (t == 0 || page_of(a, t - 1, false) != page);
-  uint32_t starts = __ballot_sync(0xffffffffu, start);
-  const int items = 2 * a.num_kv_heads;
-  int k = mine;                                            // item of the tile: start-major
-  while (starts) {
-    const int s = first + __ffs(starts) - 1;
-    starts &= starts - 1;
-    if (k >= items) {
-      k -= items;
-      continue;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int tile = static_cast<int>(kv / parts), part = static_cast<int>(kv - static_cast<int64_t>(tile) * parts);
+  const int t0 = tile * kTile;
+  if (threadIdx.x < 64) {
+    const int i = threadIdx.x;
+    const int64_t t = static_cast<int64_t>(t0) - 1 + i;
+    int64_t page = -1, pos = 0;
+    int off = 0;
+    if (t >= 0 && t < a.num_tokens && i < kSeenTokens) {
+      const Place p = place(a, static_cast<int>(t), part == 0 && i > 0 && i <= kTile);
+      if (p.write) {
+        page = p.slot / BS;
+        off = static_cast<int>(p.slot - page * BS);
+        pos = p.pos;
+      }
     }
-    // the run: up to BS tokens from s on in one page
-    const int64_t pg = __shfl_sync(0xffffffffu, page, s - first);
-    const int tt = s + lane;
-    const bool in_run = tt < a.num_tokens && page_of(a, tt, false) == pg;
-    const uint32_t same = __ballot_sync(0xffffffffu, in_run);
-    int n = same == 0xffffffffu ? 32 : __ffs(~same) - 1;
-    if (n > BS || (n == BS && page_of(a, s + BS, false) == pg)) {
-      n = BS;                                              // more tokens than slots: refused
-      if (lane == 0) report(a.device_errors, PA_DEVERR_BAD_SLOT);
+    if (i < kSeenTokens) {
+      seen.page[i] = page;
+      seen.off[i] = off;
+      seen.pos[i] = pos;
     }
-    const uint32_t bit = lane < n ? 1u << static_cast<uint32_t>(a.slots[tt] - pg * BS) : 0u;
-    const uint32_t offsets = __reduce_or_sync(0xffffffffu, bit);
-    for (; k < items; k += warps_per_tile)
-      append_run<INTER, BS>(a, s, n, offsets, pg, offsets & 1u, k >> 1, k & 1);
-    k -= items;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // bit i: entry i goes on with the page of entry i - 1
+    auto goes_on = [&](int i) {
+      return i > 0 && i < kSeenTokens && seen.page[i] >= 0 && seen.page[i] == seen.page[i - 1];
+    };
+    const uint32_t low = __ballot_sync(0xffffffffu, goes_on(lane)), high = __ballot_sync(0xffffffffu, goes_on(32 + lane));
+    const uint64_t on = (static_cast<uint64_t>(high) << 32) | low;
+    const int i = lane + 1;
+    int n = 0;
+    if (lane < kTile && seen.page[i] >= 0 && !((on >> i) & 1u)) {
+      n = __ffsll(static_cast<long long>(~(on >> (i + 1))));
+      if (n > BS) {
+        n = BS;                                            // more tokens than slots: refused
+        report(a.device_errors, PA_DEVERR_BAD_SLOT);
+      }
+    }
+    const uint32_t ones = __ballot_sync(0xffffffffu, n == 1), more = __ballot_sync(0xffffffffu, n > 1);
+    const uint32_t before = (1u << lane) - 1;
+    if (lane < kTile) seen.length[lane] = n;
+    if (n == 1) seen.ones[__popc(ones & before)] = lane;
+    if (n > 1) seen.more[__popc(more & before)] = lane;
+    if (lane == 0) {
+      seen.num_ones = __popc(ones);
+      seen.num_more = __popc(more);
+    }
+  }
+  __syncthreads();
+  for (int k = part * kWarps + warp; k < seen.num_ones * a.num_kv_heads; k += parts * kWarps) {
+    const int j = k / a.num_kv_heads, at = seen.ones[j];
+    append_one<INTER, BS>(a, static_cast<int64_t>(t0) + at, seen.pos[at + 1], seen.off[at + 1], seen.page[at + 1],
+                          k - j * a.num_kv_heads);
+  }
+  const int groups = (a.num_kv_heads + kHeadsPerItem - 1) / kHeadsPerItem;
+  for (int k = part; k < seen.num_more * groups * 2; k += parts) {
+    const int j = k / (2 * groups), m = k - j * 2 * groups, at = seen.more[j], n = seen.length[at];
+    const uint32_t offsets = __reduce_or_sync(0xffffffffu, lane < n ? 1u << seen.off[at + 1 + lane] : 0u);
+    append_run<INTER, BS>(a, seen, run_buf, tops, static_cast<int64_t>(t0) + at, at + 1, n, offsets, seen.page[at + 1],
+                          (m >> 1) * kHeadsPerItem, m & 1);
   }
 }
 
@@ -469,11 +634,12 @@ __global__ void __launch_bounds__(kThreads) copy_scales_kernel(
 }
 
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), int64_t blocks, cudaStream_t stream, A... args) {
+cudaError_t launch(void (*kernel)(P...), int64_t blocks, int threads, int smem, cudaStream_t stream, A... args) {
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -491,13 +657,14 @@ cudaError_t run_rope(const RopeArgs& a, cudaStream_t stream) {
   auto go = [&](auto kernel, int hpt) {
     const int uq = ceil_div(a.num_q_heads, hpt), uk = ceil_div(a.num_kv_heads, hpt);
     const int64_t groups = static_cast<int64_t>(a.num_tokens) * (uq + 2 * uk);
-    return launch(kernel, (groups + per_block - 1) / per_block, stream, a, groups, uq, uk);
+    return launch(kernel, (groups + per_block - 1) / per_block, kThreads, 0, stream, a, groups, uq, uk);
   };
-  // one head a thread while the rows are too few to fill the GPU, four from there on
+  // one head a thread while the rows are too few to fill the GPU
   const bool few = static_cast<int64_t>(a.num_tokens) * (a.num_q_heads + 2 * a.num_kv_heads) < 8192;
+  constexpr int H = kHeadsAtOnce;
   if (a.interleaved)
-    return few ? go(rope_and_cache_kernel<E, D, true, FP8, 1>, 1) : go(rope_and_cache_kernel<E, D, true, FP8, 4>, 4);
-  return few ? go(rope_and_cache_kernel<E, D, false, FP8, 1>, 1) : go(rope_and_cache_kernel<E, D, false, FP8, 4>, 4);
+    return few ? go(rope_and_cache_kernel<E, D, true, FP8, 1>, 1) : go(rope_and_cache_kernel<E, D, true, FP8, H>, H);
+  return few ? go(rope_and_cache_kernel<E, D, false, FP8, 1>, 1) : go(rope_and_cache_kernel<E, D, false, FP8, H>, H);
 }
 
 }  // namespace
@@ -509,20 +676,20 @@ cudaError_t launch_rope_and_cache(const RopeArgs& a, cudaStream_t stream) {
     return a.head_dim == 128 ? run_rope<uint16_t, 128, false>(a, stream) : run_rope<uint16_t, 64, false>(a, stream);
   if (a.pool == RopePool::kF32)
     return a.head_dim == 128 ? run_rope<float, 128, false>(a, stream) : run_rope<float, 64, false>(a, stream);
-  // a scale for each page and head.  Few tokens (decode steps: a run each): a tile of
-  // one token, so that every (run, head, K or V) has its warp at once; many: a tile of
-  // a page's tokens, which spares the blocks that would find no run of their own.
-  const int tile = a.num_tokens <= 1024 ? 1 : a.block_size;
-  const int warps_per_tile = 2 * a.num_kv_heads;
-  const int64_t kv_warps = static_cast<int64_t>((a.num_tokens + tile - 1) / tile) * warps_per_tile;
-  const int64_t kv_blocks = (kv_warps + kThreads / 32 - 1) / (kThreads / 32);
-  const int uq = ceil_div(a.num_q_heads, 4);
+  // a scale for each page and head.  A tile has a run for each of its tokens (a decode
+  // step) or one or two in all (a prompt): as many blocks a tile as give every token and
+  // head of a decode step a warp at once, while the tiles are few; two (K and V) from
+  // there on
+  const int64_t tiles = (a.num_tokens + kTile - 1) / kTile;
+  const int most = (kTile * a.num_kv_heads + kWarps - 1) / kWarps;
+  const int parts = static_cast<int>(std::max<int64_t>(2, std::min<int64_t>(most, 512 / tiles)));
+  const int64_t kv_blocks = tiles * parts;
+  const int uq = ceil_div(a.num_q_heads, kHeadsAtOnce);
   const int64_t q_groups = static_cast<int64_t>(a.num_tokens) * uq;
-  const int64_t q_blocks = (q_groups + kThreads / kLanesPerRow - 1) / (kThreads / kLanesPerRow);
+  const int64_t q_blocks = (q_groups + kPageThreads / kLanesPerRow - 1) / (kPageThreads / kLanesPerRow);
   if (kv_blocks > 0x3fffffff) return cudaErrorInvalidConfiguration;
   auto go = [&](auto kernel) {
-    return launch(kernel, kv_blocks + q_blocks, stream, a, tile, static_cast<int>(kv_blocks), warps_per_tile,
-                  q_groups, uq);
+    return launch(kernel, kv_blocks + q_blocks, kPageThreads, kRunBytes, stream, a, parts, kv_blocks, q_groups, uq);
   };
   if (a.interleaved)
     return a.block_size == 16 ? go(rope_and_cache_page_scale_kernel<true, 16>)
