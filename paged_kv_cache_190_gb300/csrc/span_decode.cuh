@@ -23,7 +23,8 @@
 //   * Two ways to spread (sequence, head group) segments over the GPU.  Shares: one
 //     CTA per SM, every CTA takes an equal run of all segments' stages, found by each
 //     CTA itself from the lengths (no plan kernel, no counters to reset); a segment
-//     that a share's end cuts leaves partials, which a second kernel joins.
+//     that a share's end cuts leaves partials, which a second kernel joins (it finds the
+//     cuts from the lengths too, while this one still runs).
 //     Clusters, for small calls: a segment's stages go to the CTAs of one cluster,
 //     which join their states through distributed shared memory: one launch, no
 //     scratch, half the latency.
@@ -42,34 +43,10 @@
 #include <type_traits>
 
 #include "paged_decode.cuh"
-#include "span_decode.h"
+#include "span_list.cuh"
 
 namespace pa {
 namespace span {
-
-// The blocks that a sequence of `len` tokens has to read.
-struct Span {
-  int len, lo;        // lo: first token that the window of the first new token reaches
-  int nblk;           // blocks in the list
-  int ns, shift;      // list index v is block v + (v >= ns ? shift : 0)
-  int nst;            // stages (at least one, so that empty sequences get their zero rows)
-};
-
-template <int TU>
-__device__ __forceinline__ Span make_span(const SpanParams& p, int raw_len) {
-  Span s;
-  s.len = min(max(raw_len, 0), p.max_len);
-  s.lo = max(0, s.len - p.q_len + 1 - p.window);
-  const int nb = (s.len + TU - 1) / TU;
-  const int wb = s.lo / TU;
-  s.ns = (min(p.sinks, s.len) + TU - 1) / TU;
-  s.shift = wb - s.ns;
-  if (s.shift <= 0) s.ns = s.shift = 0;
-  s.nblk = nb - s.shift;
-  const int wph_log2 = 3 - p.hg_log2;
-  s.nst = max(1, (s.nblk + (1 << wph_log2) - 1) >> wph_log2);
-  return s;
-}
 
 // (Nothing here goes through the read-only path: a kernel ahead in the stream may still
 // be writing lengths, tables or q when this one is already resident.)
@@ -81,13 +58,14 @@ struct Walk {
   const SpanParams& p;
   int b, grp, base, lens;
   Span sp;
-  __device__ __forceinline__ Walk(const SpanParams& p_, int b_, int grp_) : p(p_), b(b_), grp(grp_), base(b_) {
+  // len: sequence b_'s (known by then; the lanes' lengths are not waited for)
+  __device__ __forceinline__ Walk(const SpanParams& p_, int b_, int grp_, int len) : p(p_), b(b_), grp(grp_), base(b_) {
     load();
+    sp = make_span<TU>(p, len);
   }
   __device__ __forceinline__ void load() {
     const int lane = threadIdx.x & 31;
     lens = base + lane < p.num_seqs ? p.lens[base + lane] : 0;
-    sp = make_span<TU>(p, __shfl_sync(kFull, lens, 0));
   }
   __device__ __forceinline__ void next() {
     if (++grp < p.ngroups) return;
@@ -96,9 +74,8 @@ struct Walk {
     if (b - base == 32) {
       base = b;
       load();
-    } else {
-      sp = make_span<TU>(p, __shfl_sync(kFull, lens, b - base));
     }
+    sp = make_span<TU>(p, __shfl_sync(kFull, lens, b - base));
   }
 };
 
@@ -114,6 +91,10 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
       : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 __device__ __forceinline__ void consumer_barrier() {
@@ -132,27 +113,19 @@ __device__ __forceinline__ bool consumer_barrier_any(bool yes) {
       : "memory");
   return any != 0;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // Shared address of CTA `rank` of the cluster for a local shared address.
 __device__ __forceinline__ uint32_t peer_addr(uint32_t local, int rank) {
   uint32_t a;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
   return a;
 }
-__device__ __forceinline__ float2 peer_f2(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void peer_store(uint32_t a, float x, float y) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
 }
-__device__ __forceinline__ float4 peer_f4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
+__device__ __forceinline__ void peer_store(uint32_t a, float x, float y, float z, float w) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
 
 // Which tokens of a tile (first token t0) a query row sees.
@@ -166,7 +139,8 @@ struct Sight {
 };
 
 // ------------------------------------------------------------------ one warp's state
-// begin: reset, load q's rows of the head;  unit: fold a tile in (release() once its
+// load: q's rows of a head on their way (before the last head's state is stored: it does
+// not need q any more);  begin: reset, q ready;  unit: fold a tile in (release() once its
 // bytes are read);  store: hand the state over as (m, l) and the unnormalised sums.
 
 __device__ __forceinline__ int64_t query_row(const SpanParams& p, int b, int head, int r) {
@@ -192,7 +166,7 @@ struct Bf16Rows {
   }
   __device__ __forceinline__ int row() const { return lane >> 2; }
 
-  __device__ __forceinline__ void begin(const SpanParams& p, int b, int head) {
+  __device__ __forceinline__ void load(const SpanParams& p, int b, int head) {
     const int g = lane >> 2, c = lane & 3;
     const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + query_row(p, b, head, g < rows ? g : 0) * (2 * D));
 #pragma unroll
@@ -200,6 +174,8 @@ struct Bf16Rows {
       qa[ks][0] = g < rows ? src[8 * ks + c] : 0u;
       qa[ks][1] = g < rows ? src[8 * ks + 4 + c] : 0u;
     }
+  }
+  __device__ __forceinline__ void begin(const SpanParams&) {
     m = kNoScore;
     l = 0.f;
 #pragma unroll
@@ -211,14 +187,13 @@ struct Bf16Rows {
   __device__ __forceinline__ void unit(uint32_t kb, uint32_t vb, int slab, int, const Sight& see,
                                        float scale_log2, const float2*, int, Release release) {
     const int mi = lane >> 3, r8 = lane & 7, c = lane & 3;
-    const int frow = (mi >> 1) * 8 + r8;
+    // chunk 2 i + (mi & 1) of this lane's row: an XOR with a constant within a slab
+    const uint32_t row0 = ((mi >> 1) * 8 + r8) * 128 + (((mi & 1) ^ r8) << 4);
+    auto at = [&](uint32_t base, int i) { return (base + row0 + (i >> 2) * slab) ^ ((i & 3) << 5); };
     uint32_t kf[KS][4];
-    auto at = [&](int chunk) {
-      return static_cast<uint32_t>((chunk >> 3) * slab + frow * 128 + (((chunk & 7) ^ r8) << 4));
-    };
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
-      ldsm_x4(kb + at(2 * ks + (mi & 1)), kf[ks][0], kf[ks][1], kf[ks][2], kf[ks][3]);
+      ldsm_x4(at(kb, ks), kf[ks][0], kf[ks][1], kf[ks][2], kf[ks][3]);
     float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -255,7 +230,7 @@ struct Bf16Rows {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       uint32_t vf[4];
-      ldsm_x4_trans(vb + at(2 * mt + (mi & 1)), vf[0], vf[1], vf[2], vf[3]);
+      ldsm_x4_trans(at(vb, mt), vf[0], vf[1], vf[2], vf[3]);
       mma_bf16_full(o[mt], vf[0], vf[1], vf[2], vf[3], pb0, pb1);
     }
     release();
@@ -285,22 +260,50 @@ struct Bf16Rows {
   }
 };
 
-// e4m3 codes with a scale for each page and head, mma.sync m16n8k32 on the codes as
-// they are (Fp8TensorConsumer has the operand layouts).  q's row, scaled by a power of
-// two into [128, 256), goes in as two e4m3 parts: a bf16 element has 8 significant bits
-// and a part holds 4, so hi + lo is exact down to 2^-10 of the row's largest element.
-//
-// V's scale differs from page to page, so it goes into the weights, w_t = e^{s_t} vs_t,
-// which are what is split into two parts (within 2^-8 of each weight).  They keep a
-// running maximum of their own, mo = max(s_t + log2 vs_t): a page of tiny V rows with
-// high probability (a first token's, say) would otherwise push the other pages' weights
-// below the codes' range, or vanish from the sum.  l sums e^{s_t} under m = max s_t.
-template <int G>
+// (Not volatile: products of registers, free to move between the loads around them.)
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four e4m3 codes as two pairs of halves, exactly.
+__device__ __forceinline__ void halves_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// e4m3 codes with a scale for each page and head: codes become halves (exactly, two a
+// conversion) on the way into mma.sync m16n8k16.  The e4m3 form of the instruction does
+// the same conversions inside, of both operands and at every use, and wants q and the
+// weights as sums of two e4m3 parts: 650 instructions a tile against 440 here (256
+// sequences, 885 MB: 161.8 -> 150.4 us).
+//   * q: the row scaled by a power of two into [128, 256); a bf16 element is exact as a
+//     half down to 2^-22 of its row's largest.
+//   * The codes of a K row that ldmatrix gives a lane are columns 4 c .. 4 c + 3 of a
+//     chunk: they become k = 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of a step, for q alike.
+//   * V through ldmatrix.trans on code pairs: columns 2 g and 2 g + 1 of tokens 2 c and
+//     2 c + 1 of an 8-token block; the columns become rows g and g + 8 of O^T.
+//   * V's scale differs from page to page, so it goes into the weights,
+//     w_t = e^{s_t} vs_t, which are rounded to halves (2^-11 of each).  They keep a running
+//     maximum of their own, mo = max(s_t + log2 vs_t): a page of tiny V rows with high
+//     probability (a first token's, say) would otherwise push the other pages' weights
+//     below a half's range.  l sums e^{s_t} under m = max s_t.
 struct Fp8Rows {
-  static constexpr int D = 128, KS = 4, MT = 8, NT = 4, TU = 32;
-  static constexpr float kPScale = 256.f;
-  static constexpr bool kPack = G <= 4;      // columns 4..7 of the PV product free for the lo parts
-  uint32_t qh[KS][2], ql[KS][2];
+  static constexpr int D = 128, KS = 8, MT = 8, NT = 4, TU = 32;
+  static constexpr float kPLog2 = 10.f;      // weights are carried times 2^10
+  uint32_t qa[KS][2];
   float o[MT][4];
   float m, l, mo, qinv;
   int lane, rows;
@@ -311,21 +314,24 @@ struct Fp8Rows {
   }
   __device__ __forceinline__ int row() const { return lane >> 2; }
 
-  __device__ __forceinline__ void begin(const SpanParams& p, int b, int head) {
+  __device__ __forceinline__ void load(const SpanParams& p, int b, int head) {
     const int g = lane >> 2, c = lane & 3;
     const bool on = g < rows;
     const uint2* src = reinterpret_cast<const uint2*>(p.q + query_row(p, b, head, on ? g : 0) * (2 * D));
-    uint2 w[KS][2];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const uint2 w = on ? src[4 * ks + c] : make_uint2(0u, 0u);      // columns 16 ks + 4 c .. + 3
+      qa[ks][0] = w.x;
+      qa[ks][1] = w.y;
+    }
+  }
+  __device__ __forceinline__ void begin(const SpanParams&) {
     float amax = 0.f;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        // columns 32 ks + 16 k + 4 c .. + 3
-        w[ks][k] = on ? src[8 * ks + 4 * k + c] : make_uint2(0u, 0u);
-        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(bf16_lo(w[ks][k].x)), fabsf(bf16_hi(w[ks][k].x))),
-                                 fmaxf(fabsf(bf16_lo(w[ks][k].y)), fabsf(bf16_hi(w[ks][k].y)))));
-      }
+      for (int k = 0; k < 2; ++k)
+        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(qa[ks][k])), fabsf(bf16_hi(qa[ks][k]))));
     amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
     const int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu);
@@ -335,23 +341,7 @@ struct Fp8Rows {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float x[4] = {bf16_lo(w[ks][k].x) * up, bf16_hi(w[ks][k].x) * up, bf16_lo(w[ks][k].y) * up,
-                            bf16_hi(w[ks][k].y) * up};
-        uint32_t hi = 0, lo = 0;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const __nv_fp8x2_storage_t h =
-              __nv_cvt_float2_to_fp8x2(make_float2(x[2 * j], x[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
-          const float2 back = __half22float2(static_cast<__half2>(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-          const __nv_fp8x2_storage_t r = __nv_cvt_float2_to_fp8x2(
-              make_float2(x[2 * j] - back.x, x[2 * j + 1] - back.y), __NV_SATFINITE, __NV_E4M3);
-          hi |= static_cast<uint32_t>(h) << (16 * j);
-          lo |= static_cast<uint32_t>(r) << (16 * j);
-        }
-        qh[ks][k] = hi;
-        ql[ks][k] = lo;
-      }
+      for (int k = 0; k < 2; ++k) qa[ks][k] = pack_half2(bf16_lo(qa[ks][k]) * up, bf16_hi(qa[ks][k]) * up);
     m = mo = kNoScore;
     l = 0.f;
 #pragma unroll
@@ -365,31 +355,43 @@ struct Fp8Rows {
                                        float scale_log2, const float2* scales, int step, Release release) {
     const int mi = lane >> 3, r8 = lane & 7, c = lane & 3;
     const float2 sc0 = scales[0], sc1 = scales[step];
-    const float qs = qinv * scale_log2;
-    const float ks0 = qs * sc0.x, ks1 = qs * sc1.x;
-    const float lv0 = __log2f(sc0.y), lv1 = __log2f(sc1.y);
+    // chunk (2 ks + (mi & 1)) of row r sits at ((2 ks + (mi & 1)) ^ (r & 7)) << 4: an XOR
+    // with a constant from step to step
+    const uint32_t ka = kb + ((mi >> 1) * 8 + r8) * 128 + (((mi & 1) ^ r8) << 4);
     float sh[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) sh[n][0] = sh[n][1] = sh[n][2] = sh[n][3] = 0.f;
+    uint32_t kw[KS / 2][2][4];                              // (tokens 0-7 | 8-15) x chunks 2 k2, 2 k2 + 1
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      uint32_t kr[NT][2];
+    for (int k2 = 0; k2 < KS / 2; ++k2)
 #pragma unroll
-      for (int hb = 0; hb < 2; ++hb) {
-        const int row = (mi >> 1) * 8 + r8;
-        ldsm_x4(kb + hb * half + row * 128 + (((2 * ks + (mi & 1)) ^ r8) << 4), kr[2 * hb][0], kr[2 * hb][1],
-                kr[2 * hb + 1][0], kr[2 * hb + 1][1]);
-      }
+      for (int hb = 0; hb < 2; ++hb)
+        ldsm_x4((ka + hb * half) ^ (k2 << 5), kw[k2][hb][0], kw[k2][hb][1], kw[k2][hb][2], kw[k2][hb][3]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)                          // c0, c1: hi; c2, c3: lo (row g + 8)
-        mma_e4m3(sh[n], qh[ks][0], ql[ks][0], qh[ks][1], ql[ks][1], kr[n][0], kr[n][1]);
-    }
+    for (int k2 = 0; k2 < KS / 2; ++k2)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          uint32_t b0, b1;
+          halves_of(kw[k2][n >> 1][2 * (n & 1) + k], b0, b1);
+          mma_f16(sh[n], qa[2 * k2 + k][0], 0u, qa[2 * k2 + k][1], 0u, b0, b1);
+        }
+    // V's codes come in while the scores are worked on: token blocks 0-7, 8-15, 16-23, 24-31
+    const uint32_t va = vb + (mi >> 1) * half + ((mi & 1) * 8 + r8) * 128 + (r8 << 4);
+    uint32_t vw[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) ldsm_x4_trans(va ^ (mt << 4), vw[mt][0], vw[mt][1], vw[mt][2], vw[mt][3]);
+    release();
     // tokens 8 n + 2 c, 8 n + 2 c + 1 of row lane / 4
+    const float qs = qinv * scale_log2;
+    const float ks0 = qs * sc0.x, ks1 = qs * sc1.x;
+    const float lv0 = __log2f(sc0.y), lv1 = __log2f(sc1.y);
     float sv[2 * NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) sv[2 * n + e] = (sh[n][e] + sh[n][e + 2]) * (n < 2 ? ks0 : ks1);
+      for (int e = 0; e < 2; ++e) sv[2 * n + e] = sh[n][e] * (n < 2 ? ks0 : ks1);
     if (!see.all) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -408,29 +410,21 @@ struct Fp8Rows {
     const float alpha = fast_exp2(m - mn), beta = fast_exp2(mo - mon);
     m = mn;
     mo = mon;
+    // w = p 2^(lv + m - mo): under 1 by mo's choice.  (The bound on the factor leaves out
+    // weights only where a page's scale is 2^116 times the others' and its probability 0.)
+    const float f0 = fast_exp2(fminf(lv0 + (mn - mon) + kPLog2, 126.f));
+    const float f1 = fast_exp2(fminf(lv1 + (mn - mon) + kPLog2, 126.f));
+    uint32_t pb[NT];
     float psum = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2 * NT; ++e) psum += fast_exp2(sv[e] - mn);
-    l = l * alpha + psum;
-    const float d0 = lv0 - mon, d1 = lv1 - mon;
-    uint32_t ph[NT], pl[NT];
-#pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float d = n < 2 ? d0 : d1;
-      split_e4m3x2(fast_exp2(sv[2 * n] + d) * kPScale, fast_exp2(sv[2 * n + 1] + d) * kPScale, ph[n], pl[n]);
+      const float p0 = fast_exp2(sv[2 * n] - mn), p1 = fast_exp2(sv[2 * n + 1] - mn);
+      psum += p0 + p1;
+      pb[n] = pack_half2(p0 * (n < 2 ? f0 : f1), p1 * (n < 2 ? f0 : f1));
     }
-    uint32_t bh0 = ph[0] | (ph[1] << 16), bh1 = ph[2] | (ph[3] << 16);
-    const uint32_t bl0 = pl[0] | (pl[1] << 16), bl1 = pl[2] | (pl[3] << 16);
-    if constexpr (kPack) {
-      const uint32_t x0 = __shfl_xor_sync(kFull, bl0, 16), x1 = __shfl_xor_sync(kFull, bl1, 16);
-      if (lane >= 16) {
-        bh0 = x0;
-        bh1 = x1;
-      }
-    }
+    l = l * alpha + psum;
     if (__any_sync(kFull, beta != 1.f)) {
-      const int hc = kPack ? (c & 1) : c;
-      const float a_even = __shfl_sync(kFull, beta, 8 * hc), a_odd = __shfl_sync(kFull, beta, 8 * hc + 4);
+      const float a_even = __shfl_sync(kFull, beta, 8 * c), a_odd = __shfl_sync(kFull, beta, 8 * c + 4);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         o[mt][0] *= a_even;
@@ -440,16 +434,14 @@ struct Fp8Rows {
       }
     }
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      uint32_t vr[4];
-      ldsm_x4_trans(vb + (mi >> 1) * half + ((mi & 1) * 8 + r8) * 128 + ((mt ^ r8) << 4), vr[0], vr[1], vr[2],
-                    vr[3]);
-      const uint32_t a0 = __byte_perm(vr[0], vr[1], 0x6420), a1 = __byte_perm(vr[0], vr[1], 0x7531);
-      const uint32_t a2 = __byte_perm(vr[2], vr[3], 0x6420), a3 = __byte_perm(vr[2], vr[3], 0x7531);
-      mma_e4m3(o[mt], a0, a1, a2, a3, bh0, bh1);
-      if constexpr (!kPack) mma_e4m3(o[mt], a0, a1, a2, a3, bl0, bl1);
-    }
-    release();
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        uint32_t a[4];                                      // column 2 g's pair, column 2 g + 1's
+        halves_of(__byte_perm(vw[mt][i], 0u, 0x3120), a[0], a[1]);
+        halves_of(__byte_perm(vw[mt][i + 1], 0u, 0x3120), a[2], a[3]);
+        mma_f16(o[mt], a[0], a[1], a[2], a[3], pb[i], pb[i + 1]);
+      }
   }
 
   __device__ __forceinline__ void store(float* macc, float* ml) {
@@ -461,15 +453,11 @@ struct Fp8Rows {
       ml[g * 2 + 1] = lt;
     }
     // the sums under m instead of mo
-    const float back = fast_exp2(mo - m) * (1.f / kPScale);
+    const float back = fast_exp2(mo - m - kPLog2);
     const int h0 = 2 * c, h1 = 2 * c + 1;
-    const float b0 = __shfl_sync(kFull, back, (8 * c) & 31), b1 = __shfl_sync(kFull, back, (8 * c + 4) & 31);
+    const float b0 = __shfl_sync(kFull, back, 8 * c), b1 = __shfl_sync(kFull, back, 8 * c + 4);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      if constexpr (kPack) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][e] += __shfl_xor_sync(kFull, o[mt][e], 2);
-      }
       const int d = 16 * mt + 2 * g;                        // rows g and g + 8: columns 2 g, 2 g + 1
       if (h0 < rows) *reinterpret_cast<float2*>(macc + h0 * D + d) = make_float2(o[mt][0] * b0, o[mt][2] * b0);
       if (h1 < rows) *reinterpret_cast<float2*>(macc + h1 * D + d) = make_float2(o[mt][1] * b1, o[mt][3] * b1);
@@ -487,17 +475,19 @@ struct F32Rows : CoreConsumer<DecodeTraits<false, D, G>> {
   __device__ __forceinline__ void init(const SpanParams&, int lane_, float* ps_) { Base::init(lane_, ps_); }
   __device__ __forceinline__ int row() const { return this->g_lane; }
 
-  __device__ __forceinline__ void begin(const SpanParams& p, int b, int head) {
+  __device__ __forceinline__ void load(const SpanParams& p, int b, int head) {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const uint4* src = reinterpret_cast<const uint4*>(p.q + query_row(p, b, head, g) * (4 * D));
 #pragma unroll
-      for (int c = 0; c < Tr::NCH; ++c) {
-        const uint4 w = src[this->r + 8 * c];
-        unpack_chunk<Tr>(w, &this->qf[g][c * 4]);
+      for (int c = 0; c < Tr::NCH; ++c) unpack_chunk<Tr>(src[this->r + 8 * c], &this->qf[g][c * 4]);
+    }
+  }
+  __device__ __forceinline__ void begin(const SpanParams& p) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) this->qf[g][c * 4 + e] *= p.scale_log2;
-      }
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+      for (int e = 0; e < Tr::EPL; ++e) this->qf[g][e] *= p.scale_log2;
       this->m[g] = kNoScore;
 #pragma unroll
       for (int c = 0; c < Tr::CPL; ++c) this->acc[g][c] = 0.f;
@@ -599,14 +589,9 @@ struct Cols {
       v[0] = t.x; v[1] = t.y;
     }
   }
-  __device__ __forceinline__ void load_peer(uint32_t a) {
-    if constexpr (CPL == 4) {
-      const float4 t = peer_f4(a);
-      v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-    } else {
-      const float2 t = peer_f2(a);
-      v[0] = t.x; v[1] = t.y;
-    }
+  __device__ __forceinline__ void store_peer(uint32_t a) const {
+    if constexpr (CPL == 4) peer_store(a, v[0], v[1], v[2], v[3]);
+    else peer_store(a, v[0], v[1]);
   }
   __device__ __forceinline__ void store(float* p) const {
     if constexpr (CPL == 4)
@@ -629,12 +614,19 @@ struct Cols {
   }
 };
 
+// 1 / l, or 0 where no token was seen (l = 0: the row is zeros); NaN stays.
+__device__ __forceinline__ float inverse_sum(float l) { return l > 0.f || l != l ? 1.f / l : 0.f; }
+// Base-2 logarithm of the sum under maximum m.
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l > 0.f ? m + __log2f(l) : (l != l ? l : -INFINITY);
+}
+
 template <SpanPool P, int D, int G>
 struct RowsOf;
 template <int D, int G>
 struct RowsOf<SpanPool::kBf16, D, G> { using type = Bf16Rows<D>; };
 template <int G>
-struct RowsOf<SpanPool::kFp8, 128, G> { using type = Fp8Rows<G>; };
+struct RowsOf<SpanPool::kFp8, 128, G> { using type = Fp8Rows; };
 template <int D, int G>
 struct RowsOf<SpanPool::kF32, D, G> { using type = F32Rows<D, G>; };
 
@@ -662,6 +654,9 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + at.bars);
   uint64_t* empty = full + p.ring;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + at.flag);
+  // clusters: [row / splits][CTA] states of the rows that this CTA joins
+  float* joint = reinterpret_cast<float*>(smem + at.total);
+  float* joint_ml = joint + p.joint_slots * D;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hg = 1 << p.hg_log2, wph_log2 = 3 - p.hg_log2, wph = 1 << wph_log2;
@@ -674,19 +669,23 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
     *abort_flag = 0;
     fence_mbar_init();
   }
+  if (p.splits > 1) cluster_arrive();                        // waited for before the first store to a peer
+  if (threadIdx.x == 32) {
+    prefetch_map(&p.map_k);
+    prefetch_map(&p.map_v);
+  }
   wait_prior_grids();
   allow_next_grid();
   __syncthreads();
 
   // ---- this CTA's stages: from stage st0 of segment (b0, grp0), cnt of them
-  int b0, grp0, st0, cnt, rank = 0;
-  long long share = 0, begin_at = 0;
+  int b0, grp0, st0, cnt, len0, rank = 0;
   if (p.splits) {
-    rank = static_cast<int>(blockIdx.x) % p.splits;
-    const int seg = static_cast<int>(blockIdx.x) / p.splits;
-    b0 = seg / p.ngroups;
-    grp0 = seg - b0 * p.ngroups;
+    rank = blockIdx.x;
+    grp0 = blockIdx.y;
+    b0 = blockIdx.z;
     const int len = p.lens[b0];
+    len0 = len;
     if (threadIdx.x == 0 && rank == 0 && grp0 == 0 &&
         (len < 0 || len > p.max_len || (len > 0 && len < p.q_len)))
       report(p.device_errors, PA_DEVERR_BAD_LENGTH);
@@ -699,8 +698,10 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
     const int s0 = min(static_cast<int>(threadIdx.x) * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
     long long sum = 0;
     bool bad = false;
+    int last_len = 0;
     for (int b = s0; b < s1; ++b) {
       const int len = p.lens[b];
+      last_len = len;
       bad |= len < 0 || len > p.max_len || (len > 0 && len < p.q_len);
       sum += make_span<TU>(p, len).nst;
     }
@@ -721,12 +722,13 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
     }
     total *= p.ngroups;
     before *= p.ngroups;
-    share = (total + gridDim.x - 1) / gridDim.x;
-    begin_at = min(share * blockIdx.x, total);
+    const long long share = (total + gridDim.x - 1) / gridDim.x;
+    const long long begin_at = min(share * blockIdx.x, total);
     cnt = static_cast<int>(min(begin_at + share, total) - begin_at);
     if (cnt > 0 && before <= begin_at && begin_at < before + sum * p.ngroups) {
       for (int b = s0; b < s1; ++b) {
-        const int nst = make_span<TU>(p, p.lens[b]).nst;
+        const int len = per == 1 ? last_len : p.lens[b];
+        const int nst = make_span<TU>(p, len).nst;
         const long long n = static_cast<long long>(nst) * p.ngroups;
         if (begin_at < before + n) {
           const int rem = static_cast<int>(begin_at - before);
@@ -734,6 +736,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
           start[0] = b;
           start[1] = rem / nst;
           start[2] = rem % nst;
+          start[3] = len;
           break;
         }
         before += n;
@@ -744,10 +747,8 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
     b0 = start[0];
     grp0 = start[1];
     st0 = start[2];
-    if (cnt <= 0) {
-      if (threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
-      return;
-    }
+    len0 = start[3];
+    if (cnt <= 0) return;
   }
 
   if (warp == kSpanWarps) {
@@ -764,7 +765,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
     const bool s_mine = FP8 && s_ps < wph * parts;
     const float* s_src = kv ? p.v_scales : p.k_scales;
 
-    Walk<TU> wk(p, b0, grp0);
+    Walk<TU> wk(p, b0, grp0, len0);
     int st = st0, fetched = 0;
     int q_phys[kAhead], q_off[kAhead], q_head[kAhead];
     bool q_vis[kAhead];
@@ -867,16 +868,17 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
     const uint32_t tile_off = sub * parts * op_bytes + hl * t_op * (ROW / SLABS);
     Rows rows;
     rows.init(p, lane, reinterpret_cast<float*>(smem + at.ps) + warp * TU * p.rows);
-    Walk<TU> wk(p, b0, grp0);
+    Walk<TU> wk(p, b0, grp0, len0);
     int s = 0, left = cnt, st = st0;
     uint32_t parity = 0;
     bool first_seg = true, aborted = false;
+    rows.load(p, wk.b, (wk.grp << p.hg_log2) + hl);
     for (;;) {
-      const Span& sp = wk.sp;
+      const Span sp = wk.sp;
       const int st_end = min(sp.nst, st + left);
-      const int st_begin = st;
-      const int head = (wk.grp << p.hg_log2) + hl;
-      rows.begin(p, wk.b, head);
+      const int st_begin = st, seg_b = wk.b, seg_grp = wk.grp;
+      const int head = (seg_grp << p.hg_log2) + hl;
+      rows.begin(p);
       const int q_pos = sp.len - p.q_len + (rows.row() >> p.group_log2);   // of this lane's row
       for (; st < st_end; ++st) {
         if (!mbar_wait(&full[s], parity, p.wait_limit)) {
@@ -939,100 +941,119 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
         }
       }
       left -= st_end - st_begin;
-      // ---- the segment's part is done: join the head's warps
-      float* my_acc = macc + warp * p.rows * D;
-      rows.store(my_acc, mml + warp * p.rows * 2);
+      if (left > 0) {
+        wk.next();
+        rows.load(p, wk.b, (wk.grp << p.hg_log2) + hl);
+      }
+      // ---- the segment's part is done: join the head's warps.  Rows go round them; the
+      // lanes hold the warps' (or, of a warp alone, the rows') maxima and sums, so that no
+      // row waits for another's.
+      rows.store(macc + warp * p.rows * D, mml + warp * p.rows * 2);
       // (the warps agree on giving up, so that none waits at a barrier for one that left)
       if (wph > 1 || p.splits) aborted = consumer_barrier_any(aborted); else __syncwarp();
       const int R = hg * p.rows;
       const bool whole = st_begin == 0 && st_end == sp.nst;
-      for (int r = sub; r < p.rows; r += wph) {
-        const int w0 = hl << wph_log2;
-        float M = kNoScore;
-        for (int w = 0; w < wph; ++w) M = fmaxf(M, mml[((w0 + w) * p.rows + r) * 2]);
-        float lam = 0.f;
-        Cols<CPL> acc;
+      const int64_t part0 = (2 * static_cast<int64_t>(blockIdx.x) + (first_seg ? 0 : 1)) * R + hl * p.rows;
+      auto put = [&](int r, Cols<CPL>& acc, float inv, float lse) {
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) acc.v[c] = 0.f;
-#pragma unroll 4
-        for (int w = 0; w < wph; ++w) {
-          const float f = fast_exp2(mml[((w0 + w) * p.rows + r) * 2] - M);
-          lam = fmaf(f, mml[((w0 + w) * p.rows + r) * 2 + 1], lam);
-          Cols<CPL> x;
-          x.load(macc + ((w0 + w) * p.rows + r) * D + lane * CPL);
-#pragma unroll
-          for (int c = 0; c < CPL; ++c) acc.v[c] = fmaf(f, x.v[c], acc.v[c]);
-        }
-        if (p.splits > 1) {
-          // the cluster's CTAs join later: the ring is free by now (every copy consumed)
-          float* cb = reinterpret_cast<float*>(smem);
-          acc.store(cb + (hl * p.rows + r) * D + lane * CPL);
-          if (lane == 0) {
-            cb[R * D + (hl * p.rows + r) * 2] = M;
-            cb[R * D + (hl * p.rows + r) * 2 + 1] = lam;
-          }
+        for (int c = 0; c < CPL; ++c) acc.v[c] *= inv;
+        if (whole) {
+          acc.template store_out<BF16_OUT>(p.out, query_row(p, seg_b, head, r) * D + lane * CPL);
         } else {
-          const float inv = lam > 0.f || lam != lam ? 1.f / lam : 0.f;   // no token seen: zeros
+          acc.store(p.part_out + (part0 + r) * D + lane * CPL);
+          if (lane == 0) p.part_lse[part0 + r] = lse;
+        }
+      };
+      if (wph == 1 && p.splits <= 1) {
+        const float2 ml = lane < p.rows ? reinterpret_cast<const float2*>(mml + warp * p.rows * 2)[lane]
+                                        : make_float2(0.f, 0.f);
+        const float inv = inverse_sum(ml.y), lse = log_sum(ml.x, ml.y);
+#pragma unroll 4
+        for (int r = 0; r < p.rows; ++r) {
+          Cols<CPL> acc;
+          acc.load(macc + (warp * p.rows + r) * D + lane * CPL);
+          put(r, acc, __shfl_sync(kFull, inv, r), __shfl_sync(kFull, lse, r));
+        }
+      } else {
+        const int w0 = hl << wph_log2;
+        if (p.splits > 1) cluster_wait();                    // every CTA of the cluster runs
+        for (int r = sub; r < p.rows; r += wph) {
+          const float2 ml = lane < wph ? reinterpret_cast<const float2*>(mml)[(w0 + lane) * p.rows + r]
+                                       : make_float2(kNoScore, 0.f);
+          Cols<CPL> x[kSpanWarps];
 #pragma unroll
-          for (int c = 0; c < CPL; ++c) acc.v[c] *= inv;
-          if (whole) {
-            acc.template store_out<BF16_OUT>(p.out, query_row(p, wk.b, head, r) * D + lane * CPL);
+          for (int w = 0; w < kSpanWarps; ++w)               // (a head with fewer warps: its last again, weight 0)
+            x[w].load(macc + ((w0 + min(w, wph - 1)) * p.rows + r) * D + lane * CPL);
+          float M = ml.x;
+#pragma unroll
+          for (int o = 1; o < kSpanWarps; o <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+          const float f = lane < wph ? fast_exp2(ml.x - M) : 0.f;
+          float lam = f * ml.y;
+#pragma unroll
+          for (int o = 1; o < kSpanWarps; o <<= 1) lam += __shfl_xor_sync(kFull, lam, o);
+          M = __shfl_sync(kFull, M, 0);
+          lam = __shfl_sync(kFull, lam, 0);
+          Cols<CPL> acc;
+#pragma unroll
+          for (int c = 0; c < CPL; ++c) acc.v[c] = 0.f;
+#pragma unroll
+          for (int w = 0; w < kSpanWarps; ++w) {
+            const float fw = __shfl_sync(kFull, f, w);
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) acc.v[c] = fmaf(fw, x[w].v[c], acc.v[c]);
+          }
+          if (p.splits > 1) {
+            // to the CTA of the cluster that joins this row
+            const int row = hl * p.rows + r, to = row % p.splits, slot = row / p.splits * p.splits + rank;
+            acc.store_peer(peer_addr(smem_addr(joint + slot * D + lane * CPL), to));
+            if (lane == 0) peer_store(peer_addr(smem_addr(joint_ml + slot * 2), to), M, lam);
           } else {
-            const int64_t row = (2 * static_cast<int64_t>(blockIdx.x) + (first_seg ? 0 : 1)) * R + hl * p.rows + r;
-            acc.store(p.part_out + row * D + lane * CPL);
-            if (lane == 0) p.part_lse[row] = lam > 0.f ? M + __log2f(lam) : (lam != lam ? lam : -INFINITY);
+            put(r, acc, inverse_sum(lam), log_sum(M, lam));
           }
         }
-      }
-      if (!p.splits && first_seg && warp == 0 && lane == 0) {
-        // a segment that began in an earlier share and ends here: that share, and which
-        // of its two partials
-        int4 cut = make_int4(-1, 0, 0, 0);
-        if (st_begin > 0 && st_end == sp.nst) {
-          const long long seg_at = begin_at - st_begin;
-          const long long c1 = seg_at / share;
-          cut = make_int4(wk.b, wk.grp, static_cast<int>(c1), seg_at == c1 * share ? 0 : 1);
-        }
-        p.cuts[blockIdx.x] = cut;
       }
       if (left <= 0 || aborted) break;
       if (wph > 1) consumer_barrier(); else __syncwarp();      // the states have been read
       first_seg = false;
       st = 0;
-      wk.next();
     }
   }
 
   if (p.splits > 1) {
-    // ---- the cluster joins its CTAs' states; rows go round its warps
-    cluster_sync();
+    // ---- the cluster joins its CTAs' states: row r in CTA r mod splits, where every CTA
+    // has put its own (which nobody has to read across the cluster or wait for to leave)
+    if (warp == kSpanWarps) cluster_wait();
+    cluster_arrive();
+    cluster_wait();
     if (warp < kSpanWarps) {
       const int R = hg * p.rows;
-      const uint32_t cb = smem_addr(smem);
-      for (int r = rank * kSpanWarps + warp; r < R; r += p.splits * kSpanWarps) {
-        float2 ml[kSpanCluster];
-        float M = kNoScore;
+      for (int r = warp * p.splits + rank; r < R; r += kSpanWarps * p.splits) {
+        const int slot = r - rank;                           // of CTA 0's state
+        const float2 ml = lane < p.splits ? reinterpret_cast<const float2*>(joint_ml)[slot + lane]
+                                          : make_float2(kNoScore, 0.f);
+        Cols<CPL> x[kSpanCluster];
 #pragma unroll
         for (int c = 0; c < kSpanCluster; ++c)
-          if (c < p.splits) {
-            ml[c] = peer_f2(peer_addr(cb + (R * D + r * 2) * 4, c));
-            M = fmaxf(M, ml[c].x);
-          }
-        float lam = 0.f;
+          if (c < p.splits) x[c].load(joint + (slot + c) * D + lane * CPL);
+        float M = ml.x;
+#pragma unroll
+        for (int o = 1; o < kSpanCluster; o <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+        M = __shfl_sync(kFull, M, 0);
+        const float f = fast_exp2(ml.x - M);
+        float lam = f * ml.y;
+#pragma unroll
+        for (int o = 1; o < kSpanCluster; o <<= 1) lam += __shfl_xor_sync(kFull, lam, o);
+        const float inv = inverse_sum(__shfl_sync(kFull, lam, 0));
         Cols<CPL> acc;
 #pragma unroll
         for (int c = 0; c < CPL; ++c) acc.v[c] = 0.f;
 #pragma unroll
         for (int c = 0; c < kSpanCluster; ++c)
           if (c < p.splits) {
-            Cols<CPL> x;
-            x.load_peer(peer_addr(cb + (r * D + lane * CPL) * 4, c));
-            const float f = fast_exp2(ml[c].x - M);
-            lam = fmaf(f, ml[c].y, lam);
+            const float fc = __shfl_sync(kFull, f, c);
 #pragma unroll
-            for (int e = 0; e < CPL; ++e) acc.v[e] = fmaf(f, x.v[e], acc.v[e]);
+            for (int e = 0; e < CPL; ++e) acc.v[e] = fmaf(fc, x[c].v[e], acc.v[e]);
           }
-        const float inv = lam > 0.f || lam != lam ? 1.f / lam : 0.f;
 #pragma unroll
         for (int c = 0; c < CPL; ++c) acc.v[c] *= inv;
         const int h = r / p.rows;
@@ -1040,13 +1061,13 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
             p.out, query_row(p, b0, (grp0 << p.hg_log2) + h, r - h * p.rows) * D + lane * CPL);
       }
     }
-    cluster_sync();                                          // peers have read this CTA's memory
   }
 }
 
-// Launch of one instance: a plain grid of shares, or clusters of p.splits CTAs.
+// Launch of one instance: a plain grid of shares, or a grid (splits, head groups,
+// sequences) of clusters of p.splits CTAs.
 template <SpanPool P, int D, int G>
-cudaError_t run_span(const SpanParams& p, int grid, int smem, cudaStream_t stream) {
+cudaError_t run_span(const SpanParams& p, dim3 grid, int smem, cudaStream_t stream) {
   // the opt-in to more than 48 KiB of dynamic shared memory is per device
   static std::atomic<uint64_t> configured{0};
   int device = 0;
@@ -1059,7 +1080,7 @@ cudaError_t run_span(const SpanParams& p, int grid, int smem, cudaStream_t strea
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kSpanThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

@@ -56,7 +56,7 @@ __host__ __device__ constexpr SpanSmem span_smem(SpanPool pool, int head_dim, in
   off += 2 * ring * 8;
   s.flag = off;
   off += 8;
-  s.total = off;
+  s.total = (off + 15) / 16 * 16;
   return s;
 }
 
@@ -74,9 +74,9 @@ struct SpanParams {
   int block_size, num_blocks, max_blocks, max_len, window, sinks;
   int ring;
   int splits;                                     // CTAs of a cluster that share a segment; 0: shares
+  int joint_slots;                                // clusters: states that a CTA has room for
   float* part_out;                                // shares: [2 CTAs][hg * rows][head_dim]
   float* part_lse;                                // shares: [2 CTAs][hg * rows]
-  int4* cuts;                                     // shares: [CTAs] segments that end in a CTA but began before
   int32_t* device_errors;
   uint32_t wait_limit;
 };
@@ -103,8 +103,8 @@ struct SpanArgs {
 size_t span_workspace_size(int rows, int num_kv_heads, int head_dim, int num_sms);
 cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream);
 
-cudaError_t run_span_bf16(int head_dim, const SpanParams& p, int grid, int smem, cudaStream_t stream);
-cudaError_t run_span_f32(int head_dim, const SpanParams& p, int grid, int smem, cudaStream_t stream);
-cudaError_t run_span_fp8(const SpanParams& p, int grid, int smem, cudaStream_t stream);
+cudaError_t run_span_bf16(int head_dim, const SpanParams& p, dim3 grid, int smem, cudaStream_t stream);
+cudaError_t run_span_f32(int head_dim, const SpanParams& p, dim3 grid, int smem, cudaStream_t stream);
+cudaError_t run_span_fp8(const SpanParams& p, dim3 grid, int smem, cudaStream_t stream);
 
 }  // namespace pa

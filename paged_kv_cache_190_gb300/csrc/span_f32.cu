@@ -5,7 +5,7 @@
 namespace pa {
 namespace {
 template <int D>
-cudaError_t run(const SpanParams& p, int grid, int smem, cudaStream_t stream) {
+cudaError_t run(const SpanParams& p, dim3 grid, int smem, cudaStream_t stream) {
   switch (p.rows) {
     case 1: return span::run_span<SpanPool::kF32, D, 1>(p, grid, smem, stream);
     case 2: return span::run_span<SpanPool::kF32, D, 2>(p, grid, smem, stream);
@@ -14,7 +14,7 @@ cudaError_t run(const SpanParams& p, int grid, int smem, cudaStream_t stream) {
   }
 }
 }  // namespace
-cudaError_t run_span_f32(int head_dim, const SpanParams& p, int grid, int smem, cudaStream_t stream) {
+cudaError_t run_span_f32(int head_dim, const SpanParams& p, dim3 grid, int smem, cudaStream_t stream) {
   return head_dim == 128 ? run<128>(p, grid, smem, stream) : run<64>(p, grid, smem, stream);
 }
 }  // namespace pa

@@ -10,25 +10,12 @@
 #include <cstring>
 
 #include "pa_device.cuh"
-#include "span_decode.h"
+#include "span_list.cuh"
 
 namespace pa {
 namespace {
 
 constexpr int kJoinWarps = 8;
-
-template <int CPL>
-struct Joined {
-  float M = -3.0e38f, S = 0.f, acc[CPL] = {};
-  __device__ __forceinline__ void add(float lse, const float* v) {
-    const float mn = fmaxf(M, lse);
-    const float f = fast_exp2(M - mn), w = fast_exp2(lse - mn);
-    S = fmaf(S, f, w);
-#pragma unroll
-    for (int k = 0; k < CPL; ++k) acc[k] = fmaf(acc[k], f, w * v[k]);
-    M = mn;
-  }
-};
 
 template <int CPL>
 __device__ __forceinline__ void load_part(const float* p, float* v) {
@@ -41,64 +28,134 @@ __device__ __forceinline__ void load_part(const float* p, float* v) {
   }
 }
 
-// A segment whose shares are c1 .. c: out = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M)
-// over its partials.  Block (c, r): WIDE, the row r by 8 warps that take partials in
-// turn (few segments: each spans many shares); else 8 rows, a warp each.
-template <bool BF16, int CPL, bool WIDE>
-__global__ void __launch_bounds__(kJoinWarps * 32) span_join_kernel(const SpanParams p) {
+// A segment cut into n partials: out = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).
+// Block (x, y): BY_SEGMENT, segment x (no more of them than shares); else the segment that
+// share x ends but does not begin.  WIDE, row y by 8 warps that take partials in turn (few
+// segments: each spans many shares); else 8 rows, a warp each.  Where the cuts are follows
+// from the lengths and is worked out before the wait for the attention kernel: that one
+// lets this grid start once its own inputs are complete.  After it a lane holds a partial's
+// weight, 32 partials at a time, so that all their rows are on their way together.
+template <int TU, bool BF16, int CPL, bool BY_SEGMENT, bool WIDE>
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) span_join_kernel(const SpanParams p, int ctas) {
   constexpr int D = CPL * 32;
   __shared__ float sm[kJoinWarps], ss[kJoinWarps];
   __shared__ float sacc[WIDE ? kJoinWarps : 1][D];
-  wait_prior_grids();
+  __shared__ long long sums[kJoinWarps], found[2];
+  __shared__ int where[2];
   allow_next_grid();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x;
-  const int4 cut = p.cuts[c];
-  if (cut.x < 0) return;
+  // stages before each thread's run of sequences, and in all
+  const int per = (p.num_seqs + kJoinWarps * 32 - 1) / (kJoinWarps * 32);
+  const int s0 = min(static_cast<int>(threadIdx.x) * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
+  long long sum = 0;
+  for (int b = s0; b < s1; ++b) sum += span::make_span<TU>(p, p.lens[b]).nst;
+  long long x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  if (threadIdx.x == 0) where[0] = -1;
+  __syncthreads();
+  long long before = x - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  total *= p.ngroups;
+  before *= p.ngroups;
+  const long long share = (total + ctas - 1) / ctas;
+  const long long at = share * blockIdx.x;                   // where share x begins
+  for (int b = s0; b < s1; ++b) {
+    const int nst = span::make_span<TU>(p, p.lens[b]).nst;
+    const long long n = static_cast<long long>(nst) * p.ngroups;
+    int grp = -1;
+    if (BY_SEGMENT)
+      grp = static_cast<int>(blockIdx.x) / p.ngroups == b ? static_cast<int>(blockIdx.x) % p.ngroups : -1;
+    else if (before <= at && at < before + n)
+      grp = static_cast<int>((at - before) / nst);
+    if (grp >= 0) {
+      where[0] = b;
+      where[1] = grp;
+      found[0] = before + static_cast<long long>(grp) * nst;
+      found[1] = found[0] + nst;
+    }
+    before += n;
+  }
+  __syncthreads();
+  // the share in which the segment ends, and the one in which it began
+  const int c = BY_SEGMENT ? static_cast<int>((found[1] - 1) / share) : static_cast<int>(blockIdx.x);
+  const bool mine = where[0] >= 0 && found[1] <= share * (c + 1) && found[0] < share * c;
+  wait_prior_grids();
+  if (!mine) return;
   const int R = p.rows << p.hg_log2;
   const int r = WIDE ? static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.y) * kJoinWarps + warp;
   if (r >= R) return;                                        // (never with WIDE)
-  const int n = c - cut.z + 1;
-  Joined<CPL> st;
-#pragma unroll 4
-  for (int i = WIDE ? warp : 0; i < n; i += WIDE ? kJoinWarps : 1) {
-    const int64_t slot = 2 * static_cast<int64_t>(cut.z + i) + (i == 0 ? cut.w : 0);
-    float v[CPL];
-    load_part<CPL>(p.part_out + (slot * R + r) * D + lane * CPL, v);
-    st.add(p.part_lse[slot * R + r], v);
+  const int c1 = static_cast<int>(found[0] / share), n = c - c1 + 1;
+  // a share's first partial is its entry 2 c; its last segment's, if that is another one, 2 c + 1
+  const int first = 2 * c1 + (found[0] == share * c1 ? 0 : 1);
+  auto row_of = [&](int i) { return static_cast<int64_t>(i == 0 ? first : 2 * (c1 + i)) * R + r; };
+  constexpr int STEP = WIDE ? kJoinWarps : 1;
+  float M = -3.0e38f, S = 0.f, acc[CPL] = {};
+  for (int i0 = WIDE ? warp : 0; i0 < n; i0 += 32 * STEP) {
+    const int mine = i0 + lane * STEP;
+    const float lse = mine < n ? p.part_lse[row_of(mine)] : -INFINITY;
+    float mx = lse;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float mn = fmaxf(M, mx);
+    const float keep = fast_exp2(M - mn), w = fast_exp2(lse - mn);
+    float sum = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    S = fmaf(S, keep, sum);
+    M = mn;
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) acc[k] *= keep;
+    const int m = min(32, (n - i0 + STEP - 1) / STEP);
+#pragma unroll 8
+    for (int j = 0; j < m; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      float v[CPL];
+      load_part<CPL>(p.part_out + row_of(i0 + j * STEP) * D + lane * CPL, v);
+#pragma unroll
+      for (int k = 0; k < CPL; ++k) acc[k] = fmaf(wj, v[k], acc[k]);
+    }
   }
   if constexpr (WIDE) {
     if (lane == 0) {
-      sm[warp] = st.M;
-      ss[warp] = st.S;
+      sm[warp] = M;
+      ss[warp] = S;
     }
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) sacc[warp][lane * CPL + k] = st.acc[k];
+    for (int k = 0; k < CPL; ++k) sacc[warp][lane * CPL + k] = acc[k];
     __syncthreads();
     if (warp != 0) return;
-    float M = sm[0];
+    M = sm[0];
 #pragma unroll
     for (int w = 1; w < kJoinWarps; ++w) M = fmaxf(M, sm[w]);
-    st.S = 0.f;
+    S = 0.f;
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) st.acc[k] = 0.f;
+    for (int k = 0; k < CPL; ++k) acc[k] = 0.f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
       const float f = fast_exp2(sm[w] - M);
-      st.S = fmaf(f, ss[w], st.S);
+      S = fmaf(f, ss[w], S);
 #pragma unroll
-      for (int k = 0; k < CPL; ++k) st.acc[k] = fmaf(f, sacc[w][lane * CPL + k], st.acc[k]);
+      for (int k = 0; k < CPL; ++k) acc[k] = fmaf(f, sacc[w][lane * CPL + k], acc[k]);
     }
   }
-  const float inv = st.S > 0.f || st.S != st.S ? 1.f / st.S : 0.f;
-  const int head = (cut.y << p.hg_log2) + r / p.rows, row = r % p.rows;
-  const int64_t o = ((static_cast<int64_t>(cut.x) * p.q_len + (row >> p.group_log2)) * p.num_q_heads +
+  const float inv = S > 0.f || S != S ? 1.f / S : 0.f;
+  const int head = (where[1] << p.hg_log2) + r / p.rows, row = r % p.rows;
+  const int64_t o = ((static_cast<int64_t>(where[0]) * p.q_len + (row >> p.group_log2)) * p.num_q_heads +
                      head * p.group + (row & (p.group - 1))) * D + lane * CPL;
   if constexpr (BF16) {
     uint32_t w[CPL / 2];
 #pragma unroll
     for (int k = 0; k < CPL / 2; ++k) {
-      const __nv_bfloat162 t = __floats2bfloat162_rn(st.acc[2 * k] * inv, st.acc[2 * k + 1] * inv);
+      const __nv_bfloat162 t = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
       w[k] = *reinterpret_cast<const uint32_t*>(&t);
     }
     uint32_t* d = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + o);
@@ -107,14 +164,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) span_join_kernel(const SpanPa
   } else {
     float* d = static_cast<float*>(p.out) + o;
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) d[k] = st.acc[k] * inv;
+    for (int k = 0; k < CPL; ++k) d[k] = acc[k] * inv;
   }
 }
 
-cudaError_t launch_join(const SpanParams& p, bool bf16, int head_dim, bool wide, int ctas, cudaStream_t stream) {
+template <int TU, bool BF16, int CPL>
+cudaError_t launch_join(const SpanParams& p, int64_t segments, int ctas, cudaStream_t stream) {
   const int R = p.rows << p.hg_log2;
+  const bool by_segment = segments <= ctas;
+  const bool wide = segments * 16 <= ctas;                   // each segment is cut into many partials
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(wide ? R : (R + kJoinWarps - 1) / kJoinWarps));
+  cfg.gridDim = dim3(static_cast<unsigned>(by_segment ? segments : ctas),
+                     static_cast<unsigned>(wide ? R : (R + kJoinWarps - 1) / kJoinWarps));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -122,13 +183,9 @@ cudaError_t launch_join(const SpanParams& p, bool bf16, int head_dim, bool wide,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto go = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, p); };
-  if (bf16) {
-    if (head_dim == 128) return wide ? go(span_join_kernel<true, 4, true>) : go(span_join_kernel<true, 4, false>);
-    return wide ? go(span_join_kernel<true, 2, true>) : go(span_join_kernel<true, 2, false>);
-  }
-  if (head_dim == 128) return wide ? go(span_join_kernel<false, 4, true>) : go(span_join_kernel<false, 4, false>);
-  return wide ? go(span_join_kernel<false, 2, true>) : go(span_join_kernel<false, 2, false>);
+  return wide         ? cudaLaunchKernelEx(&cfg, span_join_kernel<TU, BF16, CPL, true, true>, p, ctas)
+         : by_segment ? cudaLaunchKernelEx(&cfg, span_join_kernel<TU, BF16, CPL, true, false>, p, ctas)
+                      : cudaLaunchKernelEx(&cfg, span_join_kernel<TU, BF16, CPL, false, false>, p, ctas);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -180,11 +237,10 @@ int most_heads(int num_kv_heads) {
 
 }  // namespace
 
-// Scratch of the shares: what ends where, and two partials for each CTA.
+// Scratch of the shares: two partials for each CTA.
 size_t span_workspace_size(int rows, int num_kv_heads, int head_dim, int num_sms) {
   const size_t R = static_cast<size_t>(most_heads(num_kv_heads)) * rows;
-  return align256(static_cast<size_t>(num_sms) * sizeof(int4)) + align256(2 * num_sms * R * 4) +
-         align256(2 * num_sms * R * head_dim * 4);
+  return align256(2 * num_sms * R * 4) + align256(2 * num_sms * R * head_dim * 4);
 }
 
 cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream) {
@@ -205,9 +261,10 @@ cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream) {
   const int64_t stages_all = (pairs * blocks + kSpanWarps - 1) / kSpanWarps;
   const SpanSmem fixed = span_smem(a.pool, a.head_dim, rows, 0);
   const int stage = span_stage_bytes(a.pool, a.head_dim);
-  const int ring_most = std::min<int>(kSpanRing, (kSpanSmem - 1024 - fixed.total) / (stage + 160));
+  int ring_most = std::min<int>(kSpanRing, (kSpanSmem - 1024 - fixed.total) / (stage + 160));
 
   int grid = 0, ring = ring_most;
+  dim3 blocks_of;
   const bool clusters = stages_all <= 6 * static_cast<int64_t>(a.num_sms);
   if (clusters) {
     while (hg > 1 && pairs / hg * kSpanCluster < a.num_sms) hg /= 2;
@@ -217,10 +274,16 @@ cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream) {
     int splits = 1;
     while (splits < kSpanCluster && segs * splits < a.num_sms && 2 * splits <= nst) splits *= 2;
     p.splits = splits;
-    grid = static_cast<int>(segs * splits);
+    if (splits > 1) {                            // room for the states that a CTA joins
+      const int joint = (hg * rows + splits) * (a.head_dim + 2) * 4;
+      ring_most = std::min<int>(ring_most, (kSpanSmem - 1024 - fixed.total - joint) / (stage + 160));
+    }
+    blocks_of = dim3(static_cast<unsigned>(splits), static_cast<unsigned>(a.num_kv_heads / hg),
+                     static_cast<unsigned>(a.num_seqs));
     ring = static_cast<int>(std::min<int64_t>(ring_most, (nst + splits - 1) / splits));
   } else {
     grid = a.num_sms;
+    blocks_of = dim3(static_cast<unsigned>(grid));
   }
   int hg_log2 = 0;
   while ((1 << hg_log2) < hg) ++hg_log2;
@@ -257,22 +320,30 @@ cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream) {
   p.wait_limit = a.wait_limit < 0 ? kMaxPolls : static_cast<uint32_t>(a.wait_limit);
   char* ws = static_cast<char*>(a.workspace);
   const size_t R = static_cast<size_t>(hg) * rows;
-  p.cuts = reinterpret_cast<int4*>(ws);
-  p.part_lse = reinterpret_cast<float*>(ws + align256(static_cast<size_t>(a.num_sms) * sizeof(int4)));
+  const int64_t segments = static_cast<int64_t>(a.num_seqs) * p.ngroups;
+  p.part_lse = reinterpret_cast<float*>(ws);
   p.part_out = p.part_lse + align256(2 * a.num_sms * R * 4) / 4;
 
   int smem = span_smem(a.pool, a.head_dim, rows, ring).total;
-  // the cluster's joined rows stand where the ring was
-  if (p.splits > 1) smem = std::max<int>(smem, static_cast<int>(R * (a.head_dim + 2) * 4));
+  if (p.splits > 1) {
+    p.joint_slots = (static_cast<int>(R) + p.splits - 1) / p.splits * p.splits;
+    smem += p.joint_slots * (a.head_dim + 2) * 4;
+  }
   smem += 1024;
   if (ring < 1 || smem > kSpanSmem) return cudaErrorInvalidValue;
-  e = a.pool == SpanPool::kBf16  ? run_span_bf16(a.head_dim, p, grid, smem, stream)
-      : a.pool == SpanPool::kF32 ? run_span_f32(a.head_dim, p, grid, smem, stream)
-                                 : run_span_fp8(p, grid, smem, stream);
+  e = a.pool == SpanPool::kBf16  ? run_span_bf16(a.head_dim, p, blocks_of, smem, stream)
+      : a.pool == SpanPool::kF32 ? run_span_f32(a.head_dim, p, blocks_of, smem, stream)
+                                 : run_span_fp8(p, blocks_of, smem, stream);
   if (e != cudaSuccess || clusters) return e;
-  // few segments: each is cut into many partials
-  const bool wide = static_cast<int64_t>(a.num_seqs) * p.ngroups * 16 <= grid;
-  return launch_join(p, a.pool != SpanPool::kF32, a.head_dim, wide, grid, stream);
+  switch (a.pool) {
+    case SpanPool::kFp8: return launch_join<32, true, 4>(p, segments, grid, stream);
+    case SpanPool::kBf16:
+      return a.head_dim == 128 ? launch_join<16, true, 4>(p, segments, grid, stream)
+                               : launch_join<16, true, 2>(p, segments, grid, stream);
+    default:
+      return a.head_dim == 128 ? launch_join<8, false, 4>(p, segments, grid, stream)
+                               : launch_join<16, false, 2>(p, segments, grid, stream);
+  }
 }
 
 }  // namespace pa
