@@ -228,9 +228,13 @@ cudaError_t make_map(CUtensorMap* map, const void* pool, SpanPool kind, int head
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Heads that a CTA can take together: the largest power of two up to 8 that divides them.
-int most_heads(int num_kv_heads) {
-  int hg = 8;
+// Heads that a CTA takes together: the largest power of two up to 8 (e4m3) or 2 that
+// divides them.  Boxes under 8 KiB cost the copy engine more than their bytes: e4m3 pages
+// of 16 tokens, 885 MB, take 144 us with 8 heads a box (16 KiB), 152 with 4, 180 with 2, 213 with 1.
+// bf16 rows are twice as long, and with 2 heads a segment leaves a quarter of the
+// partials: 131.0 us against 132.2 with 8 (833 MB), 49.5 against 52.0 (269 MB, 8 rows a head).
+int most_heads(SpanPool pool, int num_kv_heads) {
+  int hg = pool == SpanPool::kFp8 ? 8 : 2;
   while (num_kv_heads % hg) hg /= 2;
   return hg;
 }
@@ -239,7 +243,8 @@ int most_heads(int num_kv_heads) {
 
 // Scratch of the shares: two partials for each CTA.
 size_t span_workspace_size(int rows, int num_kv_heads, int head_dim, int num_sms) {
-  const size_t R = static_cast<size_t>(most_heads(num_kv_heads)) * rows;
+  const SpanPool pool = SpanPool::kFp8;                      // (enough for every pool)
+  const size_t R = static_cast<size_t>(most_heads(pool, num_kv_heads)) * rows;
   return align256(2 * num_sms * R * 4) + align256(2 * num_sms * R * head_dim * 4);
 }
 
@@ -256,7 +261,7 @@ cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream) {
   if (p.window < kNoWindow)
     blocks = std::min<int64_t>(blocks, (p.sinks + tu - 1) / tu + (static_cast<int64_t>(p.window) + a.q_len - 1 + tu - 1) / tu + 1);
   blocks = std::max<int64_t>(blocks, 1);
-  int hg = most_heads(a.num_kv_heads);
+  int hg = most_heads(a.pool, a.num_kv_heads);
   const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   const int64_t stages_all = (pairs * blocks + kSpanWarps - 1) / kSpanWarps;
   const SpanSmem fixed = span_smem(a.pool, a.head_dim, rows, 0);
