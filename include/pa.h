@@ -29,6 +29,8 @@
  *     kernels OR PA_DEVERR_* bits when they meet data they refuse (an
  *     out-of-range block id or slot, a length outside the table); the kernels
  *     skip that work instead of faulting.  Read it with pa_read_device_errors.
+ *     (The kernels of some calls start on the device before the stream's work ahead of them
+ *     has ended and wait for it there; they use nothing of it before.)
  *   - Layouts are row-major and contiguous:
  *       k_cache, v_cache : [num_blocks][num_kv_heads][block_size][head_dim]
  *       q, out           : [num_seqs][num_q_heads][head_dim]
@@ -404,10 +406,10 @@ int pa_rope_and_cache_fp8(void* q_out, const void* q, const void* k, const void*
  * pa_decode_fp8_block: decode over such pools for q_len new tokens per sequence,
  * causal among them, with the window and sinks of pa_decode_window (0, 0 for none);
  * q and out bf16, head_dim 128; scales positive and finite; workspace of
- * pa_decode_window_workspace_size.  Logits and sums are
- * float32; q enters the products as two e4m3 parts (exact for bf16 elements down to
- * 2^-10 of their row's largest), and so do the probabilities times V's scale (about
- * the precision of bf16).
+ * pa_decode_window_workspace_size.  Codes enter the products exactly, as halves, and so
+ * does q, scaled by a power of two (bf16 elements are exact down to 2^-22 of their row's
+ * largest); logits, the maxima and the sums are float32; the probabilities times V's
+ * scale are rounded to halves (2^-11) for the product with V's codes.
  *
  * pa_copy_scales: the scale rows of copied pages, dst[d] = src[s] for each pair
  * (s, d) of pa_copy_blocks (src and dst then the same arrays) or pa_swap_blocks

@@ -65,9 +65,9 @@ class Decode:
         """Largest error of each output.  Scores: D products and sums in float32, 2^-22 D of
         the sum of their magnitudes (sums may be cut instead of rounded), so a weight is
         within 2 ds + 2^-20 of itself (exp2's approximation).  bf16: half a step of 2^-8 for
-        each weight and for the result.  e4m3: q's parts are within 2^-17 of the row's
-        largest element, the weights' parts within 2^-8 of each weight (2^-7 with the
-        half-precision step before the split) and 2^-17 of the largest (subnormal steps)."""
+        each weight and for the result.  e4m3: q's elements become halves, scaled so that the
+        row's largest is at least 2^7: exact but for 2^-25 (subnormal steps), 2^-32 of the
+        largest; the weights are halves too, 2^-11 of each and 2^-35 of the largest."""
         d = self.q.shape[-1]
         ds = 2.0 ** -22 * d * parts["dots"][..., None]
         rel = 2 * ds + 2.0 ** -20
@@ -77,5 +77,5 @@ class Decode:
         if self.dtype == "bf16":
             return bar + (2.0 ** -8 * 1.01 + rel) * parts["mag"]
         qmax = np.abs(values(self.q)).max(-1, keepdims=True).astype(np.float64)
-        dq = self.scale * 2.0 ** -17 * qmax * parts["ksum"][..., None]
-        return bar + (2.0 ** -7 + rel + 2 * dq) * parts["mag"] + 2.0 ** -17 * parts["wmax"]
+        dq = self.scale * 2.0 ** -32 * qmax * parts["ksum"][..., None]
+        return bar + (2.0 ** -11 * 1.01 + rel + 2 * dq) * parts["mag"] + 2.0 ** -34 * parts["wmax"]
