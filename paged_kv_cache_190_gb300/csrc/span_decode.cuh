@@ -693,8 +693,8 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
         (len < 0 || len > p.max_len || (len > 0 && len < p.q_len)))
       report(p.device_errors, PA_DEVERR_BAD_LENGTH);
     const int nst = make_span<TU>(p, len).nst;
-    st0 = static_cast<int>(static_cast<long long>(nst) * rank / p.splits);
-    cnt = static_cast<int>(static_cast<long long>(nst) * (rank + 1) / p.splits) - st0;
+    st0 = static_cast<int>(static_cast<long long>(nst) * rank >> p.splits_log2);
+    cnt = static_cast<int>(static_cast<long long>(nst) * (rank + 1) >> p.splits_log2) - st0;
   } else {
     // every CTA adds up the stages of all sequences: thread t a run of them
     const int per = (p.num_seqs + kSpanThreads - 1) / kSpanThreads;
@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
     }
     total *= p.ngroups;
     before *= p.ngroups;
-    const long long share = (total + gridDim.x - 1) / gridDim.x;
+    const long long share = share_of(total, gridDim.x);
     const long long begin_at = min(share * blockIdx.x, total);
     cnt = static_cast<int>(min(begin_at + share, total) - begin_at);
     if (cnt > 0 && before <= begin_at && begin_at < before + sum * p.ngroups) {
@@ -1012,7 +1012,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
           }
           if (p.splits > 1) {
             // to the CTA of the cluster that joins this row
-            const int row = hl * p.rows + r, to = row % p.splits, slot = row / p.splits * p.splits + rank;
+            const int row = hl * p.rows + r, to = row & (p.splits - 1), slot = row - to + rank;
             acc.store_peer(peer_addr(smem_addr(joint + slot * D + lane * CPL), to));
             if (lane == 0) peer_store(peer_addr(smem_addr(joint_ml + slot * 2), to), M, lam);
           } else {

@@ -73,7 +73,7 @@ struct SpanParams {
   int hg_log2, ngroups;                           // kv heads of a CTA (log2), CTA head groups
   int block_size, num_blocks, max_blocks, max_len, window, sinks;
   int ring;
-  int splits;                                     // CTAs of a cluster that share a segment; 0: shares
+  int splits, splits_log2;                        // CTAs of a cluster that share a segment; 0: shares
   int joint_slots;                                // clusters: states that a CTA has room for
   float* part_out;                                // shares: [2 CTAs][hg * rows][head_dim]
   float* part_lse;                                // shares: [2 CTAs][hg * rows]

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) span_join_kernel(const Spa
   }
   total *= p.ngroups;
   before *= p.ngroups;
-  const long long share = (total + ctas - 1) / ctas;
+  const long long share = span::share_of(total, ctas);
   const long long at = share * blockIdx.x;                   // where share x begins
   for (int b = s0; b < s1; ++b) {
     const int nst = span::make_span<TU>(p, p.lens[b]).nst;
@@ -279,6 +279,7 @@ cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream) {
     int splits = 1;
     while (splits < kSpanCluster && segs * splits < a.num_sms && 2 * splits <= nst) splits *= 2;
     p.splits = splits;
+    while ((1 << p.splits_log2) < splits) ++p.splits_log2;
     if (splits > 1) {                            // room for the states that a CTA joins
       const int joint = (hg * rows + splits) * (a.head_dim + 2) * 4;
       ring_most = std::min<int>(ring_most, (kSpanSmem - 1024 - fixed.total - joint) / (stage + 160));

@@ -31,5 +31,11 @@ __device__ __forceinline__ Span make_span(const SpanParams& p, int raw_len) {
   return s;
 }
 
+// Stages of a CTA's share, rounded up (a 64-bit division takes a few hundred cycles).
+__device__ __forceinline__ long long share_of(long long total, unsigned ctas) {
+  return (total >> 31) == 0 ? static_cast<long long>((static_cast<unsigned>(total) + ctas - 1) / ctas)
+                            : (total + ctas - 1) / ctas;
+}
+
 }  // namespace span
 }  // namespace pa
