@@ -31,7 +31,8 @@ namespace {
 constexpr int kThreads = 128;
 // Heads that a thread takes of one token, when there are rows enough to fill the GPU.
 // Two: the table row serves two rows, and at 40 registers enough threads are resident to
-// keep HBM busy (16384 tokens of 32 + 8 heads: 64.5 us; four heads at 72 registers 80.1).
+// keep HBM busy (16384 tokens of 32 + 8 heads: 63.3 us, 6.5 TB/s; four heads, at 72
+// registers, 80.1).
 constexpr int kHeadsAtOnce = 2;
 
 // (No load here goes through the read-only path: the kernels start before the one ahead
@@ -297,6 +298,9 @@ __global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const RopeArgs
 constexpr int kLanesPerRow = 8;                            // 128 bf16 columns: 2 chunks a lane
 constexpr int kRowsPerPass = 32 / kLanesPerRow;
 constexpr int kPageThreads = 256;                          // of a block of this kernel
+// Heads of q that a thread takes here, where three blocks are resident for the runs' sake
+// (8190 tokens: 36.2 us; two heads and four blocks 36.8, one head 45.6).
+constexpr int kPageHeadsAtOnce = 4;
 constexpr int kKeptRows = 16;                              // tokens that a block holds at a time
 
 __device__ __forceinline__ float page_scale(float amax) {
@@ -413,11 +417,18 @@ __device__ __forceinline__ void append_run(const RopeArgs& a, const TileTokens& 
       for (int r = sub * kRowsPerPass + row; r < m; r += wph * kRowsPerPass) {
         float x0[N], x1[N];
         values(r, x0, x1);
+        float t = top;                                     // NaN drops out of fmaxf
 #pragma unroll
-        for (int e = 0; e < N; ++e) {                      // infinities and NaN do not count
-          const float y0 = fabsf(x0[e]), y1 = fabsf(x1[e]);
-          top = fmaxf(top, fmaxf(y0 < INFINITY ? y0 : 0.f, y1 < INFINITY ? y1 : 0.f));
+        for (int e = 0; e < N; ++e) t = fmaxf(t, fmaxf(fabsf(x0[e]), fabsf(x1[e])));
+        if (t == INFINITY) {                               // rare: infinities do not count either
+          t = top;
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            t = fmaxf(t, __uint_as_float(finite_bits(x0[e])));
+            t = fmaxf(t, __uint_as_float(finite_bits(x1[e])));
+          }
         }
+        top = t;
       }
   }
   top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
@@ -536,7 +547,7 @@ __device__ __forceinline__ void append_one(const RopeArgs& a, int64_t t, int64_t
 // the longer ones; the tile's `parts` blocks share these out.  Every block looks its
 // tokens up once, into shared memory.  The blocks behind rotate q.
 template <bool INTER, int BS>
-__global__ void __launch_bounds__(kPageThreads, 4) rope_and_cache_page_scale_kernel(
+__global__ void __launch_bounds__(kPageThreads, 3) rope_and_cache_page_scale_kernel(
     const RopeArgs a, int parts, int64_t kv_blocks, int64_t q_groups, int uq) {
   __shared__ TileTokens seen;
   __shared__ float tops[kWarps];
@@ -548,8 +559,8 @@ __global__ void __launch_bounds__(kPageThreads, 4) rope_and_cache_page_scale_ker
     const int64_t g = (kv - kv_blocks) * (kPageThreads / kLanesPerRow) + threadIdx.x / kLanesPerRow;
     if (g >= q_groups) return;
     const int t = static_cast<int>(g / uq);
-    rows_of_token<uint16_t, 128, INTER, false, kHeadsAtOnce>(
-        a, t, kQ, static_cast<int>(g - static_cast<int64_t>(t) * uq) * kHeadsAtOnce, threadIdx.x % kLanesPerRow);
+    rows_of_token<uint16_t, 128, INTER, false, kPageHeadsAtOnce>(
+        a, t, kQ, static_cast<int>(g - static_cast<int64_t>(t) * uq) * kPageHeadsAtOnce, threadIdx.x % kLanesPerRow);
     return;
   }
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -684,7 +695,7 @@ cudaError_t launch_rope_and_cache(const RopeArgs& a, cudaStream_t stream) {
   const int most = (kTile * a.num_kv_heads + kWarps - 1) / kWarps;
   const int parts = static_cast<int>(std::max<int64_t>(2, std::min<int64_t>(most, 512 / tiles)));
   const int64_t kv_blocks = tiles * parts;
-  const int uq = ceil_div(a.num_q_heads, kHeadsAtOnce);
+  const int uq = ceil_div(a.num_q_heads, kPageHeadsAtOnce);
   const int64_t q_groups = static_cast<int64_t>(a.num_tokens) * uq;
   const int64_t q_blocks = (q_groups + kPageThreads / kLanesPerRow - 1) / (kPageThreads / kLanesPerRow);
   if (kv_blocks > 0x3fffffff) return cudaErrorInvalidConfiguration;

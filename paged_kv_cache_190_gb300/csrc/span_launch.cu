@@ -228,23 +228,75 @@ cudaError_t make_map(CUtensorMap* map, const void* pool, SpanPool kind, int head
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Heads that a CTA takes together: the largest power of two up to 8 (e4m3) or 2 that
-// divides them.  Boxes under 8 KiB cost the copy engine more than their bytes: e4m3 pages
-// of 16 tokens, 885 MB, take 144 us with 8 heads a box (16 KiB), 152 with 4, 180 with 2, 213 with 1.
-// bf16 rows are twice as long, and with 2 heads a segment leaves a quarter of the
-// partials: 131.0 us against 132.2 with 8 (833 MB), 49.5 against 52.0 (269 MB, 8 rows a head).
-int most_heads(SpanPool pool, int num_kv_heads) {
-  int hg = pool == SpanPool::kFp8 ? 8 : 2;
+// Heads that a CTA takes together: the largest power of two up to `most` that divides them.
+int heads_together(int num_kv_heads, int most) {
+  int hg = most;
   while (num_kv_heads % hg) hg /= 2;
   return hg;
+}
+
+// In shares, up to 8 (e4m3) or 2.  Boxes under 8 KiB cost the copy engine more than their
+// bytes: e4m3 pages of 16 tokens, 885 MB, take 144 us with 8 heads a box (16 KiB), 152 with
+// 4, 171 with 2, 213 with 1.  bf16 rows are twice as long, and with 2 heads a segment leaves
+// a quarter of the partials: 129.4 us against 132.2 with 8 (833 MB), 49.5 against 52.0
+// (269 MB, 8 rows a head).
+int share_heads(SpanPool pool, int num_kv_heads) {
+  return heads_together(num_kv_heads, pool == SpanPool::kFp8 ? 8 : 2);
+}
+
+// How a call is spread, by what was measured for 1 to 64 sequences of 256 to 4096 tokens
+// (8 kv heads, pages of 16; in 10 ns): a CTA takes its start and so much a stage, more where
+// its boxes are small; joining a cluster's states takes longer the more of them there are;
+// and no stage of all SMs takes less than HBM does.  Shares start later (a pass over the
+// lengths, a second kernel) but spread evenly, while a cluster ends with its sequence: the
+// caller's bound is the longest sequence's, so lengths that no window evens out are taken
+// to be 0.7 of it in the mean.
+struct Spread {
+  int hg = 0, splits = 0;                                    // splits 0: shares
+  int64_t stages = 0, cost = 0;
+};
+Spread choose_spread(SpanPool pool, int64_t num_seqs, int num_kv_heads, int64_t blocks, bool even, int stage_bytes,
+                     int num_sms) {
+  constexpr int kShares = 800;
+  // a stage of every SM at 6.7 TB/s, and what the calls' stages take at that rate
+  const int64_t together = 145ll * stage_bytes / 65536;
+  const int64_t all = (num_seqs * num_kv_heads * blocks + kSpanWarps - 1) / kSpanWarps;
+  const int64_t hbm = together * all / num_sms * (even ? 10 : 7) / 10;
+  Spread best;
+  best.hg = share_heads(pool, num_kv_heads);
+  best.cost = kShares + std::max(hbm, together);
+  const bool fp8 = pool == SpanPool::kFp8;
+  for (int hg = heads_together(num_kv_heads, kSpanWarps); hg >= 1; hg /= 2) {
+    const int64_t segs = num_seqs * (num_kv_heads / hg);
+    const int64_t nst = (blocks + kSpanWarps / hg - 1) / (kSpanWarps / hg);
+    const int start = fp8 ? (hg >= 4 ? 450 : hg == 2 ? 380 : 360) : (hg >= 4 ? 410 : hg == 2 ? 315 : 300);
+    const int full = fp8 ? (hg == 8 ? 106 : hg == 4 ? 109 : hg == 2 ? 130 : 176)
+                         : (hg == 8 ? 63 : hg == 4 ? 67 : hg == 2 ? 79 : 103);
+    const int stage = full * (32768 + stage_bytes) / 98304;  // half a stage (bf16 heads of 64) takes two thirds
+    for (int splits = 1; splits <= kSpanCluster && splits <= nst; splits *= 2) {
+      // the clusters that the GPU's processor clusters hold at once: of 8 CTAs 15 of 19, of
+      // 4 36 of 38
+      const int64_t room = splits == 8 ? num_sms * 3 / 4 : splits == 4 ? num_sms * 9 / 10 : num_sms;
+      if (segs * splits > room) break;
+      const int64_t stages = (nst + splits - 1) / splits;
+      const int64_t cost = start + std::max<int64_t>(stages * stage, hbm) + (splits == 1 ? 0 : hg == 8 ? 150 : 75);
+      if (cost < best.cost) {
+        best.hg = hg;
+        best.splits = splits;
+        best.stages = stages;
+        best.cost = cost;
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
 // Scratch of the shares: two partials for each CTA.
 size_t span_workspace_size(int rows, int num_kv_heads, int head_dim, int num_sms) {
-  const SpanPool pool = SpanPool::kFp8;                      // (enough for every pool)
-  const size_t R = static_cast<size_t>(most_heads(pool, num_kv_heads)) * rows;
+  // (enough for every pool)
+  const size_t R = static_cast<size_t>(share_heads(SpanPool::kFp8, num_kv_heads)) * rows;
   return align256(2 * num_sms * R * 4) + align256(2 * num_sms * R * head_dim * 4);
 }
 
@@ -258,26 +310,22 @@ cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream) {
   p.sinks = a.window > 0 ? std::min(a.sinks, a.max_len) : 0;
   // the longest list of blocks that a sequence can have
   int64_t blocks = (a.max_len + tu - 1) / tu;
+  const int64_t unbound = blocks;
   if (p.window < kNoWindow)
     blocks = std::min<int64_t>(blocks, (p.sinks + tu - 1) / tu + (static_cast<int64_t>(p.window) + a.q_len - 1 + tu - 1) / tu + 1);
   blocks = std::max<int64_t>(blocks, 1);
-  int hg = most_heads(a.pool, a.num_kv_heads);
-  const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
-  const int64_t stages_all = (pairs * blocks + kSpanWarps - 1) / kSpanWarps;
   const SpanSmem fixed = span_smem(a.pool, a.head_dim, rows, 0);
   const int stage = span_stage_bytes(a.pool, a.head_dim);
+  const Spread sp = choose_spread(a.pool, a.num_seqs, a.num_kv_heads, blocks, 2 * blocks < unbound, stage,
+                                  a.num_sms);
+  const int hg = sp.hg;
+  const bool clusters = sp.splits > 0;
   int ring_most = std::min<int>(kSpanRing, (kSpanSmem - 1024 - fixed.total) / (stage + 160));
 
   int grid = 0, ring = ring_most;
   dim3 blocks_of;
-  const bool clusters = stages_all <= 6 * static_cast<int64_t>(a.num_sms);
   if (clusters) {
-    while (hg > 1 && pairs / hg * kSpanCluster < a.num_sms) hg /= 2;
-    const int64_t segs = pairs / hg;
-    const int wph = kSpanWarps / hg;
-    const int64_t nst = (blocks + wph - 1) / wph;
-    int splits = 1;
-    while (splits < kSpanCluster && segs * splits < a.num_sms && 2 * splits <= nst) splits *= 2;
+    const int splits = sp.splits;
     p.splits = splits;
     while ((1 << p.splits_log2) < splits) ++p.splits_log2;
     if (splits > 1) {                            // room for the states that a CTA joins
@@ -286,7 +334,7 @@ cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream) {
     }
     blocks_of = dim3(static_cast<unsigned>(splits), static_cast<unsigned>(a.num_kv_heads / hg),
                      static_cast<unsigned>(a.num_seqs));
-    ring = static_cast<int>(std::min<int64_t>(ring_most, (nst + splits - 1) / splits));
+    ring = static_cast<int>(std::min<int64_t>(ring_most, sp.stages));
   } else {
     grid = a.num_sms;
     blocks_of = dim3(static_cast<unsigned>(grid));

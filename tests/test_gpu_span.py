@@ -91,6 +91,26 @@ def test_large_calls_in_shares(dtype, q_len, hq, hkv, d, bs, window, sinks):
     assert torch.equal(again.view(torch.int16), dv.out.view(torch.int16)), "not the same bits twice"
 
 
+@pytest.mark.parametrize("dtype,q_len,hq,hkv,d,bs", [
+    ("bf16", 1, 8, 8, 128, 16), ("bf16", 4, 6, 3, 64, 32), ("f32", 2, 2, 2, 64, 16), ("f32", 1, 1, 1, 128, 32),
+    ("fp8", 1, 8, 8, 128, 16), ("fp8", 2, 4, 4, 128, 32), ("fp8", 1, 3, 3, 128, 16)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3), (17, 50)])
+def test_more_sequences_than_clusters_fit(dtype, q_len, hq, hkv, d, bs, window, sinks):
+    """More sequences than the GPU has SMs: shares with many short segments each, empty ones
+    among them, cut anywhere."""
+    r = np.random.default_rng(hq + bs)
+    lens = [int(x) for x in r.integers(q_len, 150, 190)] + [0, 0, 700, q_len]
+    r.shuffle(lens)
+    c = Decode(hkv + bs, dtype, lens, q_len, hq, hkv, d, bs, window, sinks, spread=2)
+    dv = Dev(c)
+    dv.call()
+    assert dv.errors() == 0
+    check(c, dv.out)
+    again = torch.empty_like(dv.out)
+    dv.call(again, workspace=torch.full((64 << 20,), 0x7F, dtype=torch.uint8, device=DEV))
+    assert torch.equal(again.view(torch.int16), dv.out.view(torch.int16)), "not the same bits twice"
+
+
 def test_one_long_sequence_over_all_shares():
     c = Decode(3, "fp8", [50000], 1, 8, 8, 128, 16, spread=1)
     dv = Dev(c)
@@ -201,7 +221,8 @@ def test_wide_scores():
 
 
 @pytest.mark.parametrize("dtype,lens", [("bf16", [300, 900]), ("fp8", [300, 900]), ("f32", [300, 900]),
-                                        ("bf16", [3000] * 60), ("fp8", [5000] * 60)])
+                                        ("bf16", [3000] * 60), ("fp8", [5000] * 60), ("bf16", [300] * 170),
+                                        ("fp8", [300] * 170), ("f32", [100] * 170)])
 @pytest.mark.parametrize("polls", [0, 40])
 def test_expired_waits_report_and_leave_the_context_usable(dtype, lens, polls):
     B, hkv, d, bs = len(lens), 8, 128, 16
