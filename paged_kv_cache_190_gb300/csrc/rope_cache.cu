@@ -9,7 +9,11 @@
 // added (no contraction), so the result does not depend on which one a compiler
 // would have fused.
 //
-// All of it is bound by memory: a token's rows are read once and written once.
+// All of it is bound by memory: a token's rows are read once and written once.  On a GB300
+// (6.78 TB/s copied), 32 query and 8 kv heads of 128, bf16: 16384 tokens, 409 MB, in 63.2 us
+// (6.47 TB/s); 256 tokens in 2.3 us, one in 1.7 (the kernel's start); into page-scaled e4m3
+// pools 8190 tokens, 188 MB, in 36.3 us (5.17 TB/s: the conversions of the K and V rows are
+// 20 us of work for the SMs, next to 23 for q's bytes), 256 tokens in 3.5 us.
 // A lane holds the two 16-byte chunks of a row that rotate into each other, and a
 // thread takes the same chunks of several heads of one token, so that the table
 // row (4 bytes per rotated column, twice what a bf16 row is) is loaded once for
@@ -352,8 +356,8 @@ __device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::
 // A run of several tokens: the block takes its rows of up to kHeadsPerItem heads, of K or
 // of V.  The rows and the tokens' table rows come into shared memory all at once, which is
 // what has to overlap; the warps go over them there twice, for the magnitude and for the
-// codes.  (Warp by warp straight from HBM, 4 rows in flight a warp, the same work took
-// 26 us for 8190 tokens of 8 heads; rows kept in registers in between, 25.)  Runs of more
+// codes.  (8190 tokens of 32 + 8 heads: 38 us; warp by warp straight from HBM, with rows kept
+// in registers or read twice, 44 to 54.)  Runs of more
 // than kKeptRows tokens come in pieces, the first of them again for its codes.
 constexpr int kHeadsPerItem = 8;
 constexpr int kWarps = kPageThreads / 32;

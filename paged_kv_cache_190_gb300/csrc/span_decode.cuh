@@ -8,7 +8,12 @@
 // one pass with a running maximum (base 2), float32 throughout.
 //
 // What bounds it: the bytes of K and V.  A token of one kv head is 2 D elements for
-// 4 D flops per query row, a flop or a few per byte.
+// 4 D flops per query row, a flop or a few per byte.  On a GB300 (6.78 TB/s copied): 256
+// windows of 1028 tokens, bf16, 8 kv heads, 833 MB in 130.7 us (6.37 TB/s); 16 windows of
+// 4100 far into contexts of 131072, 8 rows a head, 269 MB in 44.5 us (6.05); e4m3, 256
+// ragged sequences, 885 MB in 143.8 us (6.16), 4 of 131072 tokens, 1.07 GB in 163.0 us
+// (6.59); a few short sequences 3.7 to 6.2 us, of which half is the chain length -> table
+// entry -> page.
 //
 // Layout of the work:
 //   * The tokens that any row sees are cut into blocks of TU tokens (the tile of one
@@ -17,17 +22,17 @@
 //     touched, their table entries are not read.
 //   * A CTA takes hg kv heads (up to 8) of a sequence together.  All heads' rows of a
 //     page stand next to each other in the pool, so one tensor-map box brings a page's
-//     rows of all hg heads (up to 64 KiB where a box of one head's rows has 4): few
-//     copies per byte, which is what a single issuing warp is short of.  Its 8 warps
-//     are the hg heads times 8 / hg blocks of a stage.
+//     rows of all hg heads (16 to 32 KiB where one head's rows are 2 to 4): the copy
+//     engine wants few, large boxes.  Its 8 warps are the hg heads times 8 / hg blocks of
+//     a stage; with 8 heads a warp has a head to itself and nothing to join.
 //   * Two ways to spread (sequence, head group) segments over the GPU.  Shares: one
 //     CTA per SM, every CTA takes an equal run of all segments' stages, found by each
 //     CTA itself from the lengths (no plan kernel, no counters to reset); a segment
 //     that a share's end cuts leaves partials, which a second kernel joins (it finds the
 //     cuts from the lengths too, while this one still runs).
-//     Clusters, for small calls: a segment's stages go to the CTAs of one cluster,
-//     which join their states through distributed shared memory: one launch, no
-//     scratch, half the latency.
+//     Clusters, where all segments fit the GPU at once: a segment's stages go to the CTAs
+//     of one cluster, which join their states through distributed shared memory: one
+//     launch, no scratch, half the latency (span_launch.cu chooses).
 //   * A producer warp keeps a ring of stages full across segments.  Its lanes are the
 //     stage's copies (K and V, block by block); table entries are read three stages
 //     ahead, scales one, so no copy waits for a lookup.
@@ -285,10 +290,10 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 
 // e4m3 codes with a scale for each page and head: codes become halves (exactly, two a
-// conversion) on the way into mma.sync m16n8k16.  The e4m3 form of the instruction does
-// the same conversions inside, of both operands and at every use, and wants q and the
-// weights as sums of two e4m3 parts: 650 instructions a tile against 440 here (256
-// sequences, 885 MB: 161.8 -> 150.4 us).
+// conversion) on the way into mma.sync m16n8k16.  The e4m3 form of the instruction
+// converts both operands inside, at every use, and wants q and the weights as sums of two
+// e4m3 parts: 650 instructions a tile were 550 this way (161.8 -> 161.0 us for 885 MB
+// then), and the weights keep 11 bits instead of 8.
 //   * q: the row scaled by a power of two into [128, 256); a bf16 element is exact as a
 //     half down to 2^-22 of its row's largest.
 //   * The codes of a K row that ldmatrix gives a lane are columns 4 c .. 4 c + 3 of a

@@ -250,7 +250,9 @@ int share_heads(SpanPool pool, int num_kv_heads) {
 // and no stage of all SMs takes less than HBM does.  Shares start later (a pass over the
 // lengths, a second kernel) but spread evenly, while a cluster ends with its sequence: the
 // caller's bound is the longest sequence's, so lengths that no window evens out are taken
-// to be 0.7 of it in the mean.
+// to be 0.7 of it in the mean.  (us, clusters and shares, e4m3: 1 sequence of 256 tokens
+// 5.1 and 7.6, 4 of 1024 6.4 and 10.1, 16 of 2048 14.5 and 18.8, 64 of 2048 to 4096 88 and
+// 72; bf16: 4 of 4096 10.7 and 13.4, 16 windows of 4096 44.4 and 49.5, 64 of 256 9.9 and 14.2.)
 struct Spread {
   int hg = 0, splits = 0;                                    // splits 0: shares
   int64_t stages = 0, cost = 0;
