@@ -262,6 +262,45 @@ def test_refusals_of_the_python_call():
             pa.pa_rope_and_cache(**{**ok, **over})
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8", "fp8_block"])
+def test_prepared_call_given_stream_and_no_tokens(dtype):
+    c = rope_cases.Append(16, dtype, 40, 8, 4, 128, 96, 16, 6, slots=list(range(16, 56)))
+    d = Dev(c)
+    fn = {"fp8": pa.pa_rope_and_cache_fp8, "fp8_block": pa.pa_rope_and_cache_fp8_block}.get(dtype, pa.pa_rope_and_cache)
+    scale = d.scale if dtype.startswith("fp8") else ()
+    call = fn(d.q_out, d.q, d.k, d.v, d.kc, d.vc, d.slots, d.pos, d.table, *scale, device_errors=d.errs, prepare=True)
+    assert isinstance(call, pa.PreparedCall) and bool((d.q_out == -7.0).all())
+    call()
+    assert pa.pa_read_device_errors(d.errs) == 0
+    _check(c, d)
+    side = torch.cuda.Stream()
+    e = Dev(c)
+    side.wait_stream(torch.cuda.current_stream())
+    fn(e.q_out, e.q, e.k, e.v, e.kc, e.vc, e.slots, e.pos, e.table, *(e.scale if scale else ()), device_errors=e.errs,
+       stream=side)
+    side.synchronize()
+    _check(c, e)
+    before = d.kc.clone()
+    fn(d.q_out[:0], d.q[:0], d.k[:0], d.v[:0], d.kc, d.vc, d.slots[:0], d.pos[:0], d.table, *scale)
+    assert torch.equal(before.view(torch.uint8), d.kc.view(torch.uint8))
+
+
+def test_many_decode_tokens_and_mixed_runs():
+    """More tokens than one tile's blocks take at once; runs of one token among longer ones,
+    runs that begin in one tile and end in the next, padding between sequences."""
+    r = np.random.default_rng(17)
+    for bs, hkv in ((16, 5), (32, 9)):
+        spans = [(int(h), int(n)) for h, n in zip(r.integers(0, 60, 500), np.where(r.random(500) < 0.6, 1, r.integers(1, 50, 500)))]
+        slots, pos, nb = _run_of(spans, bs, 3)
+        at = np.cumsum([n for _, n in spans])[::7]                 # a padding token after every seventh sequence
+        slots, pos = list(np.insert(slots, at, -1)), list(np.insert(pos, at, -1))
+        c = rope_cases.Append(18 + bs, "fp8_block", len(slots), 2, hkv, 128, 128, bs, nb, max_position=128,
+                              slots=slots, positions=pos)
+        d = Dev(c)
+        assert d.call() == 0
+        _check(c, d)
+
+
 def test_copy_scales_follows_copied_and_swapped_pages():
     r = torch.Generator(device=DEV).manual_seed(3)
     ks, vs = (torch.rand(7, 3, generator=r, device=DEV) for _ in range(2))

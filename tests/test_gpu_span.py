@@ -111,6 +111,85 @@ def test_more_sequences_than_clusters_fit(dtype, q_len, hq, hkv, d, bs, window, 
     assert torch.equal(again.view(torch.int16), dv.out.view(torch.int16)), "not the same bits twice"
 
 
+@pytest.mark.parametrize("dtype,window", [("bf16", 0), ("bf16", 9), ("fp8", 0), ("f32", 5)])
+def test_thousands_of_short_sequences(dtype, window):
+    """More sequences in a share than a warp's lanes hold lengths of, several for each
+    thread of the pass over them."""
+    r = np.random.default_rng(30)
+    c = Decode(31, dtype, [int(x) for x in r.integers(0, 24, 6001)], 1, 1, 1, 64 if dtype == "bf16" else 128, 16,
+               window, 2 if window else 0, spread=1)
+    dv = Dev(c)
+    dv.call()
+    assert dv.errors() == 0
+    check(c, dv.out)
+
+
+@pytest.mark.parametrize("dtype,q_len,hq,hkv,B,longest", [
+    ("fp8", 1, 32, 8, 12, 900), ("fp8", 2, 32, 8, 30, 300), ("fp8", 1, 8, 8, 100, 200), ("fp8", 8, 8, 8, 5, 2000),
+    ("bf16", 1, 32, 8, 12, 900), ("bf16", 2, 32, 8, 30, 300), ("bf16", 1, 8, 8, 120, 100), ("bf16", 8, 8, 8, 3, 3000),
+    ("f32", 1, 32, 8, 6, 700), ("f32", 8, 8, 8, 40, 60), ("f32", 1, 16, 16, 9, 250)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (120, 5)])
+def test_middling_calls(dtype, q_len, hq, hkv, B, longest, window, sinks):
+    """Between one sequence and a full GPU: clusters of every size and head group."""
+    r = np.random.default_rng(B)
+    lens = [int(x) for x in r.integers(q_len, longest, B - 1)] + [longest]
+    c = Decode(B + q_len, dtype, lens, q_len, hq, hkv, 128, 16, window, sinks, spread=2)
+    dv = Dev(c)
+    dv.call()
+    assert dv.errors() == 0
+    check(c, dv.out)
+
+
+def test_nothing_to_attend_to():
+    c = Decode(32, "bf16", [5, 9], 1, 4, 2, 64, 16)
+    dv = Dev(c)
+    dv.lens.zero_()
+    dv.call(max_context_len=0)
+    assert dv.errors() == 0 and bool((dv.out == 0).all())
+    empty = dv.q[:0]
+    out = pa.pa_decode_window(empty.clone(), empty, dv.kc, dv.vc, dv.tables[:0], dv.lens[:0], 1.0, 2, 9, 4)
+    assert out.shape[0] == 0
+
+
+def test_prepared_calls_and_a_given_stream():
+    for dt in ("bf16", "fp8"):
+        c = Decode(33, dt, [300, 45, 200], 1, 8, 4, 128, 16, window=64, sinks=4)
+        dv = Dev(c)
+        ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+        call = dv.call(workspace=ws, prepare=True)
+        assert isinstance(call, pa.PreparedCall)
+        call()
+        check(c, dv.out)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        again = torch.empty_like(dv.out)
+        dv.call(again, workspace=ws, stream=side)
+        side.synchronize()
+        assert torch.equal(again.view(torch.int16), dv.out.view(torch.int16))
+
+
+def test_two_streams_at_once():
+    """Two large calls in flight together, a workspace each, over and over."""
+    cs = [Decode(34 + i, dt, [int(x) for x in np.random.default_rng(i).integers(1, 400, 180)], 1, 4, 4, 128, 16)
+          for i, dt in enumerate(("bf16", "fp8"))]
+    dvs = [Dev(c) for c in cs]
+    for dv in dvs:
+        dv.call()
+        dv.ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+        dv.side = torch.cuda.Stream()
+        dv.side.wait_stream(torch.cuda.current_stream())
+    want = [dv.out.clone() for dv in dvs]
+    outs = [[torch.empty_like(dv.out) for dv in dvs] for _ in range(20)]
+    torch.cuda.synchronize()
+    for o in outs:
+        for dv, x in zip(dvs, o):
+            dv.call(x, workspace=dv.ws, stream=dv.side)
+    torch.cuda.synchronize()
+    for o in outs:
+        for w, x in zip(want, o):
+            assert torch.equal(w.view(torch.int16), x.view(torch.int16))
+
+
 def test_one_long_sequence_over_all_shares():
     c = Decode(3, "fp8", [50000], 1, 8, 8, 128, 16, spread=1)
     dv = Dev(c)
