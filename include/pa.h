@@ -363,7 +363,7 @@ int pa_decode_window(void* out, const void* q, const void* k_cache, const void* 
  * contiguous, and may be q itself when q is.  num_q_heads 0: q and q_out are not used.
  * cos_sin: device float32, 16-byte aligned.  rot_dim: a multiple of 16 up to head_dim,
  * or 0 for no rotation (then num_q_heads is 0, positions and cos_sin may be null, and
- * every token is live).  slot_mapping and positions are device int64 arrays.
+ * every token is live).  At most 2^31 - 1 rows of q, k and v in all.  slot_mapping and positions are device int64 arrays.
  *
  * pa_rope_and_cache_fp8: the pools hold e4m3 codes with a scale per kv head, as for
  * pa_reshape_and_cache_fp8 (q, k, v bf16, head_dim 128): k' and v are divided by

@@ -18,6 +18,9 @@ int check(const pa::RopeArgs& a, int elt) {
   if (a.rot_dim < 0 || a.rot_dim > a.head_dim || a.rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
   if (a.rot_dim == 0 && a.num_q_heads > 0) return PA_ERR_INVALID_ARG;   // q would only be copied
   if (a.rot_dim > 0 && a.max_position <= 0) return PA_ERR_INVALID_ARG;
+  // groups of lanes: at most one for each row (their numbers are 32-bit in the kernels)
+  if (static_cast<int64_t>(a.num_tokens) * (a.num_q_heads + 2ll * a.num_kv_heads) > INT32_MAX)
+    return PA_ERR_INVALID_ARG;
   if (a.num_tokens == 0) return PA_OK;
   if (!a.k || !a.v || !a.k_cache || !a.v_cache || !a.slots) return PA_ERR_INVALID_ARG;
   if (a.num_q_heads > 0 && (!a.q || !a.q_out)) return PA_ERR_INVALID_ARG;
@@ -69,6 +72,7 @@ pa::RopeArgs args(void* q_out, const void* q, const void* k, const void* v, void
   a.interleaved = interleaved != 0;
   a.max_position = max_position;
   a.block_size = block_size;
+  a.block_log2 = block_size == 32 ? 5 : 4;
   a.num_blocks = num_blocks;
   a.device_errors = device_errors;
   return a;

@@ -25,7 +25,7 @@ struct RopeArgs {
   float* k_scales;             // kFp8Page: [num_blocks][num_kv_heads]
   float* v_scales;
   int num_tokens, num_q_heads, num_kv_heads, head_dim, rot_dim, interleaved;
-  int max_position, block_size, num_blocks;
+  int max_position, block_size, block_log2, num_blocks;
   RopePool pool;
   int32_t* device_errors;
 };

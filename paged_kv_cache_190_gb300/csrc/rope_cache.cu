@@ -10,8 +10,8 @@
 // would have fused.
 //
 // All of it is bound by memory: a token's rows are read once and written once.  On a GB300
-// (6.78 TB/s copied), 32 query and 8 kv heads of 128, bf16: 16384 tokens, 409 MB, in 63.2 us
-// (6.47 TB/s); 256 tokens in 2.3 us, one in 1.7 (the kernel's start); into page-scaled e4m3
+// (6.78 TB/s copied), 32 query and 8 kv heads of 128, bf16: 16384 tokens, 409 MB, in 61.6 us
+// (6.64 TB/s); 256 tokens in 2.3 us, one in 1.7 (the kernel's start); into page-scaled e4m3
 // pools 8190 tokens, 188 MB, in 36.3 us (5.17 TB/s: the conversions of the K and V rows are
 // 20 us of work for the SMs, next to 23 for q's bytes), 256 tokens in 3.5 us.
 // A lane holds the two 16-byte chunks of a row that rotate into each other, and a
@@ -34,9 +34,8 @@ namespace {
 
 constexpr int kThreads = 128;
 // Heads that a thread takes of one token, when there are rows enough to fill the GPU.
-// Two: the table row serves two rows, and at 40 registers enough threads are resident to
-// keep HBM busy (16384 tokens of 32 + 8 heads: 63.3 us, 6.5 TB/s; four heads, at 72
-// registers, 80.1).
+// Two: the table row serves two rows, and enough threads are resident to keep HBM busy
+// (16384 tokens of 32 + 8 heads: 61.6 us; one head 73.6, four heads 64.6).
 constexpr int kHeadsAtOnce = 2;
 
 // (No load here goes through the read-only path: the kernels start before the one ahead
@@ -228,8 +227,8 @@ __device__ __forceinline__ void rows_of_token(const RopeArgs& a, int t, Kind kin
   Angles<N, D, INTER> an;
   const bool turned = kind != kV && a.rot_dim > 0;
   if (turned) an.load(a.cos_sin + p.pos * a.rot_dim, a.rot_dim / 2, lc);
-  const int64_t page = p.slot / a.block_size;
-  const int64_t off = p.slot - page * a.block_size;
+  const int64_t page = p.slot >> a.block_log2;
+  const int off = static_cast<int>(p.slot) & (a.block_size - 1);
 #pragma unroll
   for (int j = 0; j < HPT; ++j) {
     if (HPT > 1 && h0 + j >= heads) break;
@@ -269,16 +268,15 @@ __device__ __forceinline__ void rows_of_token(const RopeArgs& a, int t, Kind kin
 
 // A group of D / (2 N) lanes takes HPT heads of one token and kind.
 template <typename E, int D, bool INTER, bool FP8, int HPT>
-__global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const RopeArgs a, int64_t groups,
+__global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const RopeArgs a, unsigned groups,
                                                                   int uq, int uk) {
   wait_prior_grids();
   allow_next_grid();
   constexpr int LPR = D / Vec<E>::N / 2;
-  const int64_t g = static_cast<int64_t>(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR;
+  const unsigned g = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;   // under 2^31
   if (g >= groups) return;
-  const int units = uq + 2 * uk;
-  const int t = static_cast<int>(g / units);
-  const int u = static_cast<int>(g - static_cast<int64_t>(t) * units);
+  const unsigned units = uq + 2 * uk;
+  const int t = g / units, u = g - t * units;
   const int l = threadIdx.x % LPR;
   if (u < uq)
     rows_of_token<E, D, INTER, FP8, HPT>(a, t, kQ, u * HPT, l);
@@ -356,9 +354,9 @@ __device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::
 // A run of several tokens: the block takes its rows of up to kHeadsPerItem heads, of K or
 // of V.  The rows and the tokens' table rows come into shared memory all at once, which is
 // what has to overlap; the warps go over them there twice, for the magnitude and for the
-// codes.  (8190 tokens of 32 + 8 heads: 38 us; warp by warp straight from HBM, with rows kept
-// in registers or read twice, 44 to 54.)  Runs of more
-// than kKeptRows tokens come in pieces, the first of them again for its codes.
+// codes.  (8190 tokens of 32 + 8 heads: 38 us; warp by warp straight from HBM, with rows
+// kept in registers or read twice, 44 to 54.)  Runs of more than kKeptRows tokens come in
+// pieces, the first of them again for its codes.
 constexpr int kHeadsPerItem = 8;
 constexpr int kWarps = kPageThreads / 32;
 constexpr int kRunBytes = kKeptRows * (kHeadsPerItem * 256 + 128 * 4);
@@ -552,23 +550,23 @@ __device__ __forceinline__ void append_one(const RopeArgs& a, int64_t t, int64_t
 // tokens up once, into shared memory.  The blocks behind rotate q.
 template <bool INTER, int BS>
 __global__ void __launch_bounds__(kPageThreads, 3) rope_and_cache_page_scale_kernel(
-    const RopeArgs a, int parts, int64_t kv_blocks, int64_t q_groups, int uq) {
+    const RopeArgs a, unsigned parts, unsigned kv_blocks, unsigned q_groups, unsigned uq) {
   __shared__ TileTokens seen;
   __shared__ float tops[kWarps];
   extern __shared__ __align__(16) unsigned char run_buf[];
   wait_prior_grids();
   allow_next_grid();
-  const int64_t kv = blockIdx.x;
+  const unsigned kv = blockIdx.x;
   if (kv >= kv_blocks) {
-    const int64_t g = (kv - kv_blocks) * (kPageThreads / kLanesPerRow) + threadIdx.x / kLanesPerRow;
+    const unsigned g = (kv - kv_blocks) * (kPageThreads / kLanesPerRow) + threadIdx.x / kLanesPerRow;
     if (g >= q_groups) return;
-    const int t = static_cast<int>(g / uq);
-    rows_of_token<uint16_t, 128, INTER, false, kPageHeadsAtOnce>(
-        a, t, kQ, static_cast<int>(g - static_cast<int64_t>(t) * uq) * kPageHeadsAtOnce, threadIdx.x % kLanesPerRow);
+    const unsigned t = g / uq;
+    rows_of_token<uint16_t, 128, INTER, false, kPageHeadsAtOnce>(a, t, kQ, (g - t * uq) * kPageHeadsAtOnce,
+                                                                 threadIdx.x % kLanesPerRow);
     return;
   }
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int tile = static_cast<int>(kv / parts), part = static_cast<int>(kv - static_cast<int64_t>(tile) * parts);
+  const int tile = kv / parts, part = kv - tile * parts;
   const int t0 = tile * kTile;
   if (threadIdx.x < 64) {
     const int i = threadIdx.x;
@@ -666,12 +664,17 @@ cudaError_t launch(void (*kernel)(P...), int64_t blocks, int threads, int smem, 
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// Groups of lanes that a launch may have (their numbers are 32-bit: a 64-bit division each
+// costs as much as a head's rotation).
+constexpr int64_t kMostGroups = int64_t{1} << 31;
+
 template <typename E, int D, bool FP8>
 cudaError_t run_rope(const RopeArgs& a, cudaStream_t stream) {
   constexpr int per_block = kThreads / (D / Vec<E>::N / 2);
   auto go = [&](auto kernel, int hpt) {
     const int uq = ceil_div(a.num_q_heads, hpt), uk = ceil_div(a.num_kv_heads, hpt);
     const int64_t groups = static_cast<int64_t>(a.num_tokens) * (uq + 2 * uk);
+    if (groups >= kMostGroups) return cudaErrorInvalidValue;
     return launch(kernel, (groups + per_block - 1) / per_block, kThreads, 0, stream, a, groups, uq, uk);
   };
   // one head a thread while the rows are too few to fill the GPU
@@ -702,7 +705,7 @@ cudaError_t launch_rope_and_cache(const RopeArgs& a, cudaStream_t stream) {
   const int uq = ceil_div(a.num_q_heads, kPageHeadsAtOnce);
   const int64_t q_groups = static_cast<int64_t>(a.num_tokens) * uq;
   const int64_t q_blocks = (q_groups + kPageThreads / kLanesPerRow - 1) / (kPageThreads / kLanesPerRow);
-  if (kv_blocks > 0x3fffffff) return cudaErrorInvalidConfiguration;
+  if (kv_blocks >= kMostGroups / 2 || q_groups >= kMostGroups) return cudaErrorInvalidValue;
   auto go = [&](auto kernel) {
     return launch(kernel, kv_blocks + q_blocks, kPageThreads, kRunBytes, stream, a, parts, kv_blocks, q_groups, uq);
   };

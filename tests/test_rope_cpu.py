@@ -86,7 +86,7 @@ ALL = ["pa_rope_and_cache", "pa_rope_and_cache_fp8", "pa_rope_and_cache_fp8_bloc
 
 @pytest.mark.parametrize("fn", ALL)
 @pytest.mark.parametrize("over,status", [
-    (dict(t=0), 0), (dict(t=-1), -1), (dict(hkv=0), -1), (dict(hq=-1), -1), (dict(nb=0), -1),
+    (dict(t=0), 0), (dict(t=-1), -1), (dict(t=2 ** 26), -1), (dict(hkv=0), -1), (dict(hq=-1), -1), (dict(nb=0), -1),
     (dict(d=96), -2), (dict(bs=8), -2), (dict(rot=24), -2), (dict(rot=144), -2), (dict(rot=-16), -2),
     (dict(rot=0), -1),                              # q without a rotation
     (dict(most=0), -1), (dict(q=None), -1), (dict(q_out=None), -1), (dict(k=None), -1),
