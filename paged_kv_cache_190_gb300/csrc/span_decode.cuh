@@ -165,7 +165,7 @@ struct Bf16Rows {
   float m, l;
   int lane, rows;
 
-  __device__ __forceinline__ void init(const SpanParams& p, int lane_, float*) {
+  __device__ __forceinline__ void init(const SpanParams& p, int lane_, float*, float*) {
     lane = lane_;
     rows = p.rows;
   }
@@ -313,7 +313,7 @@ struct Fp8Rows {
   float m, l, mo, qinv;
   int lane, rows;
 
-  __device__ __forceinline__ void init(const SpanParams& p, int lane_, float*) {
+  __device__ __forceinline__ void init(const SpanParams& p, int lane_, float*, float*) {
     lane = lane_;
     rows = p.rows;
   }
@@ -470,34 +470,72 @@ struct Fp8Rows {
   }
 };
 
-// float32 on the CUDA cores: 8 lanes a token for the scores, each lane D / 32 columns of
-// every row for the values (CoreConsumer's arithmetic, with the window's test).
+// float32 on the CUDA cores.  Scores: 8 lanes a token, 4 tokens a pass, a lane head_dim / 8
+// columns of every row; the butterfly leaves a lane the scores of one row (g_lane), whose
+// maximum and sum it keeps.  Values: a lane head_dim / 32 columns of every row.  (One
+// maximum a lane, sent round by shuffles, not one of every row and a choice among them:
+// the compiler makes that choice an address, and the whole state then lives in local
+// memory: 64 sequences of 2000 tokens, 8 kv heads of 8 rows of 128, 221 us.)
+// q's rows are in registers; 8 rows of 128 would take 128 of them and stand in the warp's
+// shared memory.
 template <int D, int G>
-struct F32Rows : CoreConsumer<DecodeTraits<false, D, G>> {
+struct F32Rows {
   using Tr = DecodeTraits<false, D, G>;
-  using Base = CoreConsumer<Tr>;
-  static constexpr int TU = Tr::UT;
-  __device__ __forceinline__ void init(const SpanParams&, int lane_, float* ps_) { Base::init(lane_, ps_); }
-  __device__ __forceinline__ int row() const { return this->g_lane; }
+  static constexpr int TU = Tr::UT, NCH = Tr::NCH, EPL = Tr::EPL, CPL = Tr::CPL, NP = Tr::P;
+  static constexpr bool kShared = span_q_shared(SpanPool::kF32, D, G);
+  static constexpr int LANES = 8 / G;   // lanes of 8 that hold a row's scores
+  float qf[kShared ? 1 : G][EPL];
+  float acc[G][CPL];
+  float m, lsum;                        // of row g_lane: its maximum, this lane's share of its sum
+  int lane, j4, r, base, g_lane;
+  float* ps;                            // this warp's probabilities [TU][G]
+  float4* qs;                           // this warp's rows of q [G][D / 4]
+
+  __device__ __forceinline__ void init(const SpanParams&, int lane_, float* ps_, float* qs_) {
+    lane = lane_;
+    j4 = lane >> 3;
+    r = lane & 7;
+    // the sums that the butterfly leaves here: base .. base + RC - 1 of [row][pass]
+    base = ((r >> 2) & 1) * (Tr::N / 2) + (Tr::N >= 4 ? ((r >> 1) & 1) * (Tr::N / 4) : 0) +
+           (Tr::N >= 8 ? (r & 1) * (Tr::N / 8) : 0);
+    g_lane = base / NP;
+    ps = ps_;
+    qs = reinterpret_cast<float4*>(qs_);
+  }
+  __device__ __forceinline__ int row() const { return g_lane; }
 
   __device__ __forceinline__ void load(const SpanParams& p, int b, int head) {
+    if constexpr (kShared) __syncwarp();                    // (the last segment's reads are done)
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + query_row(p, b, head, g) * (4 * D));
+      const float4* src = reinterpret_cast<const float4*>(p.q + query_row(p, b, head, g) * (4 * D));
+      if constexpr (kShared) {
+        static_assert(!kShared || D == 128, "a chunk a lane");
+        const float4 w = src[lane];
+        qs[g * (D / 4) + lane] = make_float4(w.x * p.scale_log2, w.y * p.scale_log2, w.z * p.scale_log2,
+                                             w.w * p.scale_log2);
+      } else {
 #pragma unroll
-      for (int c = 0; c < Tr::NCH; ++c) unpack_chunk<Tr>(src[this->r + 8 * c], &this->qf[g][c * 4]);
+        for (int c = 0; c < NCH; ++c) {
+          const float4 w = src[r + 8 * c];
+          qf[g][4 * c] = w.x; qf[g][4 * c + 1] = w.y; qf[g][4 * c + 2] = w.z; qf[g][4 * c + 3] = w.w;
+        }
+      }
     }
   }
   __device__ __forceinline__ void begin(const SpanParams& p) {
+    if constexpr (kShared) __syncwarp();
 #pragma unroll
     for (int g = 0; g < G; ++g) {
+      if constexpr (!kShared) {
 #pragma unroll
-      for (int e = 0; e < Tr::EPL; ++e) this->qf[g][e] *= p.scale_log2;
-      this->m[g] = kNoScore;
+        for (int e = 0; e < EPL; ++e) qf[g][e] *= p.scale_log2;
+      }
 #pragma unroll
-      for (int c = 0; c < Tr::CPL; ++c) this->acc[g][c] = 0.f;
+      for (int c = 0; c < CPL; ++c) acc[g][c] = 0.f;
     }
-    this->lsum = 0.f;
+    m = kNoScore;
+    lsum = 0.f;
   }
 
   template <typename Release>
@@ -505,23 +543,32 @@ struct F32Rows : CoreConsumer<DecodeTraits<false, D, G>> {
                                        const float2*, int, Release release) {
     const char* kt = static_cast<const char*>(__cvta_shared_to_generic(kb));
     const char* vt = static_cast<const char*>(__cvta_shared_to_generic(vb));
-    const int base = this->base, j4 = this->j4, g_lane = this->g_lane, lane = this->lane;
-    float* ps = this->ps;
-    float part[Tr::N];
+    float part[Tr::N], kf[NP][EPL];
 #pragma unroll
-    for (int pi = 0; pi < Tr::P; ++pi) {
-      const int t = 4 * pi + j4;
-      float kf[Tr::EPL];
+    for (int pi = 0; pi < NP; ++pi)
 #pragma unroll
-      for (int c = 0; c < Tr::NCH; ++c)
-        unpack_chunk<Tr>(*reinterpret_cast<const uint4*>(kt + t * Tr::ROW_BYTES + (this->r + 8 * c) * 16),
-                         &kf[c * Tr::CE]);
+      for (int c = 0; c < NCH; ++c)
+        unpack_chunk<Tr>(*reinterpret_cast<const uint4*>(kt + (4 * pi + j4) * Tr::ROW_BYTES + (r + 8 * c) * 16),
+                         &kf[pi][c * Tr::CE]);
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
+    for (int g = 0; g < G; ++g) {
+      float q[EPL];
+      if constexpr (kShared) {
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+          const float4 w = qs[g * (D / 4) + r + 8 * c];
+          q[4 * c] = w.x; q[4 * c + 1] = w.y; q[4 * c + 2] = w.z; q[4 * c + 3] = w.w;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) q[e] = qf[g][e];
+      }
+#pragma unroll
+      for (int pi = 0; pi < NP; ++pi) {
         float dot = 0.f;
 #pragma unroll
-        for (int e = 0; e < Tr::EPL; ++e) dot = fmaf(this->qf[g][e], kf[e], dot);
-        part[g * Tr::P + pi] = dot;
+        for (int e = 0; e < EPL; ++e) dot = fmaf(q[e], kf[pi][e], dot);
+        part[g * NP + pi] = dot;
       }
     }
     butterfly_level<Tr::N>(part, lane, 4);
@@ -530,55 +577,73 @@ struct F32Rows : CoreConsumer<DecodeTraits<false, D, G>> {
     float umax = -INFINITY;
 #pragma unroll
     for (int e = 0; e < Tr::RC; ++e) {
-      const int t = 4 * ((base % Tr::P) + e) + j4;
+      const int t = 4 * ((base % NP) + e) + j4;
       if (!see.all && !see.sees(t)) part[e] = -INFINITY;
       umax = fmaxf(umax, part[e]);
     }
 #pragma unroll
-    for (int mask = 1; mask < 8 / G; mask <<= 1) umax = fmaxf(umax, __shfl_xor_sync(kFull, umax, mask));
+    for (int mask = 1; mask < LANES; mask <<= 1) umax = fmaxf(umax, __shfl_xor_sync(kFull, umax, mask));
     umax = fmaxf(umax, __shfl_xor_sync(kFull, umax, 8));
     umax = fmaxf(umax, __shfl_xor_sync(kFull, umax, 16));
-    float alpha[G];
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const float mu = __shfl_sync(kFull, umax, g * (8 / G));
-      const float mn = fmaxf(this->m[g], mu);
-      alpha[g] = fast_exp2(this->m[g] - mn);
-      this->m[g] = mn;
-    }
-    float m_lane = this->m[0], a_lane = alpha[0];
-#pragma unroll
-    for (int g = 1; g < G; ++g)
-      if (g_lane == g) {
-        m_lane = this->m[g];
-        a_lane = alpha[g];
-      }
+    const float mn = fmaxf(m, umax);
+    const float alpha = fast_exp2(m - mn);
+    m = mn;
     float psum = 0.f;
 #pragma unroll
     for (int e = 0; e < Tr::RC; ++e) {
-      const int t = 4 * ((base % Tr::P) + e) + j4;
-      const float pr = fast_exp2(part[e] - m_lane);
+      const int t = 4 * ((base % NP) + e) + j4;
+      const float pr = fast_exp2(part[e] - mn);
       psum += pr;
       ps[t * G + g_lane] = pr;                              // lanes with the same sum store the same value
     }
-    this->lsum = this->lsum * a_lane + psum;
+    lsum = lsum * alpha + psum;
 #pragma unroll
-    for (int g = 0; g < G; ++g)
+    for (int g = 0; g < G; ++g) {
+      const float f = __shfl_sync(kFull, alpha, g * LANES);
 #pragma unroll
-      for (int c = 0; c < Tr::CPL; ++c) this->acc[g][c] *= alpha[g];
+      for (int c = 0; c < CPL; ++c) acc[g][c] *= f;
+    }
     __syncwarp();
 #pragma unroll
     for (int t = 0; t < TU; ++t) {
-      float vv[Tr::CPL];
+      float vv[CPL], w[G];
       load_v_cols<Tr>(vt, t, lane, vv);
+      if constexpr (G >= 4) {
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const float w = ps[t * G + g];
+        for (int g = 0; g < G; g += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(ps + t * G + g);
+          w[g] = x.x; w[g + 1] = x.y; w[g + 2] = x.z; w[g + 3] = x.w;
+        }
+      } else {
 #pragma unroll
-        for (int c = 0; c < Tr::CPL; ++c) this->acc[g][c] = fmaf(w, vv[c], this->acc[g][c]);
+        for (int g = 0; g < G; ++g) w[g] = ps[t * G + g];
       }
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) acc[g][c] = fmaf(w[g], vv[c], acc[g][c]);
     }
     release();
+  }
+
+  // to macc [G][D] and ml [G][(maximum, sum)]
+  __device__ __forceinline__ void store(float* macc, float* ml) {
+#pragma unroll
+    for (int mask = Tr::DUP_MASK_END; mask < LANES; mask <<= 1) lsum += __shfl_xor_sync(kFull, lsum, mask);
+    lsum += __shfl_xor_sync(kFull, lsum, 8);
+    lsum += __shfl_xor_sync(kFull, lsum, 16);
+    if (j4 == 0 && (r % LANES) == 0) {
+      ml[g_lane * 2] = m;
+      ml[g_lane * 2 + 1] = lsum;
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float* dst = macc + g * D + lane * CPL;
+      if constexpr (CPL == 4)
+        *reinterpret_cast<float4*>(dst) = make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]);
+      else
+        *reinterpret_cast<float2*>(dst) = make_float2(acc[g][0], acc[g][1]);
+    }
   }
 };
 
@@ -880,7 +945,8 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
     const int half = parts > 1 ? op_bytes : 16 * ROW;        // bytes between 16-token halves (fp8)
     const uint32_t tile_off = sub * parts * op_bytes + hl * t_op * (ROW / SLABS);
     Rows rows;
-    rows.init(p, lane, reinterpret_cast<float*>(smem + at.ps) + warp * TU * p.rows);
+    rows.init(p, lane, reinterpret_cast<float*>(smem + at.ps) + warp * TU * p.rows,
+              reinterpret_cast<float*>(smem + at.qs) + warp * p.rows * D);
     Walk<TU> wk(p, b0, grp0, len0);
     int s = 0, left = cnt, st = st0;
     uint32_t parity = 0;

@@ -32,9 +32,15 @@ __host__ __device__ constexpr int span_stage_bytes(SpanPool pool, int head_dim) 
   return 2 * kSpanWarps * span_tile_tokens(pool, head_dim) * span_row_bytes(pool, head_dim);
 }
 
+// float32: with this many query rows a head's q does not fit the registers (a lane would
+// hold rows * head_dim / 8 floats of it).
+__host__ __device__ constexpr bool span_q_shared(SpanPool pool, int head_dim, int rows) {
+  return pool == SpanPool::kF32 && rows * head_dim / 8 > 64;
+}
+
 // Byte offsets of a CTA's shared memory behind its ring of stages.
 struct SpanSmem {
-  int macc, ml, sc, meta, ps, scan, bars, flag, total;
+  int macc, ml, sc, meta, ps, qs, scan, bars, flag, total;
 };
 __host__ __device__ constexpr SpanSmem span_smem(SpanPool pool, int head_dim, int rows, int ring) {
   SpanSmem s{};
@@ -47,9 +53,12 @@ __host__ __device__ constexpr SpanSmem span_smem(SpanPool pool, int head_dim, in
   off += pool == SpanPool::kFp8 ? ring * 32 * 4 : 0;
   s.meta = off;
   off += ring * 4;
+  off = (off + 15) / 16 * 16;
   s.ps = off;
   off += pool == SpanPool::kF32 ? kSpanWarps * span_tile_tokens(pool, head_dim) * rows * 4 : 0;
-  off = (off + 7) / 8 * 8;
+  off = (off + 15) / 16 * 16;
+  s.qs = off;
+  off += span_q_shared(pool, head_dim, rows) ? kSpanWarps * rows * head_dim * 4 : 0;
   s.scan = off;
   off += 16 * 8;
   s.bars = off;

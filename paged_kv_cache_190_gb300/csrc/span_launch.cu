@@ -244,6 +244,16 @@ int share_heads(SpanPool pool, int num_kv_heads) {
   return heads_together(num_kv_heads, pool == SpanPool::kFp8 ? 8 : 2);
 }
 
+// Room for the states that a CTA of a cluster joins.
+int joint_bytes(int head_dim, int rows, int hg, int splits) {
+  return splits > 1 ? (hg * rows + splits) * (head_dim + 2) * 4 : 0;
+}
+// Stages that the shared memory has room for.
+int ring_stages(SpanPool pool, int head_dim, int rows, int hg, int splits) {
+  const int room = kSpanSmem - 1024 - span_smem(pool, head_dim, rows, 0).total - joint_bytes(head_dim, rows, hg, splits);
+  return std::min<int>(kSpanRing, room / (span_stage_bytes(pool, head_dim) + 160));
+}
+
 // How a call is spread, by what was measured for 1 to 64 sequences of 256 to 4096 tokens
 // (8 kv heads, pages of 16; in 10 ns): a CTA takes its start and so much a stage, more where
 // its boxes are small; joining a cluster's states takes longer the more of them there are;
@@ -253,12 +263,16 @@ int share_heads(SpanPool pool, int num_kv_heads) {
 // to be 0.7 of it in the mean.  (us, clusters and shares, e4m3: 1 sequence of 256 tokens
 // 5.1 and 7.6, 4 of 1024 6.4 and 10.1, 16 of 2048 14.5 and 18.8, 64 of 2048 to 4096 88 and
 // 72; bf16: 4 of 4096 10.7 and 13.4, 16 windows of 4096 44.4 and 49.5, 64 of 256 9.9 and 14.2.)
+// float32 rows are computed one by one: with 1, 4 and 8 of them a stage takes 0.93, 1.13 and
+// 1.50 us (one head a CTA), 0.66, 0.87 and 1.35 (8 heads).  Nothing is chosen that leaves the
+// ring a single stage (8 such heads of 8 rows in clusters: 130 us, where 2 stages take 90).
 struct Spread {
   int hg = 0, splits = 0;                                    // splits 0: shares
   int64_t stages = 0, cost = 0;
 };
-Spread choose_spread(SpanPool pool, int64_t num_seqs, int num_kv_heads, int64_t blocks, bool even, int stage_bytes,
-                     int num_sms) {
+Spread choose_spread(SpanPool pool, int head_dim, int rows, int64_t num_seqs, int num_kv_heads, int64_t blocks,
+                     bool even, int num_sms) {
+  const int stage_bytes = span_stage_bytes(pool, head_dim);
   constexpr int kShares = 800;
   // a stage of every SM at 6.7 TB/s, and what the calls' stages take at that rate
   const int64_t together = 145ll * stage_bytes / 65536;
@@ -266,20 +280,24 @@ Spread choose_spread(SpanPool pool, int64_t num_seqs, int num_kv_heads, int64_t 
   const int64_t hbm = together * all / num_sms * (even ? 10 : 7) / 10;
   Spread best;
   best.hg = share_heads(pool, num_kv_heads);
-  best.cost = kShares + std::max(hbm, together);
   const bool fp8 = pool == SpanPool::kFp8;
+  const auto stage_cost = [&](int hg) {
+    const int full = fp8 ? (hg == 8 ? 106 : hg == 4 ? 109 : hg == 2 ? 130 : 176)
+                         : (hg == 8 ? 63 : hg == 4 ? 67 : hg == 2 ? 79 : 103);
+    const int stage = full * (32768 + stage_bytes) / 98304;  // half a stage (bf16 heads of 64) takes two thirds
+    return pool == SpanPool::kF32 ? stage + 7 * (rows - 1) : stage;
+  };
+  best.cost = kShares + std::max({hbm, together, (all + num_sms - 1) / num_sms * stage_cost(best.hg)});
   for (int hg = heads_together(num_kv_heads, kSpanWarps); hg >= 1; hg /= 2) {
     const int64_t segs = num_seqs * (num_kv_heads / hg);
     const int64_t nst = (blocks + kSpanWarps / hg - 1) / (kSpanWarps / hg);
     const int start = fp8 ? (hg >= 4 ? 450 : hg == 2 ? 380 : 360) : (hg >= 4 ? 410 : hg == 2 ? 315 : 300);
-    const int full = fp8 ? (hg == 8 ? 106 : hg == 4 ? 109 : hg == 2 ? 130 : 176)
-                         : (hg == 8 ? 63 : hg == 4 ? 67 : hg == 2 ? 79 : 103);
-    const int stage = full * (32768 + stage_bytes) / 98304;  // half a stage (bf16 heads of 64) takes two thirds
+    const int stage = stage_cost(hg);
     for (int splits = 1; splits <= kSpanCluster && splits <= nst; splits *= 2) {
       // the clusters that the GPU's processor clusters hold at once: of 8 CTAs 15 of 19, of
       // 4 36 of 38
       const int64_t room = splits == 8 ? num_sms * 3 / 4 : splits == 4 ? num_sms * 9 / 10 : num_sms;
-      if (segs * splits > room) break;
+      if (segs * splits > room || ring_stages(pool, head_dim, rows, hg, splits) < 2) break;
       const int64_t stages = (nst + splits - 1) / splits;
       const int64_t cost = start + std::max<int64_t>(stages * stage, hbm) + (splits == 1 ? 0 : hg == 8 ? 150 : 75);
       if (cost < best.cost) {
@@ -316,13 +334,11 @@ cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream) {
   if (p.window < kNoWindow)
     blocks = std::min<int64_t>(blocks, (p.sinks + tu - 1) / tu + (static_cast<int64_t>(p.window) + a.q_len - 1 + tu - 1) / tu + 1);
   blocks = std::max<int64_t>(blocks, 1);
-  const SpanSmem fixed = span_smem(a.pool, a.head_dim, rows, 0);
-  const int stage = span_stage_bytes(a.pool, a.head_dim);
-  const Spread sp = choose_spread(a.pool, a.num_seqs, a.num_kv_heads, blocks, 2 * blocks < unbound, stage,
-                                  a.num_sms);
+  const Spread sp = choose_spread(a.pool, a.head_dim, rows, a.num_seqs, a.num_kv_heads, blocks,
+                                  2 * blocks < unbound, a.num_sms);
   const int hg = sp.hg;
   const bool clusters = sp.splits > 0;
-  int ring_most = std::min<int>(kSpanRing, (kSpanSmem - 1024 - fixed.total) / (stage + 160));
+  const int ring_most = ring_stages(a.pool, a.head_dim, rows, hg, sp.splits);
 
   int grid = 0, ring = ring_most;
   dim3 blocks_of;
@@ -330,10 +346,6 @@ cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream) {
     const int splits = sp.splits;
     p.splits = splits;
     while ((1 << p.splits_log2) < splits) ++p.splits_log2;
-    if (splits > 1) {                            // room for the states that a CTA joins
-      const int joint = (hg * rows + splits) * (a.head_dim + 2) * 4;
-      ring_most = std::min<int>(ring_most, (kSpanSmem - 1024 - fixed.total - joint) / (stage + 160));
-    }
     blocks_of = dim3(static_cast<unsigned>(splits), static_cast<unsigned>(a.num_kv_heads / hg),
                      static_cast<unsigned>(a.num_seqs));
     ring = static_cast<int>(std::min<int64_t>(ring_most, sp.stages));
