@@ -316,8 +316,8 @@ int pa_decode_fp8(void* out, const void* q, const void* k_cache, const void* v_c
  * the visible tokens: table entries of pages of which no new token sees a position are
  * not read (the pages may have been given back), and what stands in positions that none
  * sees does not matter, NaN and infinities included.  (A NaN or infinity in the V row of
- * a position that some new token of the sequence sees reaches every row of that kv head
- * in bf16 and e4m3 pools, as in pa_decode_multi.)
+ * a position that some new token of the sequence sees reaches the rows of that kv head
+ * that do not see it too, as a product with the weight 0.)
  *
  * q and out are [num_seqs][q_len][num_q_heads][head_dim] ([num_seqs][num_q_heads]
  * [head_dim] for q_len 1) in the pools' type, PA_F32 or PA_BF16;

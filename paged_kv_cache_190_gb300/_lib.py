@@ -603,8 +603,11 @@ def pa_decode_window_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_di
 def _span_decode(name, fp8, out, q, k_cache, v_cache, block_tables, context_lens, scale, k_scales,
                  v_scales, num_kv_heads, max_context_len, window, sinks, workspace, device_errors,
                  stream, prepare):
-    if workspace is None:
+    own = workspace is None
+    if own:
         import torch
+        if prepare:
+            raise ValueError("a prepared call needs a workspace that outlives it")
         if not q.is_cuda:
             raise ValueError("q must be a contiguous CUDA tensor")
         rows = q.shape[-2] * (q.shape[1] if q.dim() == 4 else 1)
@@ -618,6 +621,8 @@ def _span_decode(name, fp8, out, q, k_cache, v_cache, block_tables, context_lens
         num_kv_heads, max_context_len, window, sinks, workspace, device_errors, stream, prepare)
     if prepare:
         return PreparedCall(name, rc)
+    if own and stream is not None:
+        workspace.record_stream(stream)     # not given out again before the call there is done
     if rc:
         _check(rc, name)
     return out
@@ -630,7 +635,8 @@ def pa_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, scale
     none): out, q [B, Hq, D], or [B, q_len, Hq, D] for q_len new tokens per sequence;
     caches [NB, Hkv, bs, D] of their type; block_tables int32 [B, max_blocks];
     context_lens int32 [B] (see pa.h).  ``workspace``: a uint8 CUDA tensor of at least
-    pa_decode_window_workspace_size() bytes; allocated here when None."""
+    pa_decode_window_workspace_size() bytes; allocated here when None (not for a prepared
+    call, which would outlive it)."""
     return _span_decode("pa_decode_window", False, out, q, k_cache, v_cache, block_tables,
                         context_lens, scale, None, None, num_kv_heads, max_context_len, window,
                         sinks, workspace, device_errors, stream, prepare)

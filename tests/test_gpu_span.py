@@ -168,6 +168,28 @@ def test_prepared_calls_and_a_given_stream():
         assert torch.equal(again.view(torch.int16), dv.out.view(torch.int16))
 
 
+def test_its_own_workspace_outlives_a_call_on_another_stream():
+    """The workspace that a call allocates is not given out again while another stream's
+    call still needs it: here that call runs after 4 ms of other work, while the memory that
+    the current stream got meanwhile is overwritten again and again."""
+    c = Decode(36, "bf16", [int(x) for x in np.random.default_rng(5).integers(1, 400, 180)], 1, 4, 4, 128, 16)
+    dv = Dev(c)
+    dv.call()
+    nbytes = pa.pa_decode_window_workspace_size(len(c.lens), 4, 4, 128, 16, int(c.lens.max()))
+    torch.cuda.synchronize()
+    side, again, busy = torch.cuda.Stream(), torch.empty_like(dv.out), torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(8_000_000)
+    dv.call(again, stream=side)
+    other = torch.full((nbytes,), 255, dtype=torch.uint8, device=DEV)
+    busy.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(busy):
+        for _ in range(4000):
+            other.fill_(255)
+    torch.cuda.synchronize()
+    assert torch.equal(again.view(torch.int16), dv.out.view(torch.int16))
+
+
 def test_two_streams_at_once():
     """Two large calls in flight together, a workspace each, over and over."""
     cs = [Decode(34 + i, dt, [int(x) for x in np.random.default_rng(i).integers(1, 400, 180)], 1, 4, 4, 128, 16)

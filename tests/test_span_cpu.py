@@ -80,3 +80,13 @@ def test_python_calls_refuse_host_tensors():
     t = torch.zeros(1, 1, dtype=torch.int32)
     with pytest.raises(ValueError):
         pa.pa_decode_window(q, q, kc, kc, t, t[0], 1.0, 2, 1, 4)
+
+
+def test_a_prepared_call_needs_a_workspace():
+    q, t = torch.zeros(2, 4, 128, dtype=torch.bfloat16), torch.zeros(2, 4, dtype=torch.int32)
+    pool, codes = torch.zeros(8, 2, 16, 128, dtype=torch.bfloat16), torch.zeros(8, 2, 16, 128, dtype=torch.uint8)
+    lens, scales = torch.ones(2, dtype=torch.int32), torch.ones(8, 2)
+    with pytest.raises(ValueError, match="workspace"):
+        pa.pa_decode_window(q.clone(), q, pool, pool, t, lens, 1.0, 2, 64, 8, prepare=True)
+    with pytest.raises(ValueError, match="workspace"):
+        pa.pa_decode_fp8_block(q.clone(), q, codes, codes, t, lens, 1.0, scales, scales, 2, 64, prepare=True)
