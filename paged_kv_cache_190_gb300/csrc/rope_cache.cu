@@ -12,8 +12,7 @@
 // All of it is bound by memory: a token's rows are read once and written once.  On a GB300
 // (6.78 TB/s copied), 32 query and 8 kv heads of 128, bf16: 16384 tokens, 409 MB, in 61.6 us
 // (6.64 TB/s); 256 tokens in 2.3 us, one in 1.7 (the kernel's start); into page-scaled e4m3
-// pools 8190 tokens, 188 MB, in 36.3 us (5.17 TB/s: the conversions of the K and V rows are
-// 20 us of work for the SMs, next to 23 for q's bytes), 256 tokens in 3.5 us.
+// pools 8190 tokens, 188 MB, in 31.2 us (6.0 TB/s), 256 single tokens in 3.6 us.
 // A lane holds the two 16-byte chunks of a row that rotate into each other, and a
 // thread takes the same chunks of several heads of one token, so that the table
 // row (4 bytes per rotated column, twice what a bf16 row is) is loaded once for
@@ -148,8 +147,16 @@ __device__ __forceinline__ void rotate(float* x0, float* x1, const LaneChunks<N,
   }
 }
 
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
+// Four floats as e4m3 codes: nearest even, saturated, NaN kept.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t w;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(w)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return w;
 }
 
 // Division as a call: a scale that is no power of two is rare (one that the append did
@@ -167,8 +174,7 @@ __device__ __forceinline__ uint2 e4m3x8(const float* x, float s, bool pow2, floa
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = divide(x[e], s);
   }
-  return make_uint2(e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16),
-                    e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
+  return make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
 }
 
 // A normal power of two whose reciprocal is normal too.
@@ -319,17 +325,23 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
   return u < 0x7f800000u ? u : 0u;
 }
 
+// The largest magnitudes of a chunk's even and odd columns; NaN drops out.
+__device__ __forceinline__ __nv_bfloat162 largest(const uint4& w) {
+  auto pair = [](uint32_t x) {
+    x &= 0x7fff7fffu;
+    return *reinterpret_cast<const __nv_bfloat162*>(&x);
+  };
+  return __hmax2(__hmax2(pair(w.x), pair(w.y)), __hmax2(pair(w.z), pair(w.w)));
+}
+
 // Codes of a word at a new scale: value * ratio, nearest even.
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
-  uint32_t out = 0;
+  float2 f[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const __half2 h = static_cast<__half2>(__nv_cvt_fp8x2_to_halfraw2(
-        static_cast<__nv_fp8x2_storage_t>((w >> (16 * i)) & 0xffffu), __NV_E4M3));
-    const float2 f = __half22float2(h);
-    out |= e4m3x2(f.x * ratio, f.y * ratio) << (16 * i);
-  }
-  return out;
+  for (int i = 0; i < 2; ++i)
+    f[i] = __half22float2(static_cast<__half2>(__nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>((w >> (16 * i)) & 0xffffu), __NV_E4M3)));
+  return e4m3x4(f[0].x * ratio, f[0].y * ratio, f[1].x * ratio, f[1].y * ratio);
 }
 
 // Tokens around a tile, as its block sees them: token t0 - 1 + i in entry i.
@@ -354,8 +366,10 @@ __device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::
 // A run of several tokens: the block takes its rows of up to kHeadsPerItem heads, of K or
 // of V.  The rows and the tokens' table rows come into shared memory all at once, which is
 // what has to overlap; the warps go over them there twice, for the magnitude and for the
-// codes.  (8190 tokens of 32 + 8 heads: 38 us; warp by warp straight from HBM, with rows
-// kept in registers or read twice, 44 to 54.)  Runs of more than kKeptRows tokens come in
+// codes.  (8190 tokens of 32 + 8 heads, q behind: 38 us; warp by warp straight from HBM, with
+// rows kept in registers or read twice, 44 to 54.)  What is left is instructions, 0.6 a
+// cycle of each scheduler: loops that are not unrolled (36.4 -> 35.3), no division by a
+// number of heads or columns (35.3 -> 34.8).  Runs of more than kKeptRows tokens come in
 // pieces, the first of them again for its codes.
 constexpr int kHeadsPerItem = 8;
 constexpr int kWarps = kPageThreads / 32;
@@ -364,13 +378,13 @@ constexpr int kRunBytes = kKeptRows * (kHeadsPerItem * 256 + 128 * 4);
 template <bool INTER, int BS>
 __device__ __forceinline__ void append_run(const RopeArgs& a, const TileTokens& seen, unsigned char* buf, float* tops,
                                            int64_t t, int first, int n, uint32_t offsets, int64_t page, int h0,
-                                           bool is_v) {
+                                           int heads, bool is_v) {
   constexpr int N = 8, D = 128;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int l = lane % kLanesPerRow, row = lane / kLanesPerRow;
-  const int heads = min(kHeadsPerItem, a.num_kv_heads - h0);
-  const int wph = kWarps / heads;                          // warps of a head
-  const int hh = warp / wph, sub = warp - hh * wph;
+  const int wph_log2 = heads > 4 ? 0 : heads > 2 ? 1 : heads > 1 ? 2 : 3, wph = 1 << wph_log2;   // warps of a head
+  static_assert(kWarps == 8 && kHeadsPerItem == 8, "a warp or more for each head");
+  const int hh = warp >> wph_log2, sub = warp & (wph - 1);
   const bool active = hh < heads;
   const bool fresh = offsets & 1u;
   const bool turned = !is_v && a.rot_dim > 0;
@@ -382,16 +396,15 @@ __device__ __forceinline__ void append_run(const RopeArgs& a, const TileTokens& 
   const LaneChunks<N, D, INTER> lc(l, is_v ? 0 : a.rot_dim);
 
   auto fetch = [&](int r0, int m) {
-    const int cpr = heads * 16, tpr = a.rot_dim / 4;       // 16-byte chunks of a token
-    const int at = threadIdx.x % cpr;
-    if (threadIdx.x < kPageThreads / cpr * cpr)
-      for (int r = threadIdx.x / cpr; r < m; r += kPageThreads / cpr)
-        fetch16(buf + (r * cpr + at) * 16, src + (r0 + r) * stride + at * N);
-    if (turned)
-      for (int i = threadIdx.x; i < m * tpr; i += kPageThreads) {
-        const int r = i / tpr, c = i - r * tpr;
-        fetch16(table + r * a.rot_dim + c * 4, a.cos_sin + seen.pos[first + r0 + r] * a.rot_dim + c * 4);
-      }
+    // a token a warp (no divisions: they were most of the instructions here)
+    const int cpr = heads * 16, tpr = a.rot_dim / 4;       // 16-byte chunks of a token: rows, table row
+    for (int r = warp; r < m; r += kWarps) {
+      const uint16_t* from = src + (r0 + r) * stride + lane * N;
+      unsigned char* to = buf + (r * cpr + lane) * 16;
+      for (int c = lane; c < cpr; c += 32, from += 32 * N, to += 32 * 16) fetch16(to, from);
+      if (turned && lane < tpr)
+        fetch16(table + r * a.rot_dim + lane * 4, a.cos_sin + seen.pos[first + r0 + r] * a.rot_dim + lane * 4);
+    }
     fetched();
     __syncthreads();
   };
@@ -410,13 +423,22 @@ __device__ __forceinline__ void append_run(const RopeArgs& a, const TileTokens& 
   const float old = fresh || !active ? 0.f : *scale;
   const int last = (n - 1) / kKeptRows * kKeptRows;
   float top = 0.f;
+  __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
   for (int r0 = 0; r0 < n; r0 += kKeptRows) {
     if (r0 > 0) __syncthreads();
     const int m = min(n - r0, kKeptRows);
     fetch(r0, m);
     if (active)
-#pragma unroll 2
+#pragma unroll 1
       for (int r = sub * kRowsPerPass + row; r < m; r += wph * kRowsPerPass) {
+        if (!turned) {                                     // bf16 as they are, in pairs
+          const uint4* p = reinterpret_cast<const uint4*>(buf + (r * heads + hh) * 256);
+          const __nv_bfloat162 t = __hmax2(top2, __hmax2(largest(p[lc.c0]), largest(p[lc.c1])));
+          if (!__hisinf(t.x) && !__hisinf(t.y)) {
+            top2 = t;
+            continue;
+          }
+        }
         float x0[N], x1[N];
         values(r, x0, x1);
         float t = top;                                     // NaN drops out of fmaxf
@@ -433,6 +455,7 @@ __device__ __forceinline__ void append_run(const RopeArgs& a, const TileTokens& 
         top = t;
       }
   }
+  top = fmaxf(top, fmaxf(__low2float(top2), __high2float(top2)));
   top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
   if (wph > 1) {
     if (lane == 0) tops[warp] = top;
@@ -462,7 +485,7 @@ __device__ __forceinline__ void append_run(const RopeArgs& a, const TileTokens& 
       fetch(r0, m);
     }
     if (active)
-#pragma unroll 2
+#pragma unroll 1
       for (int r = sub * kRowsPerPass + row; r < m; r += wph * kRowsPerPass) {
         float x0[N], x1[N];
         values(r, x0, x1);
@@ -477,7 +500,7 @@ __device__ __forceinline__ void append_run(const RopeArgs& a, const TileTokens& 
 
 // A run of one token, which is what a decode step's are: lanes 0-15 take the head's K
 // row, lanes 16-31 its V row, a 16-byte chunk each, and get the chunk that theirs rotates
-// with from its lane.  
+// with from its lane.
 template <bool INTER, int BS>
 __device__ __forceinline__ void append_one(const RopeArgs& a, int64_t t, int64_t pos, int off, int64_t page, int h) {
   constexpr int N = 8, D = 128;
@@ -545,20 +568,28 @@ __device__ __forceinline__ void append_one(const RopeArgs& a, int64_t t, int64_t
 }
 
 // A block of a tile: the runs that start among the tile's kTile tokens, a warp for each
-// (token, head) of the runs of one token and the block for each (run, 8 heads, K or V) of
-// the longer ones; the tile's `parts` blocks share these out.  Every block looks its
-// tokens up once, into shared memory.  The blocks behind rotate q.
+// (token, head) of the runs of one token and the block for each (run, item_heads heads, K
+// or V) of the longer ones; the tile's `parts` blocks share these out.  Every block looks
+// its tokens up once, into shared memory.  After each of these blocks come `between` that
+// rotate q, and the rest of those behind all of them.
 template <bool INTER, int BS>
 __global__ void __launch_bounds__(kPageThreads, 3) rope_and_cache_page_scale_kernel(
-    const RopeArgs a, unsigned parts, unsigned kv_blocks, unsigned q_groups, unsigned uq) {
+    const RopeArgs a, unsigned parts, unsigned kv_blocks, unsigned between, unsigned q_groups, unsigned uq,
+    int item_heads) {
   __shared__ TileTokens seen;
   __shared__ float tops[kWarps];
   extern __shared__ __align__(16) unsigned char run_buf[];
   wait_prior_grids();
   allow_next_grid();
-  const unsigned kv = blockIdx.x;
-  if (kv >= kv_blocks) {
-    const unsigned g = (kv - kv_blocks) * (kPageThreads / kLanesPerRow) + threadIdx.x / kLanesPerRow;
+  unsigned kv = blockIdx.x, qb = blockIdx.x - kv_blocks;
+  bool is_q = kv >= kv_blocks;
+  if (between > 0 && kv < kv_blocks * (between + 1)) {
+    kv = blockIdx.x / (between + 1);
+    is_q = kv * (between + 1) != blockIdx.x;
+    qb = blockIdx.x - kv - 1;
+  }
+  if (is_q) {
+    const unsigned g = qb * (kPageThreads / kLanesPerRow) + threadIdx.x / kLanesPerRow;
     if (g >= q_groups) return;
     const unsigned t = g / uq;
     rows_of_token<uint16_t, 128, INTER, false, kPageHeadsAtOnce>(a, t, kQ, (g - t * uq) * kPageHeadsAtOnce,
@@ -620,12 +651,15 @@ __global__ void __launch_bounds__(kPageThreads, 3) rope_and_cache_page_scale_ker
     append_one<INTER, BS>(a, static_cast<int64_t>(t0) + at, seen.pos[at + 1], seen.off[at + 1], seen.page[at + 1],
                           k - j * a.num_kv_heads);
   }
-  const int groups = (a.num_kv_heads + kHeadsPerItem - 1) / kHeadsPerItem;
-  for (int k = part; k < seen.num_more * groups * 2; k += parts) {
-    const int j = k / (2 * groups), m = k - j * 2 * groups, at = seen.more[j], n = seen.length[at];
+  const int groups = (a.num_kv_heads + item_heads - 1) / item_heads;
+  if (seen.num_more == 0) return;                          // (a decode step)
+  for (int j = 0, m = part;; m += parts) {
+    for (; m >= 2 * groups; m -= 2 * groups) ++j;
+    if (j >= seen.num_more) break;
+    const int at = seen.more[j], n = seen.length[at], h0 = (m >> 1) * item_heads;
     const uint32_t offsets = __reduce_or_sync(0xffffffffu, lane < n ? 1u << seen.off[at + 1 + lane] : 0u);
     append_run<INTER, BS>(a, seen, run_buf, tops, static_cast<int64_t>(t0) + at, at + 1, n, offsets, seen.page[at + 1],
-                          (m >> 1) * kHeadsPerItem, m & 1);
+                          h0, min(item_heads, a.num_kv_heads - h0), m & 1);
   }
 }
 
@@ -694,20 +728,32 @@ cudaError_t launch_rope_and_cache(const RopeArgs& a, cudaStream_t stream) {
     return a.head_dim == 128 ? run_rope<uint16_t, 128, false>(a, stream) : run_rope<uint16_t, 64, false>(a, stream);
   if (a.pool == RopePool::kF32)
     return a.head_dim == 128 ? run_rope<float, 128, false>(a, stream) : run_rope<float, 64, false>(a, stream);
-  // a scale for each page and head.  A tile has a run for each of its tokens (a decode
-  // step) or one or two in all (a prompt): as many blocks a tile as give every token and
-  // head of a decode step a warp at once, while the tiles are few; two (K and V) from
-  // there on
+  // A scale for each page and head.  A tile has a run for each of its tokens (a decode
+  // step) or one or two in all (a prompt).  Heads of an item: as many as leave 256 items
+  // (512 tokens of 8 kv heads: 6.0 us with 2, 7.5 with 8; 4096: 15.2 with 8, 17.2 with 4).
+  // Blocks of a tile: while the tiles are few, as many as give every token and head of a
+  // decode step a warp at once; from there on one for two groups of heads (8190 tokens, 8 kv
+  // heads: 31.2 us, 32.4 with a block each for K and V).
   const int64_t tiles = (a.num_tokens + kTile - 1) / kTile;
-  const int most = (kTile * a.num_kv_heads + kWarps - 1) / kWarps;
-  const int parts = static_cast<int>(std::max<int64_t>(2, std::min<int64_t>(most, 512 / tiles)));
+  int item_heads = 1;
+  while (item_heads < kHeadsPerItem &&
+         static_cast<int64_t>(a.num_tokens / a.block_size) * a.num_kv_heads >= 256 * item_heads)
+    item_heads *= 2;
+  const int groups = ceil_div(a.num_kv_heads, item_heads);
+  const int most = ceil_div(kTile * a.num_kv_heads, kWarps);
+  const int parts = static_cast<int>(std::max<int64_t>((groups + 1) / 2, std::min<int64_t>(most, 512 / tiles)));
   const int64_t kv_blocks = tiles * parts;
   const int uq = ceil_div(a.num_q_heads, kPageHeadsAtOnce);
   const int64_t q_groups = static_cast<int64_t>(a.num_tokens) * uq;
   const int64_t q_blocks = (q_groups + kPageThreads / kLanesPerRow - 1) / (kPageThreads / kLanesPerRow);
+  // q's blocks between the runs' blocks, where there are rows enough of q: the runs wait and
+  // convert while q's rows move (8190 tokens of 32 + 8 heads: 31.2 us; all of q behind 34.8,
+  // all between 32.8).  Half of them, which leaves blocks for the end; a page of 32 is two
+  // tiles, of which one has the run.
+  const int64_t between = a.num_q_heads > 2 * a.num_kv_heads ? q_blocks / kv_blocks * 8 / a.block_size : 0;
   if (kv_blocks >= kMostGroups / 2 || q_groups >= kMostGroups) return cudaErrorInvalidValue;
   auto go = [&](auto kernel) {
-    return launch(kernel, kv_blocks + q_blocks, kPageThreads, kRunBytes, stream, a, parts, kv_blocks, q_groups, uq);
+    return launch(kernel, kv_blocks + q_blocks, kPageThreads, kRunBytes, stream, a, parts, kv_blocks, between, q_groups, uq, item_heads);
   };
   if (a.interleaved)
     return a.block_size == 16 ? go(rope_and_cache_page_scale_kernel<true, 16>)

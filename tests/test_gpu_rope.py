@@ -316,3 +316,17 @@ def test_copy_scales_follows_copied_and_swapped_pages():
     pa.pa_copy_scales(ks, vs, hk, hv, torch.tensor([[6, 1], [4, 0]], device=DEV), device_errors=errs)
     assert pa.pa_read_device_errors(errs) == 0
     assert torch.equal(hk, wk[[4, 6]].cpu()) and torch.equal(hv, wv[[4, 6]].cpu())
+
+
+@pytest.mark.parametrize("spans,hq,hkv,bs", [
+    ([(7, 1000)], 5, 5, 16), ([(0, 900), (40, 1200)], 5, 5, 16), ([(0, 3500)], 7, 7, 16), ([(90, 2100)], 12, 3, 32),
+    ([(17, 2900), (0, 1333)], 32, 8, 16), ([(3, 9001)], 20, 1, 16), ([(5, 8500)], 36, 2, 32), ([(0, 1700)], 9, 9, 16)])
+def test_prompts_of_many_sizes(spans, hq, hkv, bs):
+    """From one head of a run at a time to eight, one group of heads or several, q's blocks
+    between the runs' blocks or behind them."""
+    slots, pos, nb = _run_of(spans, bs, hq)
+    c = rope_cases.Append(hq + bs, "fp8_block", len(slots), hq, hkv, 128, 64, bs, nb, max_position=9100,
+                          interleaved=hkv == 3, slots=slots, positions=pos)
+    d = Dev(c)
+    assert d.call() == 0
+    _check(c, d)
