@@ -763,8 +763,11 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
         (len < 0 || len > p.max_len || (len > 0 && len < p.q_len)))
       report(p.device_errors, PA_DEVERR_BAD_LENGTH);
     const int nst = make_span<TU>(p, len).nst;
-    st0 = static_cast<int>(static_cast<long long>(nst) * rank >> p.splits_log2);
-    cnt = static_cast<int>(static_cast<long long>(nst) * (rank + 1) >> p.splits_log2) - st0;
+    // (exact: nst < 2^28, splits <= 8)
+    const int each = p.splits > 1 ? static_cast<int>(__umulhi(static_cast<uint32_t>(nst), p.over_splits)) : nst;
+    const int rest = nst - each * p.splits;
+    st0 = each * rank + min(rank, rest);
+    cnt = each + (rank < rest ? 1 : 0);
   } else {
     // every CTA adds up the stages of all sequences: thread t a run of them
     const int per = (p.num_seqs + kSpanThreads - 1) / kSpanThreads;
@@ -1083,7 +1086,8 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
           }
           if (p.splits > 1) {
             // to the CTA of the cluster that joins this row
-            const int row = hl * p.rows + r, to = row & (p.splits - 1), slot = row - to + rank;
+            const int row = hl * p.rows + r;
+            const int to = row - static_cast<int>(__umulhi(row, p.over_splits)) * p.splits, slot = row - to + rank;
             acc.store_peer(peer_addr(smem_addr(joint + slot * D + lane * CPL), to));
             if (lane == 0) peer_store(peer_addr(smem_addr(joint_ml + slot * 2), to), M, lam);
           } else {
@@ -1143,21 +1147,26 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
   }
 }
 
+// The opt-in of an instance to more than 48 KiB of dynamic shared memory, once a device.
+template <SpanPool P, int D, int G>
+cudaError_t configure_span(int* device) {
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = cudaGetDevice(device);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (*device & 63);
+  if (configured.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(span_decode_kernel<P, D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpanSmem);
+  if (e == cudaSuccess) configured.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
+
 // Launch of one instance: a plain grid of shares, or a grid (splits, head groups,
 // sequences) of clusters of p.splits CTAs.
 template <SpanPool P, int D, int G>
 cudaError_t run_span(const SpanParams& p, dim3 grid, int smem, cudaStream_t stream) {
-  // the opt-in to more than 48 KiB of dynamic shared memory is per device
-  static std::atomic<uint64_t> configured{0};
   int device = 0;
-  cudaError_t e = cudaGetDevice(&device);
+  const cudaError_t e = configure_span<P, D, G>(&device);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (device & 63);
-  if (!(configured.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(span_decode_kernel<P, D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpanSmem);
-    if (e != cudaSuccess) return e;
-    configured.fetch_or(bit, std::memory_order_acq_rel);
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kSpanThreads);

@@ -82,7 +82,8 @@ struct SpanParams {
   int hg_log2, ngroups;                           // kv heads of a CTA (log2), CTA head groups
   int block_size, num_blocks, max_blocks, max_len, window, sinks;
   int ring;
-  int splits, splits_log2;                        // CTAs of a cluster that share a segment; 0: shares
+  int splits;                                     // CTAs of a cluster that share a segment; 0: shares
+  uint32_t over_splits;                           // ceil(2^32 / splits): the high word of a product divides
   int joint_slots;                                // clusters: states that a CTA has room for
   float* part_out;                                // shares: [2 CTAs][hg * rows][head_dim]
   float* part_lse;                                // shares: [2 CTAs][hg * rows]
@@ -112,6 +113,9 @@ struct SpanArgs {
 size_t span_workspace_size(int rows, int num_kv_heads, int head_dim, int num_sms);
 cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream);
 
+// CTAs of a GPU that clusters of `splits` can hold at once (its processor clusters have SMs
+// left over: of 152, 120 for clusters of 8).
+int span_cluster_room(int splits, int num_sms);
 cudaError_t run_span_bf16(int head_dim, const SpanParams& p, dim3 grid, int smem, cudaStream_t stream);
 cudaError_t run_span_f32(int head_dim, const SpanParams& p, dim3 grid, int smem, cudaStream_t stream);
 cudaError_t run_span_fp8(const SpanParams& p, dim3 grid, int smem, cudaStream_t stream);

@@ -263,6 +263,8 @@ int ring_stages(SpanPool pool, int head_dim, int rows, int hg, int splits) {
 // to be 0.7 of it in the mean.  (us, clusters and shares, e4m3: 1 sequence of 256 tokens
 // 5.1 and 7.6, 4 of 1024 6.4 and 10.1, 16 of 2048 14.5 and 18.8, 64 of 2048 to 4096 88 and
 // 72; bf16: 4 of 4096 10.7 and 13.4, 16 windows of 4096 44.4 and 49.5, 64 of 256 9.9 and 14.2.)
+// Clusters of any size up to 8, not of powers of two alone (e4m3: 10 sequences of 1024 8.8 us
+// in clusters of 3, 9.9 without; 12 of 2048 13.4 in 5s, 14.5; bf16: 10 of 1024 8.9 and 10.3).
 // float32 rows are computed one by one: with 1, 4 and 8 of them a stage takes 0.93, 1.13 and
 // 1.50 us (one head a CTA), 0.66, 0.87 and 1.35 (8 heads).  Nothing is chosen that leaves the
 // ring a single stage (8 such heads of 8 rows in clusters: 130 us, where 2 stages take 90).
@@ -293,11 +295,9 @@ Spread choose_spread(SpanPool pool, int head_dim, int rows, int64_t num_seqs, in
     const int64_t nst = (blocks + kSpanWarps / hg - 1) / (kSpanWarps / hg);
     const int start = fp8 ? (hg >= 4 ? 450 : hg == 2 ? 380 : 360) : (hg >= 4 ? 410 : hg == 2 ? 315 : 300);
     const int stage = stage_cost(hg);
-    for (int splits = 1; splits <= kSpanCluster && splits <= nst; splits *= 2) {
-      // the clusters that the GPU's processor clusters hold at once: of 8 CTAs 15 of 19, of
-      // 4 36 of 38
-      const int64_t room = splits == 8 ? num_sms * 3 / 4 : splits == 4 ? num_sms * 9 / 10 : num_sms;
-      if (segs * splits > room || ring_stages(pool, head_dim, rows, hg, splits) < 2) break;
+    for (int splits = 1; splits <= kSpanCluster && splits <= nst; ++splits) {
+      if (segs * splits > num_sms || ring_stages(pool, head_dim, rows, hg, splits) < 2) break;
+      if (segs * splits > span_cluster_room(splits, num_sms)) continue;
       const int64_t stages = (nst + splits - 1) / splits;
       const int64_t cost = start + std::max<int64_t>(stages * stage, hbm) + (splits == 1 ? 0 : hg == 8 ? 150 : 75);
       if (cost < best.cost) {
@@ -345,7 +345,7 @@ cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream) {
   if (clusters) {
     const int splits = sp.splits;
     p.splits = splits;
-    while ((1 << p.splits_log2) < splits) ++p.splits_log2;
+    p.over_splits = static_cast<uint32_t>(((uint64_t{1} << 32) + splits - 1) / splits);
     blocks_of = dim3(static_cast<unsigned>(splits), static_cast<unsigned>(a.num_kv_heads / hg),
                      static_cast<unsigned>(a.num_seqs));
     ring = static_cast<int>(std::min<int64_t>(ring_most, sp.stages));

@@ -303,6 +303,22 @@ def test_no_window_agrees_with_the_full_decode():
     check(c, full)
 
 
+@pytest.mark.parametrize("dtype,q_len,hq,hkv", [("bf16", 1, 8, 8), ("fp8", 1, 16, 8), ("f32", 2, 8, 8), ("bf16", 2, 8, 2),
+                                                ("fp8", 4, 3, 3)])
+@pytest.mark.parametrize("seqs,most", [(1, 700), (2, 300), (3, 1500), (7, 700), (10, 1500), (12, 700), (20, 700), (24, 1500),
+                                       (45, 700)])
+def test_sequences_split_over_any_number_of_blocks(dtype, q_len, hq, hkv, seqs, most):
+    """The longest sequence over 1 to 8 blocks, the others over as many, some with less than
+    a tile for each."""
+    lens = np.random.default_rng(seqs).integers(q_len, most // 2, seqs)
+    lens[0], lens[-1] = q_len, most
+    c = Decode(seqs, dtype, lens, q_len, hq, hkv, 128, 16)
+    dv = Dev(c)
+    dv.call()
+    assert dv.errors() == 0
+    check(c, dv.out)
+
+
 @pytest.mark.parametrize("norm", [1e-30, 2.0 ** -20, 2.0 ** 12, 0.0])
 def test_first_pages_with_values_of_another_size(norm):
     """V rows of the first page far smaller (as first tokens' are) or larger than the rest."""
