@@ -330,3 +330,18 @@ def test_prompts_of_many_sizes(spans, hq, hkv, bs):
     d = Dev(c)
     assert d.call() == 0
     _check(c, d)
+
+
+@pytest.mark.parametrize("bs", [16, 32])
+@pytest.mark.parametrize("hkv,seqs,most", [(1, 71, 9), (2, 176, 3), (3, 34, 5), (8, 64, 8), (8, 200, 12), (11, 40, 8)])
+def test_a_few_tokens_of_many_sequences(hkv, seqs, most, bs):
+    """What a step of drafted tokens appends: runs of 1 to a few tokens, some over a page's
+    end, that share out a tile's blocks."""
+    r = np.random.default_rng(hkv + seqs)
+    spans = [(int(h), int(n)) for h, n in zip(r.integers(0, 100, seqs), r.integers(1, most + 1, seqs))]
+    slots, pos, nb = _run_of(spans, bs, hkv)
+    c = rope_cases.Append(seqs + bs, "fp8_block", len(slots), 2 * hkv, hkv, 128, 96, bs, nb, max_position=128,
+                          interleaved=bs == 32, slots=slots, positions=pos)
+    d = Dev(c)
+    assert d.call() == 0
+    _check(c, d)
