@@ -268,6 +268,11 @@ int ring_stages(SpanPool pool, int head_dim, int rows, int hg, int splits) {
 // float32 rows are computed one by one: with 1, 4 and 8 of them a stage takes 0.93, 1.13 and
 // 1.50 us (one head a CTA), 0.66, 0.87 and 1.35 (8 heads).  Nothing is chosen that leaves the
 // ring a single stage (8 such heads of 8 rows in clusters: 130 us, where 2 stages take 90).
+// More short sequences than SMs: the end of a segment takes a CTA of the shares 1.9 us, 2.9
+// with 8 rows, which long ones hide behind their copies; so more heads a segment, or a CTA
+// for each segment, one after another on an SM (bf16, 8 kv heads: 232 sequences of 10 to 36
+// tokens, 8 rows, 12.1 us so, in shares 25.5 with 2 heads and 19.3 with 8; 512 of 20 to 40
+// 22.6, 33.9 and 21.5; 160 of 1000 135, 109.4 and 109.3).
 struct Spread {
   int hg = 0, splits = 0;                                    // splits 0: shares
   int64_t stages = 0, cost = 0;
@@ -275,13 +280,12 @@ struct Spread {
 Spread choose_spread(SpanPool pool, int head_dim, int rows, int64_t num_seqs, int num_kv_heads, int64_t blocks,
                      bool even, int num_sms) {
   const int stage_bytes = span_stage_bytes(pool, head_dim);
-  constexpr int kShares = 800;
+  constexpr int kShares = 610;
   // a stage of every SM at 6.7 TB/s, and what the calls' stages take at that rate
   const int64_t together = 145ll * stage_bytes / 65536;
   const int64_t all = (num_seqs * num_kv_heads * blocks + kSpanWarps - 1) / kSpanWarps;
   const int64_t hbm = together * all / num_sms * (even ? 10 : 7) / 10;
   Spread best;
-  best.hg = share_heads(pool, num_kv_heads);
   const bool fp8 = pool == SpanPool::kFp8;
   const auto stage_cost = [&](int hg) {
     const int full = fp8 ? (hg == 8 ? 106 : hg == 4 ? 109 : hg == 2 ? 130 : 176)
@@ -289,17 +293,30 @@ Spread choose_spread(SpanPool pool, int head_dim, int rows, int64_t num_seqs, in
     const int stage = full * (32768 + stage_bytes) / 98304;  // half a stage (bf16 heads of 64) takes two thirds
     return pool == SpanPool::kF32 ? stage + 7 * (rows - 1) : stage;
   };
-  best.cost = kShares + std::max({hbm, together, (all + num_sms - 1) / num_sms * stage_cost(best.hg)});
+  const int64_t segment = 190 + 14 * (rows - 1);
+  best.cost = INT64_MAX;
+  for (const int hg : {share_heads(pool, num_kv_heads), heads_together(num_kv_heads, kSpanWarps)}) {
+    const int64_t cost = kShares + segment + std::max({hbm, together, (all + num_sms - 1) / num_sms * stage_cost(hg),
+                                                       num_seqs * (num_kv_heads / hg) * segment / num_sms});
+    if (cost < best.cost) {
+      best.hg = hg;
+      best.cost = cost;
+    }
+  }
   for (int hg = heads_together(num_kv_heads, kSpanWarps); hg >= 1; hg /= 2) {
     const int64_t segs = num_seqs * (num_kv_heads / hg);
     const int64_t nst = (blocks + kSpanWarps / hg - 1) / (kSpanWarps / hg);
     const int start = fp8 ? (hg >= 4 ? 450 : hg == 2 ? 380 : 360) : (hg >= 4 ? 410 : hg == 2 ? 315 : 300);
     const int stage = stage_cost(hg);
     for (int splits = 1; splits <= kSpanCluster && splits <= nst; ++splits) {
-      if (segs * splits > num_sms || ring_stages(pool, head_dim, rows, hg, splits) < 2) break;
-      if (segs * splits > span_cluster_room(splits, num_sms)) continue;
+      // (a CTA alone waits for no other: there may be more of them than SMs)
+      const int64_t turns = splits == 1 ? (segs + num_sms - 1) / num_sms : 1;
+      if (splits > 1 && segs * splits > num_sms) break;
+      if (turns > 8 || ring_stages(pool, head_dim, rows, hg, splits) < 2) break;
+      if (splits > 1 && segs * splits > span_cluster_room(splits, num_sms)) continue;
       const int64_t stages = (nst + splits - 1) / splits;
-      const int64_t cost = start + std::max<int64_t>(stages * stage, hbm) + (splits == 1 ? 0 : hg == 8 ? 150 : 75);
+      const int64_t cost = std::max<int64_t>(turns * (start + stages * stage), start + hbm) +
+                           (splits == 1 ? 0 : hg == 8 ? 150 : 75);
       if (cost < best.cost) {
         best.hg = hg;
         best.splits = splits;

@@ -319,6 +319,17 @@ def test_sequences_split_over_any_number_of_blocks(dtype, q_len, hq, hkv, seqs, 
     check(c, dv.out)
 
 
+@pytest.mark.parametrize("dtype,seqs,q_len,hq,hkv", [("bf16", 232, 2, 32, 8), ("fp8", 294, 8, 4, 4), ("f32", 300, 1, 4, 4),
+                                                     ("bf16", 512, 1, 8, 8), ("f32", 232, 2, 16, 4), ("fp8", 700, 1, 4, 1)])
+def test_more_short_sequences_than_blocks_fit(dtype, seqs, q_len, hq, hkv):
+    lens = np.random.default_rng(seqs).integers(q_len, 41, seqs)
+    c = Decode(seqs, dtype, lens, q_len, hq, hkv, 128, 16, window=30, sinks=2)
+    dv = Dev(c)
+    dv.call()
+    assert dv.errors() == 0
+    check(c, dv.out)
+
+
 @pytest.mark.parametrize("norm", [1e-30, 2.0 ** -20, 2.0 ** 12, 0.0])
 def test_first_pages_with_values_of_another_size(norm):
     """V rows of the first page far smaller (as first tokens' are) or larger than the rest."""
