@@ -268,8 +268,8 @@ int ring_stages(SpanPool pool, int head_dim, int rows, int hg, int splits) {
 // float32 rows are computed one by one: with 1, 4 and 8 of them a stage takes 0.93, 1.13 and
 // 1.50 us (one head a CTA), 0.66, 0.87 and 1.35 (8 heads).  Nothing is chosen that leaves the
 // ring a single stage (8 such heads of 8 rows in clusters: 130 us, where 2 stages take 90).
-// More short sequences than SMs: the end of a segment takes a CTA of the shares 1.9 us, 2.9
-// with 8 rows, which long ones hide behind their copies; so more heads a segment, or a CTA
+// More short sequences than SMs: the end of a segment takes a CTA of the shares 1.7 us (one
+// head of one row) to 7 (8 of 8), which long ones hide behind their copies; so more heads a segment, or a CTA
 // for each segment, one after another on an SM (bf16, 8 kv heads: 232 sequences of 10 to 36
 // tokens, 8 rows, 12.1 us so, in shares 25.5 with 2 heads and 19.3 with 8; 512 of 20 to 40
 // 22.6, 33.9 and 21.5; 160 of 1000 135, 109.4 and 109.3).
@@ -280,7 +280,7 @@ struct Spread {
 Spread choose_spread(SpanPool pool, int head_dim, int rows, int64_t num_seqs, int num_kv_heads, int64_t blocks,
                      bool even, int num_sms) {
   const int stage_bytes = span_stage_bytes(pool, head_dim);
-  constexpr int kShares = 610;
+  constexpr int kShares = 800;
   // a stage of every SM at 6.7 TB/s, and what the calls' stages take at that rate
   const int64_t together = 145ll * stage_bytes / 65536;
   const int64_t all = (num_seqs * num_kv_heads * blocks + kSpanWarps - 1) / kSpanWarps;
@@ -293,11 +293,12 @@ Spread choose_spread(SpanPool pool, int head_dim, int rows, int64_t num_seqs, in
     const int stage = full * (32768 + stage_bytes) / 98304;  // half a stage (bf16 heads of 64) takes two thirds
     return pool == SpanPool::kF32 ? stage + 7 * (rows - 1) : stage;
   };
-  const int64_t segment = 190 + 14 * (rows - 1);
   best.cost = INT64_MAX;
   for (const int hg : {share_heads(pool, num_kv_heads), heads_together(num_kv_heads, kSpanWarps)}) {
-    const int64_t cost = kShares + segment + std::max({hbm, together, (all + num_sms - 1) / num_sms * stage_cost(hg),
-                                                       num_seqs * (num_kv_heads / hg) * segment / num_sms});
+    const int64_t segment = 150 + hg * (30 + 5 * (rows - 1));
+    const int64_t copies = hg == share_heads(pool, num_kv_heads) ? hbm : hbm * 26 / 25;
+    const int64_t cost = kShares + std::max({copies, together, (all + num_sms - 1) / num_sms * stage_cost(hg),
+                                             num_seqs * (num_kv_heads / hg) * segment / num_sms});
     if (cost < best.cost) {
       best.hg = hg;
       best.cost = cost;
@@ -315,7 +316,10 @@ Spread choose_spread(SpanPool pool, int head_dim, int rows, int64_t num_seqs, in
       if (turns > 8 || ring_stages(pool, head_dim, rows, hg, splits) < 2) break;
       if (splits > 1 && segs * splits > span_cluster_room(splits, num_sms)) continue;
       const int64_t stages = (nst + splits - 1) / splits;
-      const int64_t cost = std::max<int64_t>(turns * (start + stages * stage), start + hbm) +
+      const int64_t busy = turns * (start + stages * stage);
+      // (a seventh more in turns, which lengths that differ upset most: 300 sequences of 4
+      // stages and fewer, 23.1 us, in shares 17.7)
+      const int64_t cost = std::max<int64_t>(turns > 1 ? busy * 8 / 7 : busy, start + hbm) +
                            (splits == 1 ? 0 : hg == 8 ? 150 : 75);
       if (cost < best.cost) {
         best.hg = hg;
