@@ -8,14 +8,16 @@ cudaError_t run_span_bf16(int head_dim, const SpanParams& p, dim3 grid, int smem
                          : span::run_span<SpanPool::kBf16, 64, 8>(p, grid, smem, stream);
 }
 
-int span_cluster_room(int splits, int num_sms) {
-  if (splits <= 1) return num_sms;
+void span_cluster_rooms(int num_sms, int (&room)[kSpanCluster + 1]) {
   static std::atomic<int> known[64][kSpanCluster + 1];       // 0: not asked yet
+  room[0] = 0;
+  room[1] = num_sms;
   int device = 0;
-  if (span::configure_span<SpanPool::kBf16, 128, 8>(&device) == cudaSuccess) {
-    std::atomic<int>& room = known[device & 63][splits];
-    int n = room.load(std::memory_order_relaxed);
-    if (n > 0) return n;
+  const bool ready = span::configure_span<SpanPool::kBf16, 128, 8>(&device) == cudaSuccess;
+  for (int splits = 2; splits <= kSpanCluster; ++splits) {
+    std::atomic<int>& n = known[device & 63][splits];
+    room[splits] = n.load(std::memory_order_relaxed);
+    if (room[splits] > 0) continue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(splits));
     cfg.blockDim = dim3(kSpanThreads);
@@ -26,13 +28,15 @@ int span_cluster_room(int splits, int num_sms) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, span::span_decode_kernel<SpanPool::kBf16, 128, 8>, &cfg) == cudaSuccess && n > 0) {
-      n *= splits;
-      room.store(n, std::memory_order_relaxed);
-      return n;
+    int clusters = 0;
+    if (ready && cudaOccupancyMaxActiveClusters(&clusters, span::span_decode_kernel<SpanPool::kBf16, 128, 8>, &cfg) ==
+                     cudaSuccess && clusters > 0) {
+      room[splits] = clusters * splits;
+      n.store(room[splits], std::memory_order_relaxed);
+    } else {
+      cudaGetLastError();                                    // (not this call's error)
+      room[splits] = num_sms / 2;
     }
   }
-  cudaGetLastError();
-  return num_sms / 2;
 }
 }  // namespace pa

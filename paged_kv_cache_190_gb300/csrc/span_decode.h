@@ -113,9 +113,9 @@ struct SpanArgs {
 size_t span_workspace_size(int rows, int num_kv_heads, int head_dim, int num_sms);
 cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream);
 
-// CTAs of a GPU that clusters of `splits` can hold at once (its processor clusters have SMs
-// left over: of 152, 120 for clusters of 8).
-int span_cluster_room(int splits, int num_sms);
+// room[n]: the CTAs that clusters of n can have at once on the current device (its processor
+// clusters have SMs left over: of 152, 120 for clusters of 8).
+void span_cluster_rooms(int num_sms, int (&room)[kSpanCluster + 1]);
 cudaError_t run_span_bf16(int head_dim, const SpanParams& p, dim3 grid, int smem, cudaStream_t stream);
 cudaError_t run_span_f32(int head_dim, const SpanParams& p, dim3 grid, int smem, cudaStream_t stream);
 cudaError_t run_span_fp8(const SpanParams& p, dim3 grid, int smem, cudaStream_t stream);

@@ -293,6 +293,8 @@ Spread choose_spread(SpanPool pool, int head_dim, int rows, int64_t num_seqs, in
     const int stage = full * (32768 + stage_bytes) / 98304;  // half a stage (bf16 heads of 64) takes two thirds
     return pool == SpanPool::kF32 ? stage + 7 * (rows - 1) : stage;
   };
+  int room[kSpanCluster + 1];
+  span_cluster_rooms(num_sms, room);
   best.cost = INT64_MAX;
   for (const int hg : {share_heads(pool, num_kv_heads), heads_together(num_kv_heads, kSpanWarps)}) {
     const int64_t segment = 150 + hg * (30 + 5 * (rows - 1));
@@ -313,15 +315,15 @@ Spread choose_spread(SpanPool pool, int head_dim, int rows, int64_t num_seqs, in
       // (a CTA alone waits for no other: there may be more of them than SMs)
       const int64_t turns = splits == 1 ? (segs + num_sms - 1) / num_sms : 1;
       if (splits > 1 && segs * splits > num_sms) break;
-      if (turns > 8 || ring_stages(pool, head_dim, rows, hg, splits) < 2) break;
-      if (splits > 1 && segs * splits > span_cluster_room(splits, num_sms)) continue;
+      if (turns > 8) break;
+      if (splits > 1 && segs * splits > room[splits]) continue;
       const int64_t stages = (nst + splits - 1) / splits;
       const int64_t busy = turns * (start + stages * stage);
       // (a seventh more in turns, which lengths that differ upset most: 300 sequences of 4
       // stages and fewer, 23.1 us, in shares 17.7)
       const int64_t cost = std::max<int64_t>(turns > 1 ? busy * 8 / 7 : busy, start + hbm) +
                            (splits == 1 ? 0 : hg == 8 ? 150 : 75);
-      if (cost < best.cost) {
+      if (cost < best.cost && ring_stages(pool, head_dim, rows, hg, splits) >= 2) {
         best.hg = hg;
         best.splits = splits;
         best.stages = stages;
