@@ -3,6 +3,10 @@ rotation, decode steps through windowed and full layers, a fork with copy-on-wri
 tokens verified and in part taken back -- over bf16 pools and over e4m3 pools with page
 scales.  What the pools hold is followed by the oracle; every attention output is checked
 against 64 bits over that."""
+import pathlib
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -203,3 +207,32 @@ def test_a_captured_step_with_padding():
             assert torch.equal(eager.view(torch.int16), o.view(torch.int16))
             loop.attend(list(range(live)), q_out[:live].clone(), 1, window, 2 if window else 0)
     assert pa.pa_read_device_errors(loop.errs) == 0
+
+
+FIRST_CALL = """
+import torch
+import paged_kv_cache_190_gb300 as pa
+g = torch.Generator(device="cuda").manual_seed(0)
+q = torch.randn(4, 8, 128, device="cuda", generator=g).bfloat16()
+codes = torch.randint(0, 120, (8, 2, 16, 128), device="cuda", generator=g, dtype=torch.uint8)
+scales = torch.full((8, 2), 2.0 ** -6, device="cuda")
+tables = torch.arange(8, device="cuda", dtype=torch.int32).view(4, 2)
+lens = torch.tensor([32, 1, 17, 16], device="cuda", dtype=torch.int32)
+ws = torch.empty(1 << 25, device="cuda", dtype=torch.uint8)
+out, again = torch.zeros_like(q), torch.zeros_like(q)
+call = lambda o: pa.pa_decode_fp8_block(o, q, codes, codes, tables, lens, 0.1, scales, scales, 2, 32, workspace=ws)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    call(out)
+graph.replay()
+call(again)
+torch.cuda.synchronize()
+assert out.abs().sum() > 0 and torch.equal(out, again)
+"""
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    root = pathlib.Path(__file__).resolve().parent.parent
+    done = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
