@@ -317,7 +317,9 @@ int pa_decode_fp8(void* out, const void* q, const void* k_cache, const void* v_c
  * not read (the pages may have been given back), and what stands in positions that none
  * sees does not matter, NaN and infinities included.  (A NaN or infinity in the V row of
  * a position that some new token of the sequence sees reaches the rows of that kv head
- * that do not see it too, as a product with the weight 0.)
+ * that do not see it too, as a product with the weight 0.)  Logits, maxima and sums are
+ * float32; over bf16 pools the weights meet V as two bf16 parts each (2^-16 of a weight is
+ * lost), over float32 pools as they are; the result is rounded once.
  *
  * q and out are [num_seqs][q_len][num_q_heads][head_dim] ([num_seqs][num_q_heads]
  * [head_dim] for q_len 1) in the pools' type, PA_F32 or PA_BF16;

@@ -5,7 +5,8 @@
 // Mathematics.  New token j of a sequence of L tokens (q_len of them new) sits at
 // p = L - q_len + j and sees the tokens t <= p with p - t < window or t < sinks:
 //   out = sum_t e^{s_t} V_t / sum_t e^{s_t},   s_t = scale <q, K_t>,
-// one pass with a running maximum (base 2), float32 throughout.
+// one pass with a running maximum (base 2); scores, maxima and sums in float32, the weights
+// of the tensor-core pools rounded for the product with V (two bf16 parts, or a half).
 //
 // What bounds it: the bytes of K and V.  A token of one kv head is 2 D elements for
 // 4 D flops per query row, a flop or a few per byte.  On a GB300 (6.78 TB/s copied): 256
@@ -155,8 +156,10 @@ __device__ __forceinline__ int64_t query_row(const SpanParams& p, int b, int hea
 
 // bf16, mma.sync m16n8k16: scores Q K^T with the rows as A (rows past the group are
 // zero), O^T = V^T P^T with the rows as columns; the score fragment of a lane is the B
-// fragment of the second product, so P stays in registers.  P is rounded to bf16 for
-// it, half a step of 2^-8 for each weight; the row's sum l keeps the unrounded ones.
+// fragment of the second product, so P stays in registers.  P goes into it as two bf16
+// parts, the rounded weight and what the rounding left (2^-16 of each weight is lost;
+// the rounded part alone loses 2^-8, 1.3 times the result's own rounding error); the
+// row's sum l keeps the unrounded ones.
 template <int D>
 struct Bf16Rows {
   static constexpr int KS = D / 16, MT = D / 16, TU = 16;
@@ -222,6 +225,8 @@ struct Bf16Rows {
     for (int e = 0; e < 4; ++e) pr[e] = fast_exp2(sv[e] - mn);
     l = l * alpha + ((pr[0] + pr[1]) + (pr[2] + pr[3]));
     const uint32_t pb0 = pack_bf16x2(pr[0], pr[1]), pb1 = pack_bf16x2(pr[2], pr[3]);
+    const uint32_t rb0 = pack_bf16x2(pr[0] - bf16_lo(pb0), pr[1] - bf16_hi(pb0));
+    const uint32_t rb1 = pack_bf16x2(pr[2] - bf16_lo(pb1), pr[3] - bf16_hi(pb1));
     if (__any_sync(kFull, alpha != 1.f)) {
       const float a_even = __shfl_sync(kFull, alpha, 8 * c), a_odd = __shfl_sync(kFull, alpha, 8 * c + 4);
 #pragma unroll
@@ -237,6 +242,7 @@ struct Bf16Rows {
       uint32_t vf[4];
       ldsm_x4_trans(at(vb, mt), vf[0], vf[1], vf[2], vf[3]);
       mma_bf16_full(o[mt], vf[0], vf[1], vf[2], vf[3], pb0, pb1);
+      mma_bf16_full(o[mt], vf[0], vf[1], vf[2], vf[3], rb0, rb1);
     }
     release();
   }

@@ -476,3 +476,26 @@ def test_refusals_of_the_python_call():
                        (dict(block_tables=dv.tables.t()), ValueError), (dict(context_lens=dv.lens.cpu()), ValueError)):
         with pytest.raises(kind):
             pa.pa_decode_window(**{**ok, **over})
+
+
+@pytest.mark.parametrize("q_len,hq,hkv,d,bs", [(1, 8, 8, 128, 16), (1, 8, 2, 128, 32), (2, 8, 2, 64, 16),
+                                               (8, 2, 2, 128, 16), (1, 3, 3, 64, 32)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 5)])
+@pytest.mark.parametrize("seqs", [2, 40, 200])
+def test_bf16_weights_are_not_rounded_to_bf16(q_len, hq, hkv, d, bs, window, sinks, seqs):
+    """The weights reach the product with V in two bf16 parts, p = hi + lo + e: hi is within
+    2^-8 of p, lo within 2^-8 of p - hi, so |e| <= 2^-16 p.  What is left of the error is the
+    result's own half step, 2^-8, and the scores'.  Small scores (std 0.25) keep the scores'
+    part under 2^-14; values of both signs leave results far under the sum of the magnitudes,
+    where a rounding of each weight to bf16 shows."""
+    r = np.random.default_rng(seqs)
+    lens = [int(x) for x in r.integers(q_len, 300, seqs - 1)] + [300]
+    c = Decode(50 + d, "bf16", lens, q_len, hq, hkv, d, bs, window, sinks, std=0.25)
+    dv = Dev(c)
+    dv.call()
+    assert dv.errors() == 0
+    want, parts = c.want()
+    rel = 2.0 ** -21 * d * parts["dots"][..., None] + 2.0 ** -20
+    bar = 2.0 ** -8 * np.abs(want) + (2.0 ** -16 * 1.01 + rel) * parts["mag"] + 1e-37
+    err = np.abs(out_as_f64(dv.out).reshape(want.shape) - want)
+    assert np.all(err <= bar), f"error {np.max(err / bar):.2f} of its bar"
