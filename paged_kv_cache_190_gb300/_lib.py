@@ -172,6 +172,20 @@ def _need_cuda_contig(name, t):
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
 
 
+def _workspace(nbytes, device, stream):
+    """Scratch that one call allocates itself, in memory of the stream that it runs on: the
+    allocator gives memory out again in the order of the stream it came from, so neither work
+    ahead of this call nor work behind it meets the same bytes."""
+    import torch
+    n = max(nbytes, 256)
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 class PreparedCall:
     """One C-ABI call with its arguments marshalled once.  Calling it enqueues
     the same call again -- same pointers, sizes and stream -- so the tensors it
@@ -284,7 +298,7 @@ def pa_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, num_k
         raise ValueError("num_kv_heads does not match the cache shape")
     if workspace is None:
         nbytes = pa_decode_workspace_size(B, Hq, Hkv, D, bs, max_context_len, chunk_tokens)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(nbytes, q.device, stream)
     call = PreparedCall("pa_decode", (
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
         float(scale), int(num_kv_heads), int(B), int(Hq), int(D), int(bs), int(NB),
@@ -314,7 +328,7 @@ def pa_decode_multi(out, q, k_cache, v_cache, block_tables, context_lens, scale,
         raise ValueError("num_kv_heads does not match the cache shape")
     if workspace is None:
         nbytes = pa_decode_workspace_size(B, q_len * Hq, Hkv, D, bs, max_context_len, chunk_tokens)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(nbytes, q.device, stream)
     call = PreparedCall("pa_decode_multi", (
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
         float(scale), int(num_kv_heads), int(B), int(Hq), int(q_len), int(D), int(bs), int(NB),
@@ -382,7 +396,7 @@ def pa_decode_cascade(out, q, k_cache, v_cache, block_tables, context_lens, grou
     if workspace is None:
         nbytes = pa_decode_cascade_workspace_size(B, G, Hq, Hkv, D, bs, max_context_len,
                                                   chunk_tokens)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(nbytes, q.device, stream)
     call = PreparedCall("pa_decode_cascade", (
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
         _ptr(group_start), _ptr(shared_lens), int(G), float(scale), int(num_kv_heads), int(B),
@@ -484,7 +498,7 @@ def pa_decode_fp8(out, q, k_cache, v_cache, block_tables, context_lens, scale, k
     _need_scales(k_scale, v_scale, Hkv)
     if workspace is None:
         nbytes = pa_decode_workspace_size(B, Hq, Hkv, D, bs, max_context_len, chunk_tokens)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(nbytes, q.device, stream)
     call = PreparedCall("pa_decode_fp8", (
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
         float(scale), _ptr(k_scale), _ptr(v_scale), int(num_kv_heads), int(B), int(Hq), int(D),
@@ -603,8 +617,7 @@ def pa_decode_window_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_di
 def _span_decode(name, fp8, out, q, k_cache, v_cache, block_tables, context_lens, scale, k_scales,
                  v_scales, num_kv_heads, max_context_len, window, sinks, workspace, device_errors,
                  stream, prepare):
-    own = workspace is None
-    if own:
+    if workspace is None:
         import torch
         if prepare:
             raise ValueError("a prepared call needs a workspace that outlives it")
@@ -615,14 +628,12 @@ def _span_decode(name, fp8, out, q, k_cache, v_cache, block_tables, context_lens
             nbytes = pa_decode_window_workspace_size(
                 q.shape[0], rows, num_kv_heads, q.shape[-1], k_cache.shape[2], max_context_len,
                 window, sinks)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(nbytes, q.device, stream)
     rc = (_step or _binding()).span_decode(
         fp8, out, q, k_cache, v_cache, block_tables, context_lens, scale, k_scales, v_scales,
         num_kv_heads, max_context_len, window, sinks, workspace, device_errors, stream, prepare)
     if prepare:
         return PreparedCall(name, rc)
-    if own and stream is not None:
-        workspace.record_stream(stream)     # not given out again before the call there is done
     if rc:
         _check(rc, name)
     return out

@@ -1,5 +1,7 @@
 """The windowed decode and the decode over page-scaled e4m3 pools on the GPU against the
 oracle; span_cases.Decode.bar has the error bars."""
+import types
+
 import numpy as np
 import pytest
 import torch
@@ -499,3 +501,27 @@ def test_bf16_weights_are_not_rounded_to_bf16(q_len, hq, hkv, d, bs, window, sin
     bar = 2.0 ** -8 * np.abs(want) + (2.0 ** -16 * 1.01 + rel) * parts["mag"] + 1e-37
     err = np.abs(out_as_f64(dv.out).reshape(want.shape) - want)
     assert np.all(err <= bar), f"error {np.max(err / bar):.2f} of its bar"
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_its_own_workspace_is_no_memory_that_the_current_stream_still_reads(dtype, raw):
+    """Memory freed on the current stream, of which a copy is still due there, is not the
+    workspace of a call on another stream."""
+    c = Decode(37, dtype, [int(x) for x in np.random.default_rng(6).integers(1, 400, 180)], 1, 4, 4, 128, 16)
+    dv = Dev(c)
+    dv.call()
+    nbytes = pa.pa_decode_window_workspace_size(len(c.lens), 4, 4, 128, 16, int(c.lens.max()))
+    side, again = torch.cuda.Stream(), torch.empty_like(dv.out)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    freed = torch.full((nbytes,), 17, dtype=torch.uint8, device=DEV)
+    copied = torch.empty_like(freed)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    copied.copy_(freed)
+    del freed
+    dv.call(again, stream=types.SimpleNamespace(cuda_stream=side.cuda_stream) if raw else side)
+    torch.cuda.synchronize()
+    assert bool((copied == 17).all())
+    assert torch.equal(again.view(torch.int16), dv.out.view(torch.int16))
