@@ -401,9 +401,14 @@ int pa_rope_and_cache_fp8(void* q_out, const void* q, const void* k, const void*
  *     rows are re-encoded: code' = e4m3(code * old / new).
  * The rows are stored as e4m3(x / scale) (float32 division, nearest, ties to even,
  * magnitudes above 448 and infinities saturate, NaN stores a NaN code).  The tokens
- * that one call puts into a page must stand one after another in the batch (as a
- * sequence's tokens do) and have distinct slots; more of them than the page has
- * slots set PA_DEVERR_BAD_SLOT, and those past the page's size are dropped.
+ * that one call puts into a page must have distinct slots and stand one after another
+ * in the batch (as a sequence's tokens do), the last at most 48 behind the first; tokens
+ * that are not written (padding, a negative slot, a refused position or slot) may stand
+ * between them.  What does not keep to this is dropped and sets PA_DEVERR_BAD_SLOT: more
+ * tokens than the page has slots (those past the page's size), tokens further behind the
+ * page's first, and tokens that come back to a page behind another page's.  The last is
+ * seen for pages of the 192 tokens before; tokens that come back from further off than
+ * that are not refused and leave the page's rows under different scales.
  *
  * pa_decode_fp8_block: decode over such pools for q_len new tokens per sequence,
  * causal among them, with the window and sinks of pa_decode_window (0, 0 for none);

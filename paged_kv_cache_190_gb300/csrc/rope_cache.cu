@@ -294,9 +294,11 @@ __global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const RopeArgs
 
 // ------------------------------------------------ a scale for each page and head
 //
-// The tokens that a call puts into one page stand one after another in the batch: a
-// run.  One warp takes a run's rows of one head, of K or of V: it rotates them,
-// finds their largest magnitude, and from it the page's scale
+// The tokens that a call puts into one page stand one after another in the batch, other
+// than tokens that are not written: a run.  A warp takes a head's K and V row of a run of
+// one token, a block the rows of up to eight heads of K or of V of a longer one (1 to 8
+// warps a head): they rotate the rows, find a head's largest magnitude, and from it the
+// page's scale
 //   s = 2^k, the least k >= -100 with amax <= 448 2^k
 // (a power of two: e4m3 has the same relative steps at every such scale, codes move
 // from one scale to another without a second rounding unless they fall below the
@@ -344,18 +346,129 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
   return e4m3x4(f[0].x * ratio, f[0].y * ratio, f[1].x * ratio, f[1].y * ratio);
 }
 
-// Tokens around a tile, as its block sees them: token t0 - 1 + i in entry i.
+// Tokens around a tile, as its block sees them, a thread each: token t0 - kBefore + i is
+// entry i.  A run is a page's written tokens with no other page's written token between them,
+// the last at most kBehind behind the first; the tile where it starts has it.  Tokens that
+// keep to no such run would give a page two owners and are refused: what is more than
+// kBehind behind its run's start, and runs of a page that one of the kBefore tokens ahead of
+// the tile, or of the tile's, has already begun.  (0.15 us of a decode step.)
 constexpr int kTile = 16;
-constexpr int kSeenTokens = 1 + kTile + 32;                // one before, a run's length behind
-struct TileTokens {
-  int64_t page[kSeenTokens];                               // -1: not written
-  int64_t pos[kSeenTokens];
-  int off[kSeenTokens];
-  // the runs that start in the tile, in entry j that of token t0 + j: its length (0: no
-  // start); and the starts of the runs of one token and of those of more
-  int length[kTile], ones[kTile], more[kTile];
+constexpr int kBehind = 48;                               // a page's 32 and 16 more
+constexpr int kBefore = kPageThreads - kTile - kBehind;
+constexpr int kWords = kPageThreads / 32;
+static_assert(kBefore == 192 && kTile + kBehind == 64 && kWords == 8, "the tile and what is behind it: words 6 and 7");
+struct Words {                                             // eight words of shared memory, in registers
+  uint32_t x[kWords];
+  __device__ __forceinline__ explicit Words(const uint32_t* p) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 4);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+  __device__ __forceinline__ uint64_t two(int k) const { return (static_cast<uint64_t>(x[k + 1]) << 32) | x[k]; }
+};
+struct __align__(16) TileTokens {
+  int page_of[kPageThreads];                               // by entry; -1: not written
+  uint32_t live[kWords], starts[kWords], again[kWords];
+  // the written tokens from t0 on, in order
+  int64_t pos[kTile + kBehind];
+  int page[kTile + kBehind];
+  uint8_t token[kTile + kBehind], off[kTile + kBehind];     // token: behind t0
+  // the runs that start in the tile, as their first's place among those: the runs of one
+  // token, and those of more with their lengths
+  int ones[kTile], more[kTile], length[kTile];
   int num_ones, num_more;
 };
+
+// The block looks its tokens up and finds the tile's runs.
+__device__ __forceinline__ void find_runs(const RopeArgs& a, TileTokens& seen, int t0, int block_size, bool speak) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, i = threadIdx.x;
+  const int64_t t = static_cast<int64_t>(t0) - kBefore + i;
+  int page = -1, off = 0;
+  int64_t pos = 0;
+  if (t >= 0 && t < a.num_tokens) {
+    const Place p = place(a, static_cast<int>(t), speak && i >= kBefore && i < kBefore + kTile);
+    if (p.write) {
+      page = static_cast<int>(p.slot >> a.block_log2);
+      off = static_cast<int>(p.slot) & (block_size - 1);
+      pos = p.pos;
+    }
+  }
+  seen.page_of[i] = page;
+  const uint32_t live = __ballot_sync(0xffffffffu, page >= 0), below = (1u << lane) - 1;
+  if (lane == 0) seen.live[warp] = live;
+  __syncthreads();
+  // a start: the written token before it is another page's
+  const Words all(seen.live);
+  if (warp >= 4) {                                         // (those of words 0-3 are not needed)
+    int w = warp;
+    uint32_t earlier = live & below;
+#pragma unroll
+    for (int k = kWords - 2; k >= 0; --k)
+      if (earlier == 0 && k < warp) {
+        w = k;
+        earlier = all.x[k];
+      }
+    const bool start = page >= 0 && (earlier == 0 || seen.page_of[32 * w + 31 - __clz(earlier)] != page);
+    const uint32_t starts = __ballot_sync(0xffffffffu, start);
+    if (lane == 0) seen.starts[warp] = starts;
+  }
+  // bit j: token t0 + j comes behind this one in the same page
+  uint32_t same = 0;
+#pragma unroll
+  for (int j = 0; j < kTile; j += 4) {
+    const int4 q = *reinterpret_cast<const int4*>(seen.page_of + kBefore + j);
+    same |= ((q.x == page ? 1u : 0u) | (q.y == page ? 2u : 0u) | (q.z == page ? 4u : 0u) | (q.w == page ? 8u : 0u)) << j;
+  }
+  if (page < 0 || i >= kBefore + kTile)
+    same = 0;
+  else if (i >= kBefore)
+    same &= ~1u << (i - kBefore);
+  same = __reduce_or_sync(0xffffffffu, same);
+  if (lane == 0) seen.again[warp] = same;
+  if (i >= kBefore && page >= 0) {
+    const int c = __popc(live & below) + (warp == 7 ? __popc(all.x[6]) : 0);
+    seen.pos[c] = pos;
+    seen.token[c] = i - kBefore;
+    seen.page[c] = page;
+    seen.off[c] = off;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const Words starts(seen.starts), back(seen.again);
+    const uint64_t lives = all.two(6), begins = starts.two(6), before = starts.two(4);
+    uint32_t agains = 0;
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) agains |= back.x[k];
+    const uint64_t passed = (1ull << lane) - 1;
+    int n = 0;
+    bool refused = false;
+    if (lane < kTile && ((lives >> lane) & 1u)) {
+      if ((begins >> lane) & 1u) {
+        const uint64_t later = begins >> lane >> 1;        // starts behind this one
+        const int most = min(later ? __ffsll(static_cast<long long>(later)) : 64, kBehind + 1);
+        n = __popcll((lives >> lane) & ((1ull << most) - 1));
+        refused = n > block_size || ((agains >> lane) & 1u);   // more tokens than slots
+        n = (agains >> lane) & 1u ? 0 : min(n, block_size);
+      } else {
+        // its run starts in the tile, or in entry kBefore - 64 + k for bit k of `before`
+        refused = (begins & passed) == 0 && before >> (64 - kBehind + lane) == 0;
+      }
+    }
+    if (refused && speak) report(a.device_errors, PA_DEVERR_BAD_SLOT);
+    const uint32_t ones = __ballot_sync(0xffffffffu, n == 1), more = __ballot_sync(0xffffffffu, n > 1);
+    const int c = __popcll(lives & passed);
+    if (n == 1) seen.ones[__popc(ones & below)] = c;
+    if (n > 1) {
+      seen.more[__popc(more & below)] = c;
+      seen.length[__popc(more & below)] = n;
+    }
+    if (lane == 0) {
+      seen.num_ones = __popc(ones);
+      seen.num_more = __popc(more);
+    }
+  }
+  __syncthreads();
+}
 
 // A copy of 16 bytes to shared memory that nothing waits for until fetched().
 __device__ __forceinline__ void fetch16(void* smem, const void* src) {
@@ -377,8 +490,7 @@ constexpr int kRunBytes = kKeptRows * (kHeadsPerItem * 256 + 128 * 4);
 
 template <bool INTER, int BS>
 __device__ __forceinline__ void append_run(const RopeArgs& a, const TileTokens& seen, unsigned char* buf, float* tops,
-                                           int64_t t, int first, int n, uint32_t offsets, int64_t page, int h0,
-                                           int heads, bool is_v) {
+                                           int t0, int first, int n, uint32_t offsets, int h0, int heads, bool is_v) {
   constexpr int N = 8, D = 128;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int l = lane % kLanesPerRow, row = lane / kLanesPerRow;
@@ -389,9 +501,9 @@ __device__ __forceinline__ void append_run(const RopeArgs& a, const TileTokens& 
   const bool fresh = offsets & 1u;
   const bool turned = !is_v && a.rot_dim > 0;
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
-  const uint16_t* src = static_cast<const uint16_t*>(is_v ? a.v : a.k) + t * stride + static_cast<int64_t>(h0) * D;
+  const uint16_t* src = static_cast<const uint16_t*>(is_v ? a.v : a.k) + t0 * stride + static_cast<int64_t>(h0) * D;
   float* table = reinterpret_cast<float*>(buf + kKeptRows * kHeadsPerItem * 256);
-  const int64_t head_page = page * a.num_kv_heads + h0 + hh;
+  const int64_t head_page = static_cast<int64_t>(seen.page[first]) * a.num_kv_heads + h0 + hh;
   float* scale = (is_v ? a.v_scales : a.k_scales) + head_page;
   const LaneChunks<N, D, INTER> lc(l, is_v ? 0 : a.rot_dim);
 
@@ -399,7 +511,7 @@ __device__ __forceinline__ void append_run(const RopeArgs& a, const TileTokens& 
     // a token a warp (no divisions: they were most of the instructions here)
     const int cpr = heads * 16, tpr = a.rot_dim / 4;       // 16-byte chunks of a token: rows, table row
     for (int r = warp; r < m; r += kWarps) {
-      const uint16_t* from = src + (r0 + r) * stride + lane * N;
+      const uint16_t* from = src + seen.token[first + r0 + r] * stride + lane * N;
       unsigned char* to = buf + (r * cpr + lane) * 16;
       for (int c = lane; c < cpr; c += 32, from += 32 * N, to += 32 * 16) fetch16(to, from);
       if (turned && lane < tpr)
@@ -578,7 +690,9 @@ __global__ void __launch_bounds__(kPageThreads, 3) rope_and_cache_page_scale_ker
     int item_heads) {
   __shared__ TileTokens seen;
   __shared__ float tops[kWarps];
-  extern __shared__ __align__(16) unsigned char run_buf[];
+  // (whole lines: 16 bytes past a sector's border a copy fetches each sector twice, 35.0 us
+  // for 8192 tokens instead of 33.6)
+  extern __shared__ __align__(128) unsigned char run_buf[];
   wait_prior_grids();
   allow_next_grid();
   unsigned kv = blockIdx.x, qb = blockIdx.x - kv_blocks;
@@ -599,56 +713,10 @@ __global__ void __launch_bounds__(kPageThreads, 3) rope_and_cache_page_scale_ker
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int tile = kv / parts, part = kv - tile * parts;
   const int t0 = tile * kTile;
-  if (threadIdx.x < 64) {
-    const int i = threadIdx.x;
-    const int64_t t = static_cast<int64_t>(t0) - 1 + i;
-    int64_t page = -1, pos = 0;
-    int off = 0;
-    if (t >= 0 && t < a.num_tokens && i < kSeenTokens) {
-      const Place p = place(a, static_cast<int>(t), part == 0 && i > 0 && i <= kTile);
-      if (p.write) {
-        page = p.slot / BS;
-        off = static_cast<int>(p.slot - page * BS);
-        pos = p.pos;
-      }
-    }
-    if (i < kSeenTokens) {
-      seen.page[i] = page;
-      seen.off[i] = off;
-      seen.pos[i] = pos;
-    }
-  }
-  __syncthreads();
-  if (warp == 0) {
-    // bit i: entry i goes on with the page of entry i - 1
-    auto goes_on = [&](int i) {
-      return i > 0 && i < kSeenTokens && seen.page[i] >= 0 && seen.page[i] == seen.page[i - 1];
-    };
-    const uint32_t low = __ballot_sync(0xffffffffu, goes_on(lane)), high = __ballot_sync(0xffffffffu, goes_on(32 + lane));
-    const uint64_t on = (static_cast<uint64_t>(high) << 32) | low;
-    const int i = lane + 1;
-    int n = 0;
-    if (lane < kTile && seen.page[i] >= 0 && !((on >> i) & 1u)) {
-      n = __ffsll(static_cast<long long>(~(on >> (i + 1))));
-      if (n > BS) {
-        n = BS;                                            // more tokens than slots: refused
-        report(a.device_errors, PA_DEVERR_BAD_SLOT);
-      }
-    }
-    const uint32_t ones = __ballot_sync(0xffffffffu, n == 1), more = __ballot_sync(0xffffffffu, n > 1);
-    const uint32_t before = (1u << lane) - 1;
-    if (lane < kTile) seen.length[lane] = n;
-    if (n == 1) seen.ones[__popc(ones & before)] = lane;
-    if (n > 1) seen.more[__popc(more & before)] = lane;
-    if (lane == 0) {
-      seen.num_ones = __popc(ones);
-      seen.num_more = __popc(more);
-    }
-  }
-  __syncthreads();
+  find_runs(a, seen, t0, BS, part == 0);
   for (int k = part * kWarps + warp; k < seen.num_ones * a.num_kv_heads; k += parts * kWarps) {
     const int j = k / a.num_kv_heads, at = seen.ones[j];
-    append_one<INTER, BS>(a, static_cast<int64_t>(t0) + at, seen.pos[at + 1], seen.off[at + 1], seen.page[at + 1],
+    append_one<INTER, BS>(a, static_cast<int64_t>(t0) + seen.token[at], seen.pos[at], seen.off[at], seen.page[at],
                           k - j * a.num_kv_heads);
   }
   if (seen.num_more == 0) return;                          // (a decode step)
@@ -659,15 +727,14 @@ __global__ void __launch_bounds__(kPageThreads, 3) rope_and_cache_page_scale_ker
   const int groups = (a.num_kv_heads + item_heads - 1) / item_heads;
   for (int j = 0, m = part;; m += parts) {
     for (; j < seen.num_more; ++j) {
-      const int items = 2 * (seen.length[seen.more[j]] > 8 ? groups : few_groups);
+      const int items = 2 * (seen.length[j] > 8 ? groups : few_groups);
       if (m < items) break;
       m -= items;
     }
     if (j >= seen.num_more) break;
-    const int at = seen.more[j], n = seen.length[at], h0 = (m >> 1) * heads_of(n);
-    const uint32_t offsets = __reduce_or_sync(0xffffffffu, lane < n ? 1u << seen.off[at + 1 + lane] : 0u);
-    append_run<INTER, BS>(a, seen, run_buf, tops, static_cast<int64_t>(t0) + at, at + 1, n, offsets, seen.page[at + 1],
-                          h0, min(heads_of(n), a.num_kv_heads - h0), m & 1);
+    const int at = seen.more[j], n = seen.length[j], h0 = (m >> 1) * heads_of(n);
+    const uint32_t offsets = __reduce_or_sync(0xffffffffu, lane < n ? 1u << seen.off[at + lane] : 0u);
+    append_run<INTER, BS>(a, seen, run_buf, tops, t0, at, n, offsets, h0, min(heads_of(n), a.num_kv_heads - h0), m & 1);
   }
 }
 

@@ -70,3 +70,21 @@ class Append:
         """Slot of each token, -1 where nothing is written."""
         ok = self.live() & (self.slots < self.nb * self.bs)
         return np.where(ok, self.slots, -1)
+
+
+def kept_in_pages(slots, bs, behind=48):
+    """Which tokens a page-scaled append writes, of those with a slot (>= 0): a page's tokens
+    one after another but for unwritten ones, no more than the page's size, none more than
+    `behind` behind the first, none of a page that another page's tokens have interrupted."""
+    kept, begun = np.zeros(len(slots), bool), set()
+    page = start = count = None
+    for t, s in enumerate(slots):
+        if s < 0:
+            continue
+        if s // bs != page:
+            page, start, count, fresh = s // bs, t, 0, s // bs not in begun
+            begun.add(page)
+        if fresh and t - start <= behind and count < bs:
+            kept[t] = True
+            count += 1
+    return kept

@@ -345,3 +345,55 @@ def test_a_few_tokens_of_many_sequences(hkv, seqs, most, bs):
     d = Dev(c)
     assert d.call() == 0
     _check(c, d)
+
+
+def _append_as_kept(c, sizes, flags):
+    """A page-scaled append of rows of very different sizes (scales grow and do not): written
+    are the tokens that rope_cases.kept_in_pages names."""
+    c.qkv[:] = rope_cases.storage(rope_cases.values(c.qkv) * sizes[:, None].astype(np.float32), "bf16")
+    w = np.where(c.live() & (c.slots < c.nb * c.bs), c.slots, -1)
+    kept = np.where(rope_cases.kept_in_pages(w, c.bs), w, -1)
+    c.written = lambda: kept
+    d = Dev(c)
+    assert d.call() == flags
+    _check(c, d)
+
+
+@pytest.mark.parametrize("kind", ["no slot", "padding", "bad position", "bad slot"])
+@pytest.mark.parametrize("bs", [16, 32])
+@pytest.mark.parametrize("had,new,hkv", [(0, 5, 2), (3, 4, 1), (0, 40, 8), (7, 200, 3), (20, 2, 8)])
+def test_tokens_that_are_not_written_inside_a_page(kind, bs, had, new, hkv):
+    """They leave a page's tokens one run, with one scale: of one warp or block, in one tile
+    or two, and more than one of them in a row."""
+    slots, pos, nb = _run_of([(had, new), (5, 3)], bs, new)
+    r = np.random.default_rng(had + new)
+    at = np.sort(r.choice(np.arange(1, new), max(1, new // 6), replace=False))
+    at = np.repeat(at, np.where(np.arange(len(at)) % 5 == 1, 4, 1))
+    out_slot, out_pos = {"no slot": (-1, 5), "padding": (7, -1), "bad position": (7, 256), "bad slot": (nb * bs, 5)}[kind]
+    slots, pos = np.insert(slots, at, out_slot), np.insert(pos, at, out_pos)
+    c = rope_cases.Append(new + bs, "fp8_block", len(slots), 2, hkv, 128, 64, bs, nb, max_position=256, slots=slots,
+                          positions=pos)
+    flags = {"bad position": pa.PA_DEVERR_BAD_POSITION, "bad slot": pa.PA_DEVERR_BAD_SLOT}.get(kind, 0)
+    _append_as_kept(c, 2.0 ** r.integers(-8, 8, len(slots)), flags)
+
+
+@pytest.mark.parametrize("bs", [16, 32])
+@pytest.mark.parametrize("seqs,steps,hkv", [(2, 2, 2), (3, 5, 8), (40, 3, 1), (90, 2, 4), (150, 4, 2)])
+def test_tokens_that_come_back_to_a_page_are_refused(bs, seqs, steps, hkv):
+    """Drafted tokens laid out step by step instead of sequence by sequence."""
+    slots = [b * bs + 2 + s for s in range(steps) for b in range(seqs)]
+    c = rope_cases.Append(seqs, "fp8_block", len(slots), 4, hkv, 128, 128, bs, seqs + 1, slots=slots,
+                          positions=[2 + s for s in range(steps) for _ in range(seqs)])
+    assert rope_cases.kept_in_pages(slots, bs).sum() == seqs
+    _append_as_kept(c, 2.0 ** np.random.default_rng(seqs).integers(-8, 8, len(slots)), pa.PA_DEVERR_BAD_SLOT)
+
+
+@pytest.mark.parametrize("first", [0, 9, 15])
+@pytest.mark.parametrize("gap,refused", [(45, 0), (46, 1), (47, 2), (100, 2)])
+def test_tokens_far_behind_their_page(gap, refused, first):
+    """Two tokens of a page, `gap` padding tokens, two more: the third is gap + 2 behind."""
+    slots = [0] * first + [16, 17] + [0] * gap + [18, 19, 33]
+    pos = [-1] * first + [0, 1] + [-1] * gap + [2, 3, 0]
+    c = rope_cases.Append(gap, "fp8_block", len(slots), 2, 3, 128, 128, 16, 3, slots=slots, positions=pos)
+    assert rope_cases.kept_in_pages(np.where(np.array(pos) < 0, -1, slots), 16).sum() == 5 - refused
+    _append_as_kept(c, np.array([2.0 ** (i % 7) for i in range(len(slots))]), pa.PA_DEVERR_BAD_SLOT if refused else 0)
