@@ -6,13 +6,15 @@ objects are linked by nvcc into ``paged_kv_cache_190_gb300/libpagedattn.so``
 (CUDA runtime linked statically, so the library loads on a machine without a
 GPU driver and its block manager works there).  The per-step calls have a C++
 binding for Python, ``_step.so`` beside it, compiled by g++ against torch's headers and
-linked to libpagedattn.so.
+linked to libpagedattn.so; a machine without torch or Python's headers builds the library
+alone.
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
@@ -47,6 +49,18 @@ def _headers():
     hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     hs.append(os.path.join(os.path.dirname(PKG), "include", "pa.h"))
     return hs
+
+
+def _no_binding():
+    """Why the Python binding cannot be built here, or None."""
+    try:
+        import torch  # noqa: F401
+    except (ImportError, OSError) as e:
+        return f"torch cannot be imported ({e})"
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        return f"no Python.h in {include}"
+    return None
 
 
 def _binding_command(obj: str):
@@ -89,7 +103,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or _newer(o, [s] + headers):
             jobs.append(["g++", "-O2", "-std=c++17", "-fPIC", "-c", s, "-o", o])
     binding_obj = os.path.join(OUT_DIR, "step_binding.cpp.o")
-    if force or _newer(binding_obj, [BINDING_SOURCE] + headers):
+    why_not = _no_binding()
+    if why_not:
+        print(f"libpagedattn: the Python binding of the per-step calls is not built: {why_not}", file=sys.stderr)
+    elif force or _newer(binding_obj, [BINDING_SOURCE] + headers):
         jobs.insert(0, _binding_command(binding_obj))          # the longest of them first
 
     def run(cmd):
@@ -108,7 +125,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    if force or _newer(BINDING, [binding_obj]):
+    if not why_not and (force or _newer(BINDING, [binding_obj])):
         tmp = BINDING + f".tmp{os.getpid()}"
         run(_binding_link(binding_obj, tmp))
         os.replace(tmp, BINDING)
@@ -116,5 +133,4 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
