@@ -5,9 +5,9 @@ Each CUDA translation unit is compiled by nvcc in parallel with
 objects are linked by nvcc into ``paged_kv_cache_190_gb300/libpagedattn.so``
 (CUDA runtime linked statically, so the library loads on a machine without a
 GPU driver and its block manager works there).  The per-step calls have a C++
-binding for Python, ``_step.so`` beside it, compiled by g++ against torch's headers and
-linked to libpagedattn.so; a machine without torch or Python's headers builds the library
-alone.
+binding for Python beside it, compiled by g++ against torch's headers and linked to
+libpagedattn.so; its file name has the versions of torch and of the interpreter that it
+serves.  A machine without torch or Python's headers builds the library alone.
 """
 from __future__ import annotations
 
@@ -22,7 +22,6 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedattn.so")
-BINDING = os.path.join(PKG, "_step.so")
 BINDING_SOURCE = os.path.join(CSRC, "step_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CU_SOURCES = ["capi.cu", "cache_ops.cu", "decode_launch.cu", "decode_bf16.cu", "decode_f32.cu",
@@ -61,6 +60,12 @@ def _no_binding():
     if not os.path.exists(os.path.join(include, "Python.h")):
         return f"no Python.h in {include}"
     return None
+
+
+def binding_path() -> str:
+    """The Python binding for this interpreter and the torch that it imports."""
+    import torch
+    return os.path.join(PKG, f"_step.torch-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def _binding_command(obj: str):
@@ -102,12 +107,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(o)
         if force or _newer(o, [s] + headers):
             jobs.append(["g++", "-O2", "-std=c++17", "-fPIC", "-c", s, "-o", o])
-    binding_obj = os.path.join(OUT_DIR, "step_binding.cpp.o")
     why_not = _no_binding()
     if why_not:
         print(f"libpagedattn: the Python binding of the per-step calls is not built: {why_not}", file=sys.stderr)
-    elif force or _newer(binding_obj, [BINDING_SOURCE] + headers):
-        jobs.insert(0, _binding_command(binding_obj))          # the longest of them first
+    else:
+        binding = binding_path()
+        binding_obj = os.path.join(OUT_DIR, os.path.basename(binding) + ".o")
+        if force or _newer(binding_obj, [BINDING_SOURCE] + headers):
+            jobs.insert(0, _binding_command(binding_obj))      # the longest of them first
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -125,10 +132,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    if not why_not and (force or _newer(BINDING, [binding_obj])):
-        tmp = BINDING + f".tmp{os.getpid()}"
+    if not why_not and (force or _newer(binding, [binding_obj])):
+        tmp = binding + f".tmp{os.getpid()}"
         run(_binding_link(binding_obj, tmp))
-        os.replace(tmp, BINDING)
+        os.replace(tmp, binding)
     return LIB
 
 

@@ -520,12 +520,17 @@ _step = None
 def _binding():
     global _step
     if _step is None:
+        import importlib.util
+        import torch
+        from ._build import binding_path
         library()
-        try:
-            from . import _step as module
-        except ImportError as e:
-            raise RuntimeError("the per-step binding has not been built for this interpreter: build it "
-                               "with `python -c \"import __graft_entry__ as g; g.build()\"`") from e
+        path = binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"the per-step binding has not been built for torch {torch.__version__} and this "
+                               "interpreter: build it with `python -c \"import __graft_entry__ as g; g.build()\"`")
+        spec = importlib.util.spec_from_file_location(f"{__package__}._step", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
         _step = module
     return _step
 

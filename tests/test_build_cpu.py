@@ -38,3 +38,19 @@ def test_the_library_builds_without_python_headers(monkeypatch, only_the_binding
 def test_a_binding_that_does_not_compile_is_an_error(monkeypatch, only_the_binding):
     with pytest.raises(AssertionError):
         _build.build()
+
+
+def test_a_binding_belongs_to_one_torch_and_one_interpreter(monkeypatch):
+    """A torch or a Python that was changed finds no binding made for another one."""
+    import torch
+    from paged_kv_cache_190_gb300 import _lib
+    here = _build.binding_path()
+    assert os.path.exists(here) and here.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    monkeypatch.setattr(_lib, "_step", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    assert _build.binding_path() != here
+    with pytest.raises(RuntimeError, match="0.0.1.other"):
+        _lib._binding()
+    monkeypatch.undo()
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: ".cpython-399-other.so")
+    assert _build.binding_path() != here
