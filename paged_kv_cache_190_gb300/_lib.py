@@ -522,16 +522,21 @@ def _binding():
     if _step is None:
         import importlib.util
         import torch
-        from ._build import binding_path
+        from . import _build
         library()
-        path = binding_path()
+        path = _build.binding_path()
         if not os.path.exists(path):
             raise RuntimeError(f"the per-step binding has not been built for torch {torch.__version__} and this "
                                "interpreter: build it with `python -c \"import __graft_entry__ as g; g.build()\"`")
-        spec = importlib.util.spec_from_file_location(f"{__package__}._step", path)
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
-        _step = module
+        with _lock:
+            if _step is None:
+                spec = importlib.util.spec_from_file_location(f"{__package__}._step", path)
+                try:
+                    module = importlib.util.module_from_spec(spec)
+                    spec.loader.exec_module(module)
+                except ImportError as e:
+                    raise RuntimeError(f"the per-step binding does not load: {e}") from e
+                _step = module
     return _step
 
 

@@ -54,3 +54,27 @@ def test_a_binding_belongs_to_one_torch_and_one_interpreter(monkeypatch):
     monkeypatch.undo()
     monkeypatch.setattr(sysconfig, "get_config_var", lambda name: ".cpython-399-other.so")
     assert _build.binding_path() != here
+
+
+def test_a_binding_that_does_not_load_says_why(monkeypatch, tmp_path):
+    from paged_kv_cache_190_gb300 import _lib
+    bad = tmp_path / "_step.so"
+    bad.write_bytes(b"no library")
+    monkeypatch.setattr(_lib, "_step", None)
+    monkeypatch.setattr(_build, "binding_path", lambda: str(bad))
+    with pytest.raises(RuntimeError, match=f"does not load.*{bad}"):
+        _lib._binding()
+    assert _lib._step is None
+
+
+def test_the_first_calls_of_two_threads_load_one_binding(monkeypatch):
+    import threading
+    from paged_kv_cache_190_gb300 import _lib
+    monkeypatch.setattr(_lib, "_step", None)
+    got = []
+    threads = [threading.Thread(target=lambda: got.append(_lib._binding())) for _ in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(got) == 8 and len({id(m) for m in got}) == 1
