@@ -397,3 +397,63 @@ def test_tokens_far_behind_their_page(gap, refused, first):
     c = rope_cases.Append(gap, "fp8_block", len(slots), 2, 3, 128, 128, 16, 3, slots=slots, positions=pos)
     assert rope_cases.kept_in_pages(np.where(np.array(pos) < 0, -1, slots), 16).sum() == 5 - refused
     _append_as_kept(c, np.array([2.0 ** (i % 7) for i in range(len(slots))]), pa.PA_DEVERR_BAD_SLOT if refused else 0)
+
+
+@pytest.mark.parametrize("factor", [1.25, 1 / 3, 1.75])
+@pytest.mark.parametrize("size", [2.0 ** -12, 1.0, 2.0 ** 6])
+@pytest.mark.parametrize("new,bs,hkv", [(1, 16, 8), (1, 32, 3), (7, 16, 8), (20, 32, 2), (9, 16, 1)])
+def test_pages_that_go_on_under_any_scale(new, bs, hkv, size, factor):
+    """Old scales that are no powers of two: kept, rows are divided by them; outgrown, the
+    rows of the page come to the new one by the rounded quotient."""
+    slots, pos, nb = _run_of([(5, new), (11, new)], bs, new)
+    c = rope_cases.Append(new + bs, "fp8_block", len(slots), 2, hkv, 128, 96, bs, nb, slots=slots, positions=pos)
+    for s in (c.k_scales, c.v_scales):
+        s *= np.float32(factor)
+    c.qkv[:] = rope_cases.storage(rope_cases.values(c.qkv) * np.float32(size), "bf16")
+    d = Dev(c)
+    assert d.call() == 0
+    _check(c, d)
+
+
+def _special_rows(tokens, hkv):
+    """A head each of zeros, subnormals, infinities, NaN, the largest finite values."""
+    x = np.random.default_rng(tokens).standard_normal((tokens, 2 * hkv, 128)).astype(np.float32)
+    for base in (0, hkv):
+        x[:, base] = 0.0
+        x[:, base + 1] = 1e-39
+        x[tokens // 3, base + 2, 5], x[tokens // 2, base + 2, 70], x[-1, base + 2, 7] = np.inf, -np.inf, np.nan
+        x[:, base + 3] = 3.3e38
+        x[:, base + 4] = -1e-30
+        x[:, base + 5, 1:] = np.nan
+        x[:, base + 6] = np.inf
+    return x
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("each", [1, 2, 16])
+@pytest.mark.parametrize("rot", [128, 48])
+def test_special_values_that_turn(inter, each, rot):
+    """The special values through the rotation, `each` tokens a call into one page."""
+    hkv, bs, nb = 8, 16, 2
+    rows = _special_rows(16, hkv)
+    state = None
+    for at in range(0, 16, each):
+        c = rope_cases.Append(at, "fp8_block", each, 0, hkv, 128, rot, bs, nb, interleaved=inter,
+                              slots=[16 + at + i for i in range(each)], positions=[3 + at + i for i in range(each)])
+        c.qkv[:] = rope_cases.storage(rows[at:at + each].reshape(each, -1), "bf16")
+        if state is not None:
+            c.k_cache, c.k_scales, c.v_cache, c.v_scales = state
+        d = Dev(c)
+        pa.pa_rope_and_cache_fp8_block(None, None, d.k, d.v, d.kc, d.vc, d.slots, d.pos, d.table, *d.scale,
+                                       interleaved=inter, device_errors=d.errs)
+        assert pa.pa_read_device_errors(d.errs) == 0
+        with np.errstate(all="ignore"):
+            oracle.page_scale_append(c.rotated32(c.k), c.slots, c.k_cache, c.k_scales)
+            oracle.page_scale_append(rope_cases.values(c.v), c.slots, c.v_cache, c.v_scales)
+        for cache, s, got, gs in ((c.k_cache, c.k_scales, d.kc, d.scale[0]), (c.v_cache, c.v_scales, d.vc, d.scale[1])):
+            np.testing.assert_array_equal(storage_to_host(gs, "f32"), s)
+            g = storage_to_host(got, "fp8")
+            nan = (cache & 0x7F) == 0x7F
+            np.testing.assert_array_equal(g[~nan], cache[~nan])
+            assert np.all((g[nan] & 0x7F) == 0x7F)
+        state = c.k_cache, c.k_scales, c.v_cache, c.v_scales

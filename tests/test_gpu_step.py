@@ -236,3 +236,35 @@ def test_the_first_call_of_a_process_may_be_captured():
     root = pathlib.Path(__file__).resolve().parent.parent
     done = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_the_pools_hold_what_was_written_and_nothing_else(fp8):
+    """Prompts, a fork, copy-on-write and decode steps, then every byte of the pools: slots
+    that nothing was written to are as they were."""
+    loop = Loop(fp8)
+    bm = loop.bm
+    slots, pos = [], []
+    for s, n in {1: 70, 2: 1, 3: 33}.items():
+        bm.add_seq(s)
+        for p in range(n):
+            slots.append(bm.append_slot(s)[0])
+            pos.append(p)
+    loop.append(slots, pos)
+    bm.fork(1, 9)
+    ids = [1, 2, 3, 9]
+    for _ in range(20):
+        lens = [bm.block_table(s)[1] for s in ids]
+        new, cow = bm.append_slots(ids)
+        loop.copy(cow)
+        loop.attend(ids, loop.append(new, lens), 1, 24, 3)
+    assert pa.pa_read_device_errors(loop.errs) == 0
+    for dev, host in zip(loop.pools, loop.host):
+        got = storage_to_host(dev, "fp8" if fp8 else "bf16")
+        nan = (host & 0x7F) == 0x7F if fp8 else np.zeros(host.shape, bool)     # a NaN code's sign is free
+        np.testing.assert_array_equal(got[~nan], host[~nan])
+        assert np.all((got[nan] & 0x7F) == 0x7F)
+        assert np.any(host == (0x7F if fp8 else 0x7FC0))
+    if fp8:
+        for dev, host in zip(loop.scales, loop.host_scales):
+            np.testing.assert_array_equal(storage_to_host(dev, "f32"), host)
