@@ -191,12 +191,13 @@ class PreparedCall:
     the same call again -- same pointers, sizes and stream -- so the tensors it
     was made from must stay alive and in place.  The device-op wrappers below
     return one instead of calling when given ``prepare=True``: for loops that
-    issue the same step over and over with no per-call argument checks."""
+    issue the same step over and over with no per-call argument checks.
+    ``keep``: the workspace, which the wrapper may have allocated."""
 
-    __slots__ = ("name", "fn", "args")
+    __slots__ = ("name", "fn", "args", "keep")
 
-    def __init__(self, name, args):
-        self.name, self.fn, self.args = name, getattr(library(), name), args
+    def __init__(self, name, args, keep=None):
+        self.name, self.fn, self.args, self.keep = name, getattr(library(), name), args, keep
 
     def __call__(self):
         rc = self.fn(*self.args)
@@ -304,7 +305,7 @@ def pa_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, num_k
         float(scale), int(num_kv_heads), int(B), int(Hq), int(D), int(bs), int(NB),
         int(block_tables.shape[1]), int(max_context_len), _dtype_code(q), int(chunk_tokens),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(device_errors),
-        _stream(stream, q.device)))
+        _stream(stream, q.device)), workspace)
     if prepare:
         return call
     call()
@@ -334,7 +335,7 @@ def pa_decode_multi(out, q, k_cache, v_cache, block_tables, context_lens, scale,
         float(scale), int(num_kv_heads), int(B), int(Hq), int(q_len), int(D), int(bs), int(NB),
         int(block_tables.shape[1]), int(max_context_len), _dtype_code(q), int(chunk_tokens),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(device_errors),
-        _stream(stream, q.device)))
+        _stream(stream, q.device)), workspace)
     if prepare:
         return call
     call()
@@ -402,7 +403,7 @@ def pa_decode_cascade(out, q, k_cache, v_cache, block_tables, context_lens, grou
         _ptr(group_start), _ptr(shared_lens), int(G), float(scale), int(num_kv_heads), int(B),
         int(Hq), int(D), int(bs), int(NB), int(block_tables.shape[1]), int(max_context_len),
         int(chunk_tokens), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _ptr(device_errors), _stream(stream, q.device)))
+        _ptr(device_errors), _stream(stream, q.device)), workspace)
     if prepare:
         return call
     call()
@@ -504,7 +505,7 @@ def pa_decode_fp8(out, q, k_cache, v_cache, block_tables, context_lens, scale, k
         float(scale), _ptr(k_scale), _ptr(v_scale), int(num_kv_heads), int(B), int(Hq), int(D),
         int(bs), int(NB), int(block_tables.shape[1]), int(max_context_len), int(chunk_tokens),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(device_errors),
-        _stream(stream, q.device)))
+        _stream(stream, q.device)), workspace)
     if prepare:
         return call
     call()

@@ -11,9 +11,16 @@ import paged_kv_cache_190_gb300 as pa
 from paged_kv_cache_190_gb300 import _lib
 
 
+PREPARED = _lib.PreparedCall
+
+
 class Stream:
     def __init__(self, cuda_stream=77, device=None):
         self.cuda_stream = cuda_stream
+
+
+class Block(types.SimpleNamespace):
+    pass
 
 
 class Raw:                                  # a stream of another library: only its handle
@@ -33,8 +40,8 @@ def taken(monkeypatch):
 
     def empty(n, **kw):
         taken.append(current[-1] if current else None)
-        block = types.SimpleNamespace(numel=lambda: n, element_size=lambda: 1, data_ptr=lambda: 256,
-                                      record_stream=lambda s: None)
+        block = Block(numel=lambda: n, element_size=lambda: 1, data_ptr=lambda: 256,
+                      record_stream=lambda s: None)
         return block
 
     monkeypatch.setattr(torch.cuda, "Stream", Stream)
@@ -44,7 +51,7 @@ def taken(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: Stream(0))
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(_lib, "_step", types.SimpleNamespace(span_decode=lambda *a: 0))
-    monkeypatch.setattr(_lib, "PreparedCall", lambda name, args: lambda: None)
+    monkeypatch.setattr(_lib, "PreparedCall", lambda name, args, keep=None: lambda: None)
     monkeypatch.setattr(_lib, "_need_cuda_contig", lambda *a: None)
     return taken
 
@@ -92,3 +99,31 @@ def test_workspace_comes_from_the_stream_of_the_call(taken, call):
     call()
     call(stream=Raw())
     assert taken == [7, None, 99]
+
+
+def cascade(**kw):
+    q, c = tensor(2, 4, 128), tensor(3, 2, 16, 128)
+    i, g = tensor(2, 2, dtype=torch.int32), tensor(2, dtype=torch.int32)
+    return pa.pa_decode_cascade(q, q, c, c, i, i, g, tensor(1, dtype=torch.int32), 1.0, 2, 16, workspace=None, **kw)
+
+
+@pytest.mark.parametrize("call", [full, multi, fixed_scale, cascade])
+def test_a_prepared_call_keeps_the_workspace_that_it_allocated(monkeypatch, taken, call):
+    """Its pointer is in the call's arguments: given out again, every later call of the
+    prepared one would write into another tensor."""
+    import weakref
+    blocks = []
+    empty = torch.empty
+
+    def watched(*a, **kw):
+        block = empty(*a, **kw)
+        blocks.append(weakref.ref(block))
+        return block
+
+    monkeypatch.setattr(torch, "empty", watched)
+    monkeypatch.setattr(_lib, "PreparedCall", PREPARED)
+    monkeypatch.setattr(_lib, "pa_decode_cascade_workspace_size", lambda *a: 4096)
+    prepared = call(prepare=True)
+    assert len(blocks) == 1 and blocks[0]() is not None
+    del prepared
+    assert blocks[0]() is None
