@@ -154,6 +154,12 @@ PyObject* issue(int device, F f) {
   return PyLong_FromLong(rc);
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v != 0;
+}
+
 // The arguments of a C call as a tuple, for a prepared call.
 PyObject* item(const void* p) { return p ? PyLong_FromVoidPtr(const_cast<void*>(p)) : Py_NewRef(Py_None); }
 PyObject* item(int64_t v) { return PyLong_FromLongLong(v); }
@@ -246,14 +252,13 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       s0 = page_scales(a[10], "k_scales", p);
       s1 = page_scales(a[11], "v_scales", p);
     }
-    const int inter = PyObject_IsTrue(a[12]);
-    if (inter < 0) throw Raised{};
+    const int inter = truth(a[12]);
     int32_t* errs = error_word(a[13], p.device);
     void* stream = stream_of(a[14], p.device);
     const int T = int32(tokens, "tokens"), hq = int32(heads, "heads"), hkv = int32(p.heads, "kv heads"),
               d = int32(p.head_dim, "head_dim"), r = int32(rot, "rot_dim"), m = int32(most, "max_position"),
               bs = int32(p.block_size, "block_size"), nb = int32(p.blocks, "blocks");
-    if (PyObject_IsTrue(a[15])) {
+    if (truth(a[15])) {
       if (kind == 0)
         return arguments(out_ptr, q_ptr, k.data_ptr(), v.data_ptr(), p.k, p.v, slots, pos, table, qs, ks, vs, T, hq,
                          hkv, d, r, inter, m, bs, nb, dtype, errs, stream);
@@ -322,7 +327,7 @@ PyObject* span_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void *op = out.data_ptr(), *wp = ws.data_ptr();
     const void* qp = q.data_ptr();
     const int32_t* tp = static_cast<const int32_t*>(tables.data_ptr());
-    if (PyObject_IsTrue(a[17])) {
+    if (truth(a[17])) {
       if (fp8)
         return arguments(op, qp, p.k, p.v, tp, lens, sc, s0, s1, hkv, B, hq, ql, d, bs, nb, mb, ml, win, sinks, wp,
                          ws_bytes, errs, stream);

@@ -268,3 +268,26 @@ def test_the_pools_hold_what_was_written_and_nothing_else(fp8):
     if fp8:
         for dev, host in zip(loop.scales, loop.host_scales):
             np.testing.assert_array_equal(storage_to_host(dev, "f32"), host)
+
+
+class NoTruth:
+    def __bool__(self):
+        raise ArithmeticError("neither")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_an_argument_without_a_truth_value_raises_its_own_error(fp8):
+    loop = Loop(fp8)
+    x = torch.zeros(1, HKV, D, dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros(1, HQ, D, dtype=torch.bfloat16, device=DEV)
+    slots = torch.zeros(1, dtype=torch.int64, device=DEV)
+    tables, lens = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    scales = loop.scales if fp8 else ()
+    append = pa.pa_rope_and_cache_fp8_block if fp8 else pa.pa_rope_and_cache
+    decode = pa.pa_decode_fp8_block if fp8 else pa.pa_decode_window
+    for kw in (dict(prepare=NoTruth()), dict(interleaved=NoTruth())):
+        with pytest.raises(ArithmeticError):
+            append(None, None, x, x, *loop.pools, slots, None, None, *scales, **kw)
+    with pytest.raises(ArithmeticError):
+        decode(torch.empty_like(q), q, *loop.pools, tables, lens, 1.0, *scales, HKV, BS, window=4, workspace=loop.ws,
+               prepare=NoTruth())
