@@ -1,4 +1,5 @@
-"""ctypes binding of libpagedattn (argument marshalling only)."""
+"""Binding of libpagedattn (argument marshalling only): ctypes, and the C++ extension of the
+per-step calls."""
 from __future__ import annotations
 
 import ctypes

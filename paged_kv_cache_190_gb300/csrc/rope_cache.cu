@@ -12,7 +12,8 @@
 // All of it is bound by memory: a token's rows are read once and written once.  On a GB300
 // (6.78 TB/s copied), 32 query and 8 kv heads of 128, bf16: 16384 tokens, 409 MB, in 61.6 us
 // (6.64 TB/s); 256 tokens in 2.3 us, one in 1.7 (the kernel's start); into page-scaled e4m3
-// pools 8190 tokens, 188 MB, in 31.2 us (6.0 TB/s), 256 single tokens in 3.6 us.
+// pools 8190 tokens, 188 MB, in 31.8 us (5.9 TB/s), 256 single tokens in 3.7 us; into pools
+// with a fixed scale per head, 16384 tokens, 378 MB, in 81.7 us (4.6 TB/s): divisions.
 // A lane holds the two 16-byte chunks of a row that rotate into each other, and a
 // thread takes the same chunks of several heads of one token, so that the table
 // row (4 bytes per rotated column, twice what a bf16 row is) is loaded once for
@@ -34,7 +35,8 @@ namespace {
 constexpr int kThreads = 128;
 // Heads that a thread takes of one token, when there are rows enough to fill the GPU.
 // Two: the table row serves two rows, and enough threads are resident to keep HBM busy
-// (16384 tokens of 32 + 8 heads: 61.6 us; one head 73.6, four heads 64.6).
+// (32 + 8 heads; bf16, 16384 tokens: 61.4 us, one head 73.4, four heads 64.6; float32, 8192:
+// 59.3, 60.9, 59.7; e4m3 with a scale per head, 16384: 81.7, 80.2, 164).
 constexpr int kHeadsAtOnce = 2;
 
 // (No load here goes through the read-only path: the kernels start before the one ahead
@@ -309,7 +311,7 @@ constexpr int kLanesPerRow = 8;                            // 128 bf16 columns: 
 constexpr int kRowsPerPass = 32 / kLanesPerRow;
 constexpr int kPageThreads = 256;                          // of a block of this kernel
 // Heads of q that a thread takes here, where three blocks are resident for the runs' sake
-// (8190 tokens: 36.2 us; two heads and four blocks 36.8, one head 45.6).
+// (8190 tokens: 31.8 us; two heads and four blocks 32.8, one head 44.9).
 constexpr int kPageHeadsAtOnce = 4;
 constexpr int kKeptRows = 16;                              // tokens that a block holds at a time
 
@@ -479,11 +481,10 @@ __device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::
 // A run of several tokens: the block takes its rows of up to kHeadsPerItem heads, of K or
 // of V.  The rows and the tokens' table rows come into shared memory all at once, which is
 // what has to overlap; the warps go over them there twice, for the magnitude and for the
-// codes.  (8190 tokens of 32 + 8 heads, q behind: 38 us; warp by warp straight from HBM, with
-// rows kept in registers or read twice, 44 to 54.)  What is left is instructions, 0.6 a
-// cycle of each scheduler: loops that are not unrolled (36.4 -> 35.3), no division by a
-// number of heads or columns (35.3 -> 34.8).  Runs of more than kKeptRows tokens come in
-// pieces, the first of them again for its codes.
+// codes.  What is left is instructions, 0.54 a cycle of each scheduler over 8190 tokens of
+// 32 + 8 heads: hence loops that are not unrolled and no division by a number of heads or
+// columns.  Runs of more than kKeptRows tokens come in pieces, the first of them again for
+// its codes.
 constexpr int kHeadsPerItem = 8;
 constexpr int kWarps = kPageThreads / 32;
 constexpr int kRunBytes = kKeptRows * (kHeadsPerItem * 256 + 128 * 4);
@@ -721,7 +722,7 @@ __global__ void __launch_bounds__(kPageThreads, 3) rope_and_cache_page_scale_ker
   }
   if (seen.num_more == 0) return;                          // (a decode step)
   // a run of few tokens gives its warps a head each, whatever the launch shares out (64
-  // sequences of 4 tokens, 8 kv heads: 10.3 -> 7.3 us)
+  // sequences of 4 tokens, 8 kv heads: 7.4 us, 10.6 with the launch's)
   auto heads_of = [&](int n) { return n > 8 ? item_heads : kHeadsPerItem; };
   const int few_groups = (a.num_kv_heads + kHeadsPerItem - 1) / kHeadsPerItem;
   const int groups = (a.num_kv_heads + item_heads - 1) / item_heads;
@@ -805,12 +806,12 @@ cudaError_t launch_rope_and_cache(const RopeArgs& a, cudaStream_t stream) {
     return a.head_dim == 128 ? run_rope<float, 128, false>(a, stream) : run_rope<float, 64, false>(a, stream);
   // A scale for each page and head.  A tile has a run for each of its tokens (a decode
   // step) or one or two in all (a prompt).  Heads of an item: as many as leave 256 items
-  // (512 tokens of 8 kv heads: 6.0 us with 2, 7.5 with 8; 4096: 15.2 with 8, 17.2 with 4).
+  // (512 tokens of 8 kv heads: 6.4 us with 2, 7.6 with 8; 1024: 7.7 with 4, 8.3 with 8).
   // Blocks of a tile: while the tiles are few, as many as give every token and head of a
   // decode step a warp at once, and 16, for as many short runs of a few tokens (333 tokens of
-  // 71 sequences, 1 kv head: 4.9 us, 10.3 without; a decode step of 256 tokens, 2 kv heads,
+  // 71 sequences, 1 kv head: 5.0 us, 10.0 without; a decode step of 256 tokens, 2 kv heads,
   // 3.4 and 3.0); from there on one for two groups of heads (8190 tokens, 8 kv
-  // heads: 31.2 us, 32.4 with a block each for K and V).
+  // heads: 31.8 us, 33.2 with a block each for K and V).
   const int64_t tiles = (a.num_tokens + kTile - 1) / kTile;
   int item_heads = 1;
   while (item_heads < kHeadsPerItem &&
@@ -824,8 +825,8 @@ cudaError_t launch_rope_and_cache(const RopeArgs& a, cudaStream_t stream) {
   const int64_t q_groups = static_cast<int64_t>(a.num_tokens) * uq;
   const int64_t q_blocks = (q_groups + kPageThreads / kLanesPerRow - 1) / (kPageThreads / kLanesPerRow);
   // q's blocks between the runs' blocks, where there are rows enough of q: the runs wait and
-  // convert while q's rows move (8190 tokens of 32 + 8 heads: 31.2 us; all of q behind 34.8,
-  // all between 32.8).  Half of them, which leaves blocks for the end; a page of 32 is two
+  // convert while q's rows move (8190 tokens of 32 + 8 heads: 31.8 us; all of q behind 35.0,
+  // all between 37.2).  Half of them, which leaves blocks for the end; a page of 32 is two
   // tiles, of which one has the run.
   const int64_t between = a.num_q_heads > 2 * a.num_kv_heads ? q_blocks / kv_blocks * 8 / a.block_size : 0;
   if (kv_blocks >= kMostGroups / 2 || q_groups >= kMostGroups) return cudaErrorInvalidValue;

@@ -10,8 +10,8 @@
 //
 // What bounds it: the bytes of K and V.  A token of one kv head is 2 D elements for
 // 4 D flops per query row, a flop or a few per byte.  On a GB300 (6.78 TB/s copied): 256
-// windows of 1028 tokens, bf16, 8 kv heads, 833 MB in 130.7 us (6.37 TB/s); 16 windows of
-// 4100 far into contexts of 131072, 8 rows a head, 269 MB in 44.5 us (6.05); e4m3, 256
+// windows of 1028 tokens, bf16, 8 kv heads, 833 MB in 130.6 us (6.38 TB/s); 16 windows of
+// 4100 far into contexts of 131072, 8 rows a head, 269 MB in 44.2 us (6.09); e4m3, 256
 // ragged sequences, 885 MB in 143.8 us (6.16), 4 of 131072 tokens, 1.07 GB in 163.0 us
 // (6.59); a few short sequences 3.7 to 6.2 us, of which half is the chain length -> table
 // entry -> page.
@@ -158,7 +158,7 @@ __device__ __forceinline__ int64_t query_row(const SpanParams& p, int b, int hea
 // zero), O^T = V^T P^T with the rows as columns; the score fragment of a lane is the B
 // fragment of the second product, so P stays in registers.  P goes into it as two bf16
 // parts, the rounded weight and what the rounding left (2^-16 of each weight is lost;
-// the rounded part alone loses 2^-8, 1.3 times the result's own rounding error); the
+// the rounded part alone loses 2^-8, which makes the error 1.25 times the result's own); the
 // row's sum l keeps the unrounded ones.
 template <int D>
 struct Bf16Rows {
