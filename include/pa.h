@@ -443,6 +443,93 @@ int pa_copy_scales(const float* src_k_scales, const float* src_v_scales, float* 
                    int32_t* device_errors, void* stream);
 
 /*
+ * 4-bit pools.  A row (one token of one kv head, head_dim 128) is 72 bytes: 64 of e2m1
+ * codes (1 sign, 2 exponent bits, 1 fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6), column 2 i
+ * in the low half of byte i and column 2 i + 1 in its high half, then 8 scales, byte j for
+ * columns 16 j .. 16 j + 15.  A scale is the upper bits of a positive half (5 of exponent,
+ * 3 of fraction): byte b stands for the half with the bits b << 7, so 2^-17 .. 10240 here,
+ * and a NaN.  An element is code * scale.  Nothing has to be calibrated, and a row depends
+ * on its own token alone.  k_cache and v_cache: [num_blocks][num_kv_heads][block_size][72]
+ * bytes; pa_copy_blocks and pa_swap_blocks move such pages like any others.
+ *
+ * pa_rope_and_cache_fp4: pa_rope_and_cache into such pools (q, k, v bf16, head_dim 128).
+ * For each 16 columns of k' and of v, amax being their largest magnitude:
+ *     scale = the nearest to amax / 6 (float32 division; ties to even; at most 10240),
+ *     code = the nearest to x / scale (float32 division, ties to the even code),
+ * with magnitudes beyond 6 scale (infinities too) at +-6; scale 0 stores zeros.  A NaN
+ * makes the scale, and so its 16 columns, NaN.
+ *
+ * pa_read_pages_fp4: pages read back in bf16, exactly: for each pair (src, dst) of
+ * src_dst_pairs (device int64 [num_pairs][2]) the rows of k_cache[src] and v_cache[src] are
+ * written to k_out[dst] and v_out[dst], bf16 [num_dst_blocks][num_kv_heads][block_size]
+ * [128].  With a table of the dst pages, pa_prefill attends to them.  Ids outside
+ * [0, num_src_blocks) or [0, num_dst_blocks) set PA_DEVERR_BAD_BLOCK and that pair is
+ * skipped.  Destinations must be distinct; the pools must not overlap.
+ *
+ * pa_decode_fp4: pa_decode_window over such pools (window 0, sinks 0 for none): q and out
+ * bf16; workspace of pa_decode_window_workspace_size.  Elements enter the products exactly,
+ * as halves, and so does q, scaled by a power of two (bf16 elements are exact down to 2^-22
+ * of their row's largest); logits, the maxima and the sums are float32; the probabilities
+ * are rounded to halves (2^-11) for the product with V.
+ */
+int pa_rope_and_cache_fp4(void* q_out, const void* q, const void* k, const void* v, void* k_cache,
+                          void* v_cache, const int64_t* slot_mapping, const int64_t* positions,
+                          const float* cos_sin, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                          int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                          int rot_dim, int interleaved, int max_position, int block_size,
+                          int num_blocks, int32_t* device_errors, void* stream);
+int pa_read_pages_fp4(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                      const int64_t* src_dst_pairs, int num_pairs, int num_kv_heads, int head_dim,
+                      int block_size, int num_src_blocks, int num_dst_blocks,
+                      int32_t* device_errors, void* stream);
+int pa_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                  const int32_t* block_tables, const int32_t* context_lens, float scale,
+                  int num_kv_heads, int num_seqs, int num_q_heads, int q_len, int head_dim,
+                  int block_size, int num_blocks, int max_blocks_per_seq, int max_context_len,
+                  int window, int sinks, void* workspace, size_t workspace_bytes,
+                  int32_t* device_errors, void* stream);
+
+/*
+ * Attention of prompts: the new tokens of each sequence, any number of them, over the paged
+ * cache that their keys and values have been written to -- a whole prompt, or the next
+ * chunk of one.  Sequence b's new tokens are rows q_starts[b] .. q_starts[b + 1] - 1 of q
+ * (packed one sequence after another; q_starts: device int32 [num_seqs + 1], not
+ * decreasing, within [0, num_tokens]) and the last of its context_lens[b] tokens: new token
+ * j of n stands at position p = L_b - n + j and attends, causally, to the positions t <= p,
+ * with window > 0 to those with p - t < window or t < sinks:
+ *     out[row][i] = softmax_t(scale q[row][i] . K_t) V_t.
+ * q and out are [num_tokens][num_q_heads][head_dim] in the pools' type; head_dim, block_size
+ * and group sizes as above; scale positive and finite.  A sequence may have no new token.
+ * Rows of out before q_starts[0] or from q_starts[num_seqs] on are left as they were; rows
+ * that see no token are zeros.  Table entries of pages of which no new token sees a
+ * position are not read (a window may have given them back), and what stands in positions
+ * that none sees does not matter; a NaN or infinity in a V row reaches other rows of its kv
+ * head near the tokens that see it, as a product with the weight 0.
+ * A length below 0 or above max_context_len, a sequence shorter than its new tokens and
+ * q_starts that decrease or leave the rows set PA_DEVERR_BAD_LENGTH (lengths are clamped,
+ * such rows are left as they were); block ids outside the pool set PA_DEVERR_BAD_BLOCK and
+ * their tokens are not seen.
+ *
+ * Logits, maxima and sums are float32, the result is rounded once.  Over bf16 pools the
+ * weights are rounded to bf16 for the product with V (2^-8 of each; the sum is that of the
+ * unrounded ones), as is usual for whole prompts, where the products are the cost: a second
+ * bf16 part of each weight would take half as long again.  Over float32 pools nothing is
+ * rounded.
+ *
+ * workspace: device scratch of pa_prefill_workspace_size bytes, 256-byte aligned; it
+ * carries no state between calls, but two calls in flight at once must not share it.
+ * The results do not depend on what else runs, bit for bit.
+ */
+size_t pa_prefill_workspace_size(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads,
+                                 int head_dim);
+int pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cache,
+               const int32_t* block_tables, const int32_t* context_lens, const int32_t* q_starts,
+               float scale, int num_kv_heads, int num_seqs, int num_tokens, int num_q_heads,
+               int head_dim, int block_size, int num_blocks, int max_blocks_per_seq,
+               int max_context_len, int window, int sinks, pa_dtype dtype, void* workspace,
+               size_t workspace_bytes, int32_t* device_errors, void* stream);
+
+/*
  * Test hook for the failure path.  Every pipeline wait of the decode kernels
  * enqueued after this call gives up after `polls` polls (0: at once) and
  * reports PA_DEVERR_TIMEOUT; the kernel then waits for its own copies in flight

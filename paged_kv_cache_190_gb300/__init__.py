@@ -19,4 +19,5 @@ from ._lib import (  # noqa: F401
     pa_get_error_string, pa_read_device_errors, pa_reshape_and_cache, pa_reshape_and_cache_fp8,
     pa_swap_blocks, pa_rope_and_cache, pa_rope_and_cache_fp8, pa_rope_and_cache_fp8_block,
     pa_copy_scales, pa_decode_window, pa_decode_window_workspace_size, pa_decode_fp8_block,
+    pa_rope_and_cache_fp4, pa_read_pages_fp4, pa_decode_fp4, pa_prefill, pa_prefill_workspace_size,
 )

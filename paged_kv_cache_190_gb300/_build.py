@@ -26,7 +26,9 @@ BINDING_SOURCE = os.path.join(CSRC, "step_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CU_SOURCES = ["capi.cu", "cache_ops.cu", "decode_launch.cu", "decode_bf16.cu", "decode_f32.cu",
               "decode_fp8.cu", "decode_noalloc.cu", "cascade.cu", "rope_cache.cu", "capi_rope.cu",
-              "span_launch.cu", "span_bf16.cu", "span_f32.cu", "span_fp8.cu", "capi_span.cu"]
+              "span_launch.cu", "span_bf16.cu", "span_f32.cu", "span_fp8.cu", "span_fp4.cu",
+              "capi_span.cu", "read_pages.cu", "prefill_launch.cu", "prefill_bf16.cu",
+              "prefill_f32.cu", "capi_prefill.cu"]
 CPP_SOURCES = ["block_manager.cpp", "cascade_groups.cpp"]
 
 

@@ -26,7 +26,8 @@ EXPORTED_SYMBOLS = [
     "pa_decode_multi", "pa_decode_cascade", "pa_decode_cascade_workspace_size",
     "pa_cascade_groups", "pa_rope_and_cache", "pa_rope_and_cache_fp8",
     "pa_rope_and_cache_fp8_block", "pa_copy_scales", "pa_decode_window_workspace_size",
-    "pa_decode_window", "pa_decode_fp8_block",
+    "pa_decode_window", "pa_decode_fp8_block", "pa_rope_and_cache_fp4", "pa_read_pages_fp4",
+    "pa_decode_fp4", "pa_prefill_workspace_size", "pa_prefill",
     "pa_bm_create", "pa_bm_destroy", "pa_bm_add_seq", "pa_bm_append_slot", "pa_bm_fork",
     "pa_bm_free", "pa_bm_block_table", "pa_bm_refcount", "pa_bm_num_free", "pa_bm_free_list",
     "pa_bm_stats", "pa_bm_append_slots", "pa_bm_build_block_tables", "pa_bm_enable_swap",
@@ -73,6 +74,11 @@ _SIGNATURES = {
     "pa_decode_window": (_i32, [_vp] * 6 + [ctypes.c_float] + [_i32] * 12 + [_vp, _sz, _vp, _vp]),
     "pa_decode_fp8_block": (_i32, [_vp] * 6 + [ctypes.c_float, _vp, _vp] + [_i32] * 11 +
                             [_vp, _sz, _vp, _vp]),
+    "pa_rope_and_cache_fp4": (_i32, [_vp] * 9 + [_i64] * 3 + [_i32] * 9 + [_vp, _vp]),
+    "pa_read_pages_fp4": (_i32, [_vp] * 5 + [_i32] * 6 + [_vp, _vp]),
+    "pa_decode_fp4": (_i32, [_vp] * 6 + [ctypes.c_float] + [_i32] * 11 + [_vp, _sz, _vp, _vp]),
+    "pa_prefill_workspace_size": (_sz, [_i32] * 5),
+    "pa_prefill": (_i32, [_vp] * 7 + [ctypes.c_float] + [_i32] * 12 + [_vp, _sz, _vp, _vp]),
     "pa_debug_set_wait_limit": (_i32, [_i32]),
     "pa_read_device_errors": (_i32, [_vp, _pi32, _i32, _vp]),
     "pa_bm_create": (_i32, [_i32, _i32, _pi32, ctypes.POINTER(_vp)]),
@@ -584,6 +590,27 @@ def pa_rope_and_cache_fp8_block(q_out, q, k, v, k_cache, v_cache, slot_mapping, 
                         device_errors, stream, prepare)
 
 
+def pa_rope_and_cache_fp4(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                          interleaved=False, device_errors=None, stream=None, prepare=False):
+    """pa_rope_and_cache into 4-bit pools: caches uint8 [NB, Hkv, bs, 72], a row's codes and
+    then its scales; q, k, v bf16 (see pa.h)."""
+    return _rope_append("pa_rope_and_cache_fp4", 3, q_out, q, k, v, k_cache, v_cache, slot_mapping,
+                        positions, cos_sin, None, None, interleaved, device_errors, stream, prepare)
+
+
+def pa_read_pages_fp4(k_out, v_out, k_cache, v_cache, src_dst_pairs, device_errors=None,
+                      stream=None, prepare=False):
+    """Pages of 4-bit pools read back in bf16: k_out[d], v_out[d] = the rows of k_cache[s],
+    v_cache[s] for each (s, d) of src_dst_pairs (int64 [P, 2] on the device); k_out, v_out
+    bf16 [NB2, Hkv, bs, 128] (see pa.h)."""
+    rc = (_step or _binding()).read_pages(k_out, v_out, k_cache, v_cache, src_dst_pairs,
+                                          device_errors, stream, prepare)
+    if prepare:
+        return PreparedCall("pa_read_pages_fp4", rc)
+    if rc:
+        _check(rc, "pa_read_pages_fp4")
+
+
 def pa_copy_scales(src_k_scales, src_v_scales, dst_k_scales, dst_v_scales, src_dst_pairs,
                    device_errors=None, stream=None, prepare=False):
     """The scale rows of copied pages, dst[d] = src[s] for each (s, d) of src_dst_pairs
@@ -619,14 +646,14 @@ def pa_copy_scales(src_k_scales, src_v_scales, dst_k_scales, dst_v_scales, src_d
 # ------------------------------------------- windowed and page-scaled decode
 def pa_decode_window_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                                     max_context_len, window=0, sinks=0) -> int:
-    """Bytes of workspace of pa_decode_window and pa_decode_fp8_block; num_q_heads counts
+    """Bytes of workspace of pa_decode_window, pa_decode_fp8_block and pa_decode_fp4; num_q_heads counts
     the rows of all new tokens (q_len * Hq)."""
     return int(library().pa_decode_window_workspace_size(
         int(num_seqs), int(num_q_heads), int(num_kv_heads), int(head_dim), int(block_size),
         int(max_context_len), int(window), int(sinks)))
 
 
-def _span_decode(name, fp8, out, q, k_cache, v_cache, block_tables, context_lens, scale, k_scales,
+def _span_decode(name, kind, out, q, k_cache, v_cache, block_tables, context_lens, scale, k_scales,
                  v_scales, num_kv_heads, max_context_len, window, sinks, workspace, device_errors,
                  stream, prepare):
     if workspace is None:
@@ -642,7 +669,7 @@ def _span_decode(name, fp8, out, q, k_cache, v_cache, block_tables, context_lens
                 window, sinks)
         workspace = _workspace(nbytes, q.device, stream)
     rc = (_step or _binding()).span_decode(
-        fp8, out, q, k_cache, v_cache, block_tables, context_lens, scale, k_scales, v_scales,
+        kind, out, q, k_cache, v_cache, block_tables, context_lens, scale, k_scales, v_scales,
         num_kv_heads, max_context_len, window, sinks, workspace, device_errors, stream, prepare)
     if prepare:
         return PreparedCall(name, rc)
@@ -660,7 +687,7 @@ def pa_decode_window(out, q, k_cache, v_cache, block_tables, context_lens, scale
     context_lens int32 [B] (see pa.h).  ``workspace``: a uint8 CUDA tensor of at least
     pa_decode_window_workspace_size() bytes; allocated here when None (not for a prepared
     call, which would outlive it)."""
-    return _span_decode("pa_decode_window", False, out, q, k_cache, v_cache, block_tables,
+    return _span_decode("pa_decode_window", 0, out, q, k_cache, v_cache, block_tables,
                         context_lens, scale, None, None, num_kv_heads, max_context_len, window,
                         sinks, workspace, device_errors, stream, prepare)
 
@@ -670,9 +697,56 @@ def pa_decode_fp8_block(out, q, k_cache, v_cache, block_tables, context_lens, sc
                         workspace=None, device_errors=None, stream=None, prepare=False):
     """pa_decode_window over e4m3 pools with a scale for each page and head: out, q bf16;
     caches one-byte [NB, Hkv, bs, 128]; k_scales, v_scales float32 [NB, Hkv] (see pa.h)."""
-    return _span_decode("pa_decode_fp8_block", True, out, q, k_cache, v_cache, block_tables,
+    return _span_decode("pa_decode_fp8_block", 1, out, q, k_cache, v_cache, block_tables,
                         context_lens, scale, k_scales, v_scales, num_kv_heads, max_context_len,
                         window, sinks, workspace, device_errors, stream, prepare)
+
+
+def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads,
+                  max_context_len, window=0, sinks=0, workspace=None, device_errors=None,
+                  stream=None, prepare=False):
+    """pa_decode_window over 4-bit pools: out, q bf16; caches uint8 [NB, Hkv, bs, 72] (see
+    pa.h)."""
+    return _span_decode("pa_decode_fp4", 2, out, q, k_cache, v_cache, block_tables, context_lens,
+                        scale, None, None, num_kv_heads, max_context_len, window, sinks, workspace,
+                        device_errors, stream, prepare)
+
+
+# ------------------------------------------------------------------- prompts
+def pa_prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim) -> int:
+    """Bytes of workspace of pa_prefill for up to so many rows and sequences."""
+    return int(library().pa_prefill_workspace_size(
+        int(num_tokens), int(num_seqs), int(num_q_heads), int(num_kv_heads), int(head_dim)))
+
+
+def pa_prefill(out, q, k_cache, v_cache, block_tables, context_lens, q_starts, scale, num_kv_heads,
+               max_context_len, window=0, sinks=0, workspace=None, device_errors=None, stream=None,
+               prepare=False):
+    """Causal attention of prompts, or of the next chunks of prompts, over the paged cache:
+    out, q [T, Hq, D], the sequences' new tokens one after another; q_starts int32 [B + 1],
+    sequence b's rows being q_starts[b] .. q_starts[b + 1] - 1, the last of its
+    context_lens[b] tokens; caches [NB, Hkv, bs, D] of their type; block_tables int32
+    [B, max_blocks]; window and sinks as in pa_decode_window (see pa.h).  ``workspace``: a
+    uint8 CUDA tensor of at least pa_prefill_workspace_size() bytes; allocated here when
+    None (not for a prepared call, which would outlive it)."""
+    if workspace is None:
+        import torch
+        if prepare:
+            raise ValueError("a prepared call needs a workspace that outlives it")
+        if not q.is_cuda or q.dim() != 3:
+            raise ValueError("q must be a contiguous CUDA tensor [T, Hq, D]")
+        with torch.cuda.device(q.device):
+            nbytes = pa_prefill_workspace_size(q.shape[0], block_tables.shape[0], q.shape[1],
+                                               num_kv_heads, q.shape[2])
+        workspace = _workspace(nbytes, q.device, stream)
+    rc = (_step or _binding()).prefill(
+        out, q, k_cache, v_cache, block_tables, context_lens, q_starts, scale, num_kv_heads,
+        max_context_len, window, sinks, workspace, device_errors, stream, prepare)
+    if prepare:
+        return PreparedCall("pa_prefill", rc)
+    if rc:
+        _check(rc, "pa_prefill")
+    return out
 
 
 def pa_debug_set_wait_limit(polls: int) -> None:

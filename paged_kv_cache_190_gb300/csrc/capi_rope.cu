@@ -10,7 +10,7 @@
 
 namespace {
 
-// What the three appends check alike.  Returns PA_OK with nothing to do left in
+// What the appends check alike.  Returns PA_OK with nothing to do left in
 // num_tokens == 0.
 int check(const pa::RopeArgs& a, int elt) {
   if (a.num_tokens < 0 || a.num_q_heads < 0 || a.num_kv_heads <= 0 || a.num_blocks <= 0)
@@ -131,6 +131,39 @@ int pa_rope_and_cache_fp8_block(void* q_out, const void* q, const void* k, const
   a.v_scales = v_scales;
   a.pool = pa::RopePool::kFp8Page;
   return run(a, 2, stream);
+}
+
+int pa_rope_and_cache_fp4(void* q_out, const void* q, const void* k, const void* v, void* k_cache,
+                          void* v_cache, const int64_t* slot_mapping, const int64_t* positions,
+                          const float* cos_sin, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                          int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                          int rot_dim, int interleaved, int max_position, int block_size,
+                          int num_blocks, int32_t* device_errors, void* stream) {
+  if (head_dim != 128 || !shape_ok(head_dim, block_size)) return PA_ERR_UNSUPPORTED;
+  pa::RopeArgs a = args(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, q_stride,
+                        k_stride, v_stride, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                        rot_dim, interleaved, max_position, block_size, num_blocks, device_errors);
+  a.pool = pa::RopePool::kFp4;
+  return run(a, 2, stream);
+}
+
+int pa_read_pages_fp4(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                      const int64_t* src_dst_pairs, int num_pairs, int num_kv_heads, int head_dim,
+                      int block_size, int num_src_blocks, int num_dst_blocks,
+                      int32_t* device_errors, void* stream) {
+  if (head_dim != 128 || !shape_ok(head_dim, block_size)) return PA_ERR_UNSUPPORTED;
+  if (num_pairs < 0 || num_kv_heads <= 0 || num_src_blocks <= 0 || num_dst_blocks <= 0 ||
+      num_kv_heads > 65536)
+    return PA_ERR_INVALID_ARG;
+  if (num_pairs == 0) return PA_OK;
+  if (!k_out || !v_out || !k_cache || !v_cache || !src_dst_pairs) return PA_ERR_INVALID_ARG;
+  using pa::aligned16;
+  if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_cache) || !aligned16(v_cache))
+    return PA_ERR_INVALID_ARG;
+  const cudaError_t e = pa::launch_read_pages_fp4(
+      k_out, v_out, k_cache, v_cache, src_dst_pairs, num_pairs, num_kv_heads * block_size,
+      num_src_blocks, num_dst_blocks, device_errors, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 int pa_copy_scales(const float* src_k_scales, const float* src_v_scales, float* dst_k_scales,

@@ -1,5 +1,5 @@
-// C ABI entry points of the windowed decode and of the decode over e4m3 pools with a
-// scale for each page and head: argument checks on the host, then the launcher.
+// C ABI entry points of the windowed decode, of the decode over e4m3 pools with a scale
+// for each page and head, and of the decode over 4-bit rows: argument checks on the host, then the launcher.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -110,6 +110,19 @@ int pa_decode_fp8_block(void* out, const void* q, const void* k_cache, const voi
   if (head_dim != 128 || !shape_ok(head_dim, block_size)) return PA_ERR_UNSUPPORTED;
   return run(pa::SpanPool::kFp8, out, q, k_cache, v_cache, block_tables, context_lens, scale,
              k_scales, v_scales, num_kv_heads, num_seqs, num_q_heads, q_len, head_dim, block_size,
+             num_blocks, max_blocks_per_seq, max_context_len, window, sinks, workspace,
+             workspace_bytes, device_errors, stream);
+}
+
+int pa_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                  const int32_t* block_tables, const int32_t* context_lens, float scale,
+                  int num_kv_heads, int num_seqs, int num_q_heads, int q_len, int head_dim,
+                  int block_size, int num_blocks, int max_blocks_per_seq, int max_context_len,
+                  int window, int sinks, void* workspace, size_t workspace_bytes,
+                  int32_t* device_errors, void* stream) {
+  if (head_dim != 128 || !shape_ok(head_dim, block_size)) return PA_ERR_UNSUPPORTED;
+  return run(pa::SpanPool::kFp4, out, q, k_cache, v_cache, block_tables, context_lens, scale,
+             nullptr, nullptr, num_kv_heads, num_seqs, num_q_heads, q_len, head_dim, block_size,
              num_blocks, max_blocks_per_seq, max_context_len, window, sinks, workspace,
              workspace_bytes, device_errors, stream);
 }

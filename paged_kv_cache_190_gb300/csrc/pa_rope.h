@@ -7,7 +7,7 @@
 
 namespace pa {
 
-enum class RopePool { kF32, kBf16, kFp8Head, kFp8Page };
+enum class RopePool { kF32, kBf16, kFp8Head, kFp8Page, kFp4 };
 
 struct RopeArgs {
   void* q_out;                 // [num_tokens][num_q_heads][head_dim], contiguous
@@ -34,5 +34,9 @@ cudaError_t launch_rope_and_cache(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_copy_scales(const float* src_k, const float* src_v, float* dst_k, float* dst_v,
                                const int64_t* pairs, int num_pairs, int num_kv_heads, int num_src,
                                int num_dst, int32_t* device_errors, cudaStream_t stream);
+// Pages of 4-bit rows as bf16 pages (read_pages.cu).
+cudaError_t launch_read_pages_fp4(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                                  const int64_t* pairs, int num_pairs, int page_rows, int num_src,
+                                  int num_dst, int32_t* device_errors, cudaStream_t stream);
 
 }  // namespace pa

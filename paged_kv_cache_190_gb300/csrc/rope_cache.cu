@@ -26,6 +26,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "fp4.cuh"
 #include "pa_device.cuh"
 #include "pa_rope.h"
 
@@ -213,8 +214,44 @@ __device__ __forceinline__ Place place(const RopeArgs& a, int t, bool speak) {
 
 // HPT rows (heads h0 .. h0 + HPT - 1, stride D elements) of one kind of one token.
 enum Kind { kQ, kK, kV };
+// What the pools hold: the rows' own type, e4m3 codes with a scale per head, or 4-bit rows.
+enum class Held { kSame, kE4m3, kE2m1 };
 
-template <typename E, int D, bool INTER, bool FP8, int HPT>
+// This lane's two chunks of a row (8 lanes, 8 columns a chunk) into a 4-bit row.  The 16
+// columns of a scale are chunks c and c ^ 1, held by one lane or by two of the eight,
+// which tell each other their largest magnitudes.
+template <bool INTER>
+__device__ __forceinline__ void store_row4(unsigned char* row, const float* x0, const float* x1,
+                                           const LaneChunks<8, 128, INTER>& lc, int half) {
+  const int lane = threadIdx.x & 31, first = lane & 24;
+  uint32_t top[2] = {0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    top[0] = max(top[0], __float_as_uint(x0[e]) & 0x7fffffffu);
+    top[1] = max(top[1], __float_as_uint(x1[e]) & 0x7fffffffu);
+  }
+  uint32_t* codes = reinterpret_cast<uint32_t*>(row);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int c = k ? lc.c1 : lc.c0, other = c ^ 1;
+    // the lane that holds the other chunk, and as which of its two
+    int owner, slot;
+    if constexpr (INTER) {
+      owner = other & 7;
+      slot = other >> 3;
+    } else {
+      slot = other < 2 * half ? (other >= half) : (other & 1);
+      owner = other < 2 * half ? (slot ? other - half : other) : other >> 1;
+    }
+    const uint32_t t0 = __shfl_sync(0xffu << first, top[0], first + owner);
+    const uint32_t t1 = __shfl_sync(0xffu << first, top[1], first + owner);
+    const uint32_t s = scale4_of(max(top[k], slot ? t1 : t0));
+    codes[c] = codes4_of(k ? x1 : x0, scale4_value(s));
+    if ((c & 1) == 0) row[kRow4Codes + (c >> 1)] = static_cast<unsigned char>(s);
+  }
+}
+
+template <typename E, int D, bool INTER, Held HELD, int HPT>
 __device__ __forceinline__ void rows_of_token(const RopeArgs& a, int t, Kind kind, int h0, int l) {
   constexpr int N = Vec<E>::N;
   constexpr int CPR = D / N;                               // chunks of a row
@@ -241,7 +278,7 @@ __device__ __forceinline__ void rows_of_token(const RopeArgs& a, int t, Kind kin
   for (int j = 0; j < HPT; ++j) {
     if (HPT > 1 && h0 + j >= heads) break;
     const int h = h0 + j;
-    if (kind == kV && !FP8) {                              // bytes as they are
+    if (kind == kV && HELD == Held::kSame) {               // bytes as they are
       uint4* dst = reinterpret_cast<uint4*>(a.v_cache) +
                    ((page * a.num_kv_heads + h) * a.block_size + off) * CPR;
       dst[lc.c0] = w0[j];
@@ -257,7 +294,11 @@ __device__ __forceinline__ void rows_of_token(const RopeArgs& a, int t, Kind kin
                    (static_cast<int64_t>(t) * a.num_q_heads + h) * CPR;
       dst[lc.c0] = Vec<E>::pack(x0);
       dst[lc.c1] = Vec<E>::pack(x1);
-    } else if constexpr (FP8) {
+    } else if constexpr (HELD == Held::kE2m1) {
+      unsigned char* dst = static_cast<unsigned char*>(kind == kK ? a.k_cache : a.v_cache) +
+                           ((page * a.num_kv_heads + h) * a.block_size + off) * kRow4Bytes;
+      store_row4<INTER>(dst, x0, x1, lc, kind == kK ? a.rot_dim / 16 : 0);
+    } else if constexpr (HELD == Held::kE4m3) {
       const float s = (kind == kK ? a.k_scale : a.v_scale)[h];
       const bool pow2 = is_pow2(s);
       const float inv = pow2 ? pow2_reciprocal(s) : 0.f;
@@ -275,7 +316,7 @@ __device__ __forceinline__ void rows_of_token(const RopeArgs& a, int t, Kind kin
 }
 
 // A group of D / (2 N) lanes takes HPT heads of one token and kind.
-template <typename E, int D, bool INTER, bool FP8, int HPT>
+template <typename E, int D, bool INTER, Held HELD, int HPT>
 __global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const RopeArgs a, unsigned groups,
                                                                   int uq, int uk) {
   wait_prior_grids();
@@ -287,11 +328,11 @@ __global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const RopeArgs
   const int t = g / units, u = g - t * units;
   const int l = threadIdx.x % LPR;
   if (u < uq)
-    rows_of_token<E, D, INTER, FP8, HPT>(a, t, kQ, u * HPT, l);
+    rows_of_token<E, D, INTER, HELD, HPT>(a, t, kQ, u * HPT, l);
   else if (u < uq + uk)
-    rows_of_token<E, D, INTER, FP8, HPT>(a, t, kK, (u - uq) * HPT, l);
+    rows_of_token<E, D, INTER, HELD, HPT>(a, t, kK, (u - uq) * HPT, l);
   else
-    rows_of_token<E, D, INTER, FP8, HPT>(a, t, kV, (u - uq - uk) * HPT, l);
+    rows_of_token<E, D, INTER, HELD, HPT>(a, t, kV, (u - uq - uk) * HPT, l);
 }
 
 // ------------------------------------------------ a scale for each page and head
@@ -707,7 +748,7 @@ __global__ void __launch_bounds__(kPageThreads, 3) rope_and_cache_page_scale_ker
     const unsigned g = qb * (kPageThreads / kLanesPerRow) + threadIdx.x / kLanesPerRow;
     if (g >= q_groups) return;
     const unsigned t = g / uq;
-    rows_of_token<uint16_t, 128, INTER, false, kPageHeadsAtOnce>(a, t, kQ, (g - t * uq) * kPageHeadsAtOnce,
+    rows_of_token<uint16_t, 128, INTER, Held::kSame, kPageHeadsAtOnce>(a, t, kQ, (g - t * uq) * kPageHeadsAtOnce,
                                                                  threadIdx.x % kLanesPerRow);
     return;
   }
@@ -778,7 +819,7 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // costs as much as a head's rotation).
 constexpr int64_t kMostGroups = int64_t{1} << 31;
 
-template <typename E, int D, bool FP8>
+template <typename E, int D, Held HELD>
 cudaError_t run_rope(const RopeArgs& a, cudaStream_t stream) {
   constexpr int per_block = kThreads / (D / Vec<E>::N / 2);
   auto go = [&](auto kernel, int hpt) {
@@ -791,19 +832,20 @@ cudaError_t run_rope(const RopeArgs& a, cudaStream_t stream) {
   const bool few = static_cast<int64_t>(a.num_tokens) * (a.num_q_heads + 2 * a.num_kv_heads) < 8192;
   constexpr int H = kHeadsAtOnce;
   if (a.interleaved)
-    return few ? go(rope_and_cache_kernel<E, D, true, FP8, 1>, 1) : go(rope_and_cache_kernel<E, D, true, FP8, H>, H);
-  return few ? go(rope_and_cache_kernel<E, D, false, FP8, 1>, 1) : go(rope_and_cache_kernel<E, D, false, FP8, H>, H);
+    return few ? go(rope_and_cache_kernel<E, D, true, HELD, 1>, 1) : go(rope_and_cache_kernel<E, D, true, HELD, H>, H);
+  return few ? go(rope_and_cache_kernel<E, D, false, HELD, 1>, 1) : go(rope_and_cache_kernel<E, D, false, HELD, H>, H);
 }
 
 }  // namespace
 
 cudaError_t launch_rope_and_cache(const RopeArgs& a, cudaStream_t stream) {
   if (a.num_tokens == 0) return cudaSuccess;
-  if (a.pool == RopePool::kFp8Head) return run_rope<uint16_t, 128, true>(a, stream);
+  if (a.pool == RopePool::kFp8Head) return run_rope<uint16_t, 128, Held::kE4m3>(a, stream);
+  if (a.pool == RopePool::kFp4) return run_rope<uint16_t, 128, Held::kE2m1>(a, stream);
   if (a.pool == RopePool::kBf16)
-    return a.head_dim == 128 ? run_rope<uint16_t, 128, false>(a, stream) : run_rope<uint16_t, 64, false>(a, stream);
+    return a.head_dim == 128 ? run_rope<uint16_t, 128, Held::kSame>(a, stream) : run_rope<uint16_t, 64, Held::kSame>(a, stream);
   if (a.pool == RopePool::kF32)
-    return a.head_dim == 128 ? run_rope<float, 128, false>(a, stream) : run_rope<float, 64, false>(a, stream);
+    return a.head_dim == 128 ? run_rope<float, 128, Held::kSame>(a, stream) : run_rope<float, 64, Held::kSame>(a, stream);
   // A scale for each page and head.  A tile has a run for each of its tokens (a decode
   // step) or one or two in all (a prompt).  Heads of an item: as many as leave 256 items
   // (512 tokens of 8 kv heads: 6.4 us with 2, 7.6 with 8; 1024: 7.7 with 4, 8.3 with 8).

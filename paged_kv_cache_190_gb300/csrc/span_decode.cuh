@@ -48,6 +48,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "fp4.cuh"
 #include "paged_decode.cuh"
 #include "span_list.cuh"
 
@@ -295,13 +296,36 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// A row of q, spread over four lanes in pairs of bf16, as halves: scaled by a power of two
+// into [128, 256); a bf16 element is exact as a half down to 2^-22 of its row's largest.
+// Returns the power's inverse.
+template <int KS>
+__device__ __forceinline__ float halves_of_q(uint32_t (&qa)[KS][2]) {
+  float amax = 0.f;
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(qa[ks][k])), fabsf(bf16_hi(qa[ks][k]))));
+  amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+  const int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu);
+  const int se = min(max(134 - e, -126), 126);            // amax 2^se in [128, 256)
+  const float up = __uint_as_float(static_cast<uint32_t>(se + 127) << 23);
+  const float back = __uint_as_float(static_cast<uint32_t>(127 - se) << 23);
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) qa[ks][k] = pack_half2(bf16_lo(qa[ks][k]) * up, bf16_hi(qa[ks][k]) * up);
+  return back;
+}
+
 // e4m3 codes with a scale for each page and head: codes become halves (exactly, two a
 // conversion) on the way into mma.sync m16n8k16.  The e4m3 form of the instruction
 // converts both operands inside, at every use, and wants q and the weights as sums of two
 // e4m3 parts: 650 instructions a tile were 550 this way (161.8 -> 161.0 us for 885 MB
 // then), and the weights keep 11 bits instead of 8.
-//   * q: the row scaled by a power of two into [128, 256); a bf16 element is exact as a
-//     half down to 2^-22 of its row's largest.
+//   * q: halves_of_q.
 //   * The codes of a K row that ldmatrix gives a lane are columns 4 c .. 4 c + 3 of a
 //     chunk: they become k = 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of a step, for q alike.
 //   * V through ldmatrix.trans on code pairs: columns 2 g and 2 g + 1 of tokens 2 c and
@@ -337,22 +361,7 @@ struct Fp8Rows {
     }
   }
   __device__ __forceinline__ void begin(const SpanParams&) {
-    float amax = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(qa[ks][k])), fabsf(bf16_hi(qa[ks][k]))));
-    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-    const int e = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu);
-    const int se = min(max(134 - e, -126), 126);            // amax 2^se in [128, 256)
-    const float up = __uint_as_float(static_cast<uint32_t>(se + 127) << 23);
-    qinv = __uint_as_float(static_cast<uint32_t>(127 - se) << 23);
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) qa[ks][k] = pack_half2(bf16_lo(qa[ks][k]) * up, bf16_hi(qa[ks][k]) * up);
+    qinv = halves_of_q<KS>(qa);
     m = mo = kNoScore;
     l = 0.f;
 #pragma unroll
@@ -473,6 +482,171 @@ struct Fp8Rows {
       if (h0 < rows) *reinterpret_cast<float2*>(macc + h0 * D + d) = make_float2(o[mt][0] * b0, o[mt][2] * b0);
       if (h1 < rows) *reinterpret_cast<float2*>(macc + h1 * D + d) = make_float2(o[mt][1] * b1, o[mt][3] * b1);
     }
+  }
+};
+
+// 4-bit rows (fp4.cuh): a code times its scale is exact as a half, so K and V become halves
+// on the way into mma.sync m16n8k16, two a conversion, and one product of two of them
+// brings the scale in; q and the weights as for e4m3 (the scales differ within a row, so
+// they cannot go into the weights; nor need they, for a half holds the values).
+//   * A row of 72 bytes is loaded as it stands, 8 bytes of 16 columns a time: piece p of
+//     rows 4 c + i of 16 tokens falls on banks 8 c + 2 p, a half-warp's on all 32.
+//   * Scores: a lane has pieces c and c + 4 of its token's row; q's columns go with them.
+//   * Column 2 j of a score tile is token 4 c + 2 (tile & 1) of its 16 and column 2 j + 1 the
+//     next, so that a lane's weights are those of 4 tokens in a row.
+//   * Values: lane (g, c) has piece g of those 4 tokens.  The codes of a column of two
+//     tokens are put into one byte (two shifts and two selections for 16 codes), which one
+//     conversion makes the pair of halves that the product wants; the columns 16 g + 2 t
+//     and 16 g + 2 t + 1 become rows g and g + 8 of O^T's tile t, under the scales of one
+//     piece.
+struct Fp4Rows {
+  static constexpr int D = 128, KS = 8, MT = 8, NT = 4, TU = 32;
+  static constexpr float kPLog2 = 10.f;      // weights are carried times 2^10
+  uint32_t qa[KS][2];
+  float o[MT][4];
+  float m, l, qinv;
+  int lane, rows;
+
+  __device__ __forceinline__ void init(const SpanParams& p, int lane_, float*, float*) {
+    lane = lane_;
+    rows = p.rows;
+  }
+  __device__ __forceinline__ int row() const { return lane >> 2; }
+
+  __device__ __forceinline__ void load(const SpanParams& p, int b, int head) {
+    const int g = lane >> 2, c = lane & 3;
+    const bool on = g < rows;
+    const uint2* src = reinterpret_cast<const uint2*>(p.q + query_row(p, b, head, on ? g : 0) * (2 * D));
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      // columns 4 (ks & 3) .. + 3 of piece c + 4 (ks >> 2)
+      const uint2 w = on ? src[4 * (c + 4 * (ks >> 2)) + (ks & 3)] : make_uint2(0u, 0u);
+      qa[ks][0] = w.x;
+      qa[ks][1] = w.y;
+    }
+  }
+  __device__ __forceinline__ void begin(const SpanParams&) {
+    qinv = halves_of_q<KS>(qa);
+    m = kNoScore;
+    l = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+  }
+
+  // half: bytes between tokens 0-15 and 16-31
+  template <typename Release>
+  __device__ __forceinline__ void unit(uint32_t kb, uint32_t vb, int, int half, const Sight& see,
+                                       float scale_log2, const float2*, int, Release release) {
+    const int g = lane >> 2, c = lane & 3;
+    const char* kt = static_cast<const char*>(__cvta_shared_to_generic(kb)) + (4 * (g >> 1) + (g & 1)) * kRow4Bytes;
+    const char* vt = static_cast<const char*>(__cvta_shared_to_generic(vb)) + 4 * c * kRow4Bytes;
+    float sh[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      sh[n][0] = sh[n][1] = sh[n][2] = sh[n][3] = 0.f;
+      const char* row = kt + (n >> 1) * half + 2 * (n & 1) * kRow4Bytes;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint2 w = *reinterpret_cast<const uint2*>(row + 8 * c + 32 * k);
+        const uint32_t s = *reinterpret_cast<const unsigned char*>(row + kRow4Codes + c + 4 * k) * 0x00800080u;
+        uint32_t b[8];
+        halves4_of(w.x, b[0], b[1], b[2], b[3]);
+        halves4_of(w.y, b[4], b[5], b[6], b[7]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = mul_half2(b[i], s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mma_f16(sh[n], qa[4 * k + i][0], 0u, qa[4 * k + i][1], 0u, b[2 * i], b[2 * i + 1]);
+      }
+    }
+    // V's codes come in while the scores are worked on
+    uint2 vw[2][4];
+    uint32_t vs[2][4];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const char* row = vt + hf * half + i * kRow4Bytes;
+        vw[hf][i] = *reinterpret_cast<const uint2*>(row + 8 * g);
+        vs[hf][i] = *reinterpret_cast<const unsigned char*>(row + kRow4Codes + g);
+      }
+    release();
+    const float qs = qinv * scale_log2;
+    float sv[2 * NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) sv[2 * n + e] = sh[n][e] * qs;
+    if (!see.all) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (!see.sees(16 * (n >> 1) + 4 * c + 2 * (n & 1) + e)) sv[2 * n + e] = -INFINITY;
+    }
+    float mx = fmaxf(fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3])), fmaxf(fmaxf(sv[4], sv[5]), fmaxf(sv[6], sv[7])));
+    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+    const float mn = fmaxf(m, mx);
+    const float alpha = fast_exp2(m - mn);
+    m = mn;
+    uint32_t pb[NT];
+    float psum = 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float p0 = fast_exp2(sv[2 * n] - mn), p1 = fast_exp2(sv[2 * n + 1] - mn);
+      psum += p0 + p1;
+      pb[n] = pack_half2(p0 * 1024.f, p1 * 1024.f);
+    }
+    l = l * alpha + psum;
+    if (__any_sync(kFull, alpha != 1.f)) {
+      const float a_even = __shfl_sync(kFull, alpha, 8 * c), a_odd = __shfl_sync(kFull, alpha, 8 * c + 4);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        o[mt][0] *= a_even;
+        o[mt][1] *= a_odd;
+        o[mt][2] *= a_even;
+        o[mt][3] *= a_odd;
+      }
+    }
+    constexpr uint32_t kLow = 0x0f0f0f0fu;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const uint32_t s01 = (vs[hf][0] << 7) + vs[hf][1] * 0x00800000u;
+      const uint32_t s23 = (vs[hf][2] << 7) + vs[hf][3] * 0x00800000u;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = j ? vw[hf][i].y : vw[hf][i].x;
+        uint32_t a0[4], a1[4], a2[4], a3[4];                // of tiles 4 j .. 4 j + 3
+        halves4_of((x[0] & kLow) | ((x[1] << 4) & ~kLow), a0[0], a0[1], a0[2], a0[3]);
+        halves4_of(((x[0] >> 4) & kLow) | (x[1] & ~kLow), a1[0], a1[1], a1[2], a1[3]);
+        halves4_of((x[2] & kLow) | ((x[3] << 4) & ~kLow), a2[0], a2[1], a2[2], a2[3]);
+        halves4_of(((x[2] >> 4) & kLow) | (x[3] & ~kLow), a3[0], a3[1], a3[2], a3[3]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          mma_f16(o[4 * j + t], mul_half2(a0[t], s01), mul_half2(a1[t], s01), mul_half2(a2[t], s23),
+                  mul_half2(a3[t], s23), pb[2 * hf], pb[2 * hf + 1]);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void store(float* macc, float* ml) {
+    float lt = l + __shfl_xor_sync(kFull, l, 1);
+    lt += __shfl_xor_sync(kFull, lt, 2);
+    const int g = lane >> 2, c = lane & 3;
+    if (g < rows && c == 0) {
+      ml[g * 2] = m;
+      ml[g * 2 + 1] = lt;
+    }
+    constexpr float kBack = 1.f / 1024.f;
+#pragma unroll
+    for (int mt = 0; mt < MT; mt += 2)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (2 * c + h < rows)
+          *reinterpret_cast<float4*>(macc + (2 * c + h) * D + 16 * g + 2 * mt) =
+              make_float4(o[mt][h] * kBack, o[mt][2 + h] * kBack, o[mt + 1][h] * kBack, o[mt + 1][2 + h] * kBack);
   }
 };
 
@@ -703,6 +877,8 @@ template <int D, int G>
 struct RowsOf<SpanPool::kBf16, D, G> { using type = Bf16Rows<D>; };
 template <int G>
 struct RowsOf<SpanPool::kFp8, 128, G> { using type = Fp8Rows; };
+template <int G>
+struct RowsOf<SpanPool::kFp4, 128, G> { using type = Fp4Rows; };
 template <int D, int G>
 struct RowsOf<SpanPool::kF32, D, G> { using type = F32Rows<D, G>; };
 
@@ -717,7 +893,8 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
   constexpr int TU = span_tile_tokens(P, D);
   constexpr int ROW = span_row_bytes(P, D);
   constexpr int STAGE = span_stage_bytes(P, D);
-  constexpr int SLABS = P == SpanPool::kF32 ? 1 : ROW / 128;
+  constexpr bool FP4 = P == SpanPool::kFp4;
+  constexpr int SLABS = P == SpanPool::kF32 || FP4 ? 1 : ROW / 128;
   constexpr int CPL = D / 32;
   constexpr bool BF16_OUT = P != SpanPool::kF32;
   constexpr bool FP8 = P == SpanPool::kFp8;
@@ -749,7 +926,7 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
     fence_mbar_init();
   }
   if (p.splits > 1) cluster_arrive();                        // waited for before the first store to a peer
-  if (threadIdx.x == 32) {
+  if (!FP4 && threadIdx.x == 32) {
     prefetch_map(&p.map_k);
     prefetch_map(&p.map_v);
   }
@@ -907,7 +1084,9 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
         unsigned char* dst = smem + s * STAGE + kv * (STAGE / 2) + ps * op_bytes;
         const CUtensorMap* map = kv ? &p.map_v : &p.map_k;
         const int z = q_phys[0] * p.pool_heads + q_head[0];
-        if constexpr (SLABS > 1)
+        if constexpr (FP4)                                   // whole pages, of all the CTA's heads in one piece
+          bulk_g2s(dst, (kv ? p.v_pool : p.k_pool) + static_cast<int64_t>(z) * p.block_size * ROW, op_bytes, &full[s]);
+        else if constexpr (SLABS > 1)
           tma_load_4d(dst, map, 0, q_off[0], z, 0, &full[s]);
         else
           tma_load_3d(dst, map, 0, q_off[0], z, &full[s]);
@@ -995,7 +1174,15 @@ __global__ void __launch_bounds__(kSpanThreads, 1) span_decode_kernel(const __gr
           if (!see.all) {
             // V rows that no row of the sequence sees (stale, never written, of a missing
             // page) must not meet the zero weights as NaN or infinity
-            for (int i = lane; i < TU * (ROW / 16); i += 32) {
+            if constexpr (FP4) {
+              // (a code is always finite: the scales are all there is to clear)
+              static_assert(!FP4 || TU == 32, "a token a lane");
+              const int tt = t0 + lane;
+              if (tt >= sp.len || (tt >= p.sinks && tt < sp.lo) || ((bad >> (lane >> 4)) & 1u))
+                asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(vb + (lane >> 4) * half + (lane & 15) * ROW + kRow4Codes),
+                             "r"(0u) : "memory");
+            }
+            for (int i = FP4 ? TU * (ROW / 16) : lane; i < TU * (ROW / 16); i += 32) {
               const int t = i / (ROW / 16), ch = i % (ROW / 16);
               const int tt = t0 + t;
               if (tt >= sp.len || (tt >= p.sinks && tt < sp.lo) || ((bad >> (t >> 4)) & 1u)) {

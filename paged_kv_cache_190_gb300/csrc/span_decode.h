@@ -11,7 +11,7 @@
 
 namespace pa {
 
-enum class SpanPool { kF32, kBf16, kFp8 };
+enum class SpanPool { kF32, kBf16, kFp8, kFp4 };
 
 constexpr int kSpanWarps = 8;                     // consumer warps of a CTA
 constexpr int kSpanThreads = (kSpanWarps + 1) * 32;
@@ -21,11 +21,12 @@ constexpr int kSpanCluster = 8;                   // most CTAs that share a sequ
 constexpr int kNoWindow = 1 << 30;
 
 // Tokens that a warp takes from one stage: a tile of 4 KiB of K and 4 KiB of V
-// (2 KiB each for bf16 heads of 64).
+// (2 KiB each for bf16 heads of 64, 2.25 for 4-bit rows).
 __host__ __device__ constexpr int span_tile_tokens(SpanPool pool, int head_dim) {
-  return pool == SpanPool::kFp8 ? 32 : pool == SpanPool::kBf16 ? 16 : head_dim == 128 ? 8 : 16;
+  return pool == SpanPool::kFp8 || pool == SpanPool::kFp4 ? 32 : pool == SpanPool::kBf16 ? 16 : head_dim == 128 ? 8 : 16;
 }
 __host__ __device__ constexpr int span_row_bytes(SpanPool pool, int head_dim) {
+  if (pool == SpanPool::kFp4) return head_dim / 2 + head_dim / 16;   // codes and their scales
   return head_dim * (pool == SpanPool::kFp8 ? 1 : pool == SpanPool::kBf16 ? 2 : 4);
 }
 __host__ __device__ constexpr int span_stage_bytes(SpanPool pool, int head_dim) {
@@ -71,6 +72,8 @@ __host__ __device__ constexpr SpanSmem span_smem(SpanPool pool, int head_dim, in
 
 struct SpanParams {
   CUtensorMap map_k, map_v;
+  const unsigned char* k_pool;                    // kFp4: copied as they stand
+  const unsigned char* v_pool;
   void* out;
   const char* q;
   const int32_t* tables;
@@ -119,5 +122,6 @@ void span_cluster_rooms(int num_sms, int (&room)[kSpanCluster + 1]);
 cudaError_t run_span_bf16(int head_dim, const SpanParams& p, dim3 grid, int smem, cudaStream_t stream);
 cudaError_t run_span_f32(int head_dim, const SpanParams& p, dim3 grid, int smem, cudaStream_t stream);
 cudaError_t run_span_fp8(const SpanParams& p, dim3 grid, int smem, cudaStream_t stream);
+cudaError_t run_span_fp4(const SpanParams& p, dim3 grid, int smem, cudaStream_t stream);
 
 }  // namespace pa

@@ -240,8 +240,9 @@ int heads_together(int num_kv_heads, int most) {
 // 4, 171 with 2, 213 with 1.  bf16 rows are twice as long, and with 2 heads a segment leaves
 // a quarter of the partials: 129.4 us against 132.2 with 8 (833 MB), 49.5 against 52.0
 // (269 MB, 8 rows a head).
+bool codes(SpanPool pool) { return pool == SpanPool::kFp8 || pool == SpanPool::kFp4; }
 int share_heads(SpanPool pool, int num_kv_heads) {
-  return heads_together(num_kv_heads, pool == SpanPool::kFp8 ? 8 : 2);
+  return heads_together(num_kv_heads, codes(pool) ? 8 : 2);
 }
 
 // Room for the states that a CTA of a cluster joins.
@@ -286,7 +287,7 @@ Spread choose_spread(SpanPool pool, int head_dim, int rows, int64_t num_seqs, in
   const int64_t all = (num_seqs * num_kv_heads * blocks + kSpanWarps - 1) / kSpanWarps;
   const int64_t hbm = together * all / num_sms * (even ? 10 : 7) / 10;
   Spread best;
-  const bool fp8 = pool == SpanPool::kFp8;
+  const bool fp8 = codes(pool);
   const auto stage_cost = [&](int hg) {
     const int full = fp8 ? (hg == 8 ? 106 : hg == 4 ? 109 : hg == 2 ? 130 : 176)
                          : (hg == 8 ? 63 : hg == 4 ? 67 : hg == 2 ? 79 : 103);
@@ -382,8 +383,12 @@ cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream) {
   const int64_t head_pages = static_cast<int64_t>(a.num_blocks) * a.num_kv_heads;
   if (head_pages > INT_MAX) return cudaErrorInvalidValue;
   const int box_tokens = std::min(a.block_size, tu);
-  cudaError_t e = make_map(&p.map_k, a.k_cache, a.pool, a.head_dim, a.block_size, head_pages, box_tokens, hg);
-  if (e == cudaSuccess)
+  cudaError_t e = cudaSuccess;
+  p.k_pool = static_cast<const unsigned char*>(a.k_cache);
+  p.v_pool = static_cast<const unsigned char*>(a.v_cache);
+  if (a.pool != SpanPool::kFp4)
+    e = make_map(&p.map_k, a.k_cache, a.pool, a.head_dim, a.block_size, head_pages, box_tokens, hg);
+  if (a.pool != SpanPool::kFp4 && e == cudaSuccess)
     e = make_map(&p.map_v, a.v_cache, a.pool, a.head_dim, a.block_size, head_pages, box_tokens, hg);
   if (e != cudaSuccess) return e;
   p.out = a.out;
@@ -424,10 +429,12 @@ cudaError_t launch_span_decode(const SpanArgs& a, cudaStream_t stream) {
   if (ring < 1 || smem > kSpanSmem) return cudaErrorInvalidValue;
   e = a.pool == SpanPool::kBf16  ? run_span_bf16(a.head_dim, p, blocks_of, smem, stream)
       : a.pool == SpanPool::kF32 ? run_span_f32(a.head_dim, p, blocks_of, smem, stream)
-                                 : run_span_fp8(p, blocks_of, smem, stream);
+      : a.pool == SpanPool::kFp8 ? run_span_fp8(p, blocks_of, smem, stream)
+                                 : run_span_fp4(p, blocks_of, smem, stream);
   if (e != cudaSuccess || clusters) return e;
   switch (a.pool) {
-    case SpanPool::kFp8: return launch_join<32, true, 4>(p, segments, grid, stream);
+    case SpanPool::kFp8:
+    case SpanPool::kFp4: return launch_join<32, true, 4>(p, segments, grid, stream);
     case SpanPool::kBf16:
       return a.head_dim == 128 ? launch_join<16, true, 4>(p, segments, grid, stream)
                                : launch_join<16, true, 2>(p, segments, grid, stream);

@@ -1,5 +1,5 @@
 // Python binding of the calls that a serving loop issues every step on small tensors: the
-// rotating appends and the windowed / page-scaled decodes.  Their arguments are checked
+// rotating appends, the windowed / page-scaled / 4-bit decodes, pages read back, and prompts.  Their arguments are checked
 // and handed to the C ABI here, in C++: the same checks cost 7 to 15 us a call in Python
 // (about 70 attribute reads and a ctypes call of 26 arguments on a Grace core), more than
 // the kernels of a small step run; here they cost about one.
@@ -101,15 +101,23 @@ struct Pools {
   void* v;
 };
 
-Pools pools(PyObject* ok, PyObject* ov, bool codes) {
+enum Codes { kNoCodes, kE4m3, kE2m1 };
+
+Pools pools(PyObject* ok, PyObject* ov, Codes codes) {
   const at::Tensor &k = tensor(ok, "k_cache"), &v = tensor(ov, "v_cache");
   on_device(k, "k_cache", -1);
   on_device(v, "v_cache", k.get_device());
   if (k.dim() != 4 || v.sizes() != k.sizes())
     refuse("k_cache and v_cache must be [blocks, kv heads, block size, head_dim], alike");
   if (v.scalar_type() != k.scalar_type()) refuse_type("k_cache and v_cache differ in type");
-  if (codes && k.element_size() != 1)
+  if (codes == kE4m3 && k.element_size() != 1)
     refuse_type("k_cache and v_cache must hold one-byte e4m3 codes (uint8 or float8_e4m3fn)");
+  if (codes == kE2m1) {
+    if (k.scalar_type() != at::kByte) refuse_type("k_cache and v_cache must be uint8");
+    if (k.size(3) != 72) refuse("k_cache and v_cache must have rows of 72 bytes (128 columns)");
+    return {static_cast<int>(k.get_device()), k.size(0), k.size(1), k.size(2), 128, k.scalar_type(),
+            k.data_ptr(), v.data_ptr()};
+  }
   return {static_cast<int>(k.get_device()), k.size(0), k.size(1), k.size(2), k.size(3), k.scalar_type(),
           k.data_ptr(), v.data_ptr()};
 }
@@ -203,12 +211,12 @@ PyObject* guarded(F f) {
 
 // rope_append(kind, q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin,
 //             k_scale(s), v_scale(s), interleaved, device_errors, stream, prepare)
-// kind 0: pools of the rows' type; 1: e4m3, a scale per head; 2: e4m3, one per page and head
+// kind 0: pools of the rows' type; 1: e4m3, a scale per head; 2: e4m3, one per page and head; 3: 4-bit rows
 PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     if (n != 16) refuse_type("rope_append takes 16 arguments");
     const int kind = int32(integer(a[0], "kind"), "kind");
-    const Pools p = pools(a[5], a[6], kind != 0);
+    const Pools p = pools(a[5], a[6], kind == 3 ? kE2m1 : kind ? kE4m3 : kNoCodes);
     const at::Tensor &k = tensor(a[3], "k"), &v = tensor(a[4], "v");
     const at::ScalarType type = kind ? at::kBFloat16 : k.scalar_type();
     const pa_dtype dtype = code_of(type);
@@ -262,6 +270,9 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (kind == 0)
         return arguments(out_ptr, q_ptr, k.data_ptr(), v.data_ptr(), p.k, p.v, slots, pos, table, qs, ks, vs, T, hq,
                          hkv, d, r, inter, m, bs, nb, dtype, errs, stream);
+      if (kind == 3)
+        return arguments(out_ptr, q_ptr, k.data_ptr(), v.data_ptr(), p.k, p.v, slots, pos, table, qs, ks, vs, T, hq,
+                         hkv, d, r, inter, m, bs, nb, errs, stream);
       return arguments(out_ptr, q_ptr, k.data_ptr(), v.data_ptr(), p.k, p.v, slots, pos, table, s0, s1, qs, ks, vs, T,
                        hq, hkv, d, r, inter, m, bs, nb, errs, stream);
     }
@@ -273,27 +284,32 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (kind == 1)
         return pa_rope_and_cache_fp8(out_ptr, q_ptr, kp, vp, p.k, p.v, slots, pos, table, s0, s1, qs, ks, vs, T, hq,
                                      hkv, d, r, inter, m, bs, nb, errs, stream);
+      if (kind == 3)
+        return pa_rope_and_cache_fp4(out_ptr, q_ptr, kp, vp, p.k, p.v, slots, pos, table, qs, ks, vs, T, hq, hkv, d, r,
+                                     inter, m, bs, nb, errs, stream);
       return pa_rope_and_cache_fp8_block(out_ptr, q_ptr, kp, vp, p.k, p.v, slots, pos, table, s0, s1, qs, ks, vs, T,
                                          hq, hkv, d, r, inter, m, bs, nb, errs, stream);
     });
   });
 }
 
-// span_decode(fp8, out, q, k_cache, v_cache, block_tables, context_lens, scale, k_scales,
+// span_decode(kind, out, q, k_cache, v_cache, block_tables, context_lens, scale, k_scales,
 //             v_scales, num_kv_heads, max_context_len, window, sinks, workspace,
 //             device_errors, stream, prepare)
+// kind 0: pools of q's type; 1: e4m3, a scale for each page and head; 2: 4-bit rows
 PyObject* span_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     if (n != 18) refuse_type("span_decode takes 18 arguments");
-    const bool fp8 = a[0] == Py_True;
+    const int kind = int32(integer(a[0], "kind"), "kind");
+    const bool fp8 = kind == 1, fp4 = kind == 2;
     const at::Tensor &out = tensor(a[1], "out"), &q = tensor(a[2], "q");
-    const Pools p = pools(a[3], a[4], fp8);
+    const Pools p = pools(a[3], a[4], fp4 ? kE2m1 : fp8 ? kE4m3 : kNoCodes);
     on_device(q, "q", p.device);
     on_device(out, "out", p.device);
     const at::ScalarType type = q.scalar_type();
     const pa_dtype dtype = code_of(type);
-    if (fp8 && dtype != PA_BF16) refuse_type("q and out must be bf16");
-    if (!fp8 && p.type != type) refuse_type("the pools must have the type of q");
+    if (kind && dtype != PA_BF16) refuse_type("q and out must be bf16");
+    if (!kind && p.type != type) refuse_type("the pools must have the type of q");
     if (q.dim() != 3 && q.dim() != 4) refuse("q must be [B, Hq, D] or [B, q_len, Hq, D]");
     if (out.scalar_type() != type) refuse_type("out must have q's type");
     if (out.sizes() != q.sizes()) refuse("out must have q's shape");
@@ -331,6 +347,9 @@ PyObject* span_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (fp8)
         return arguments(op, qp, p.k, p.v, tp, lens, sc, s0, s1, hkv, B, hq, ql, d, bs, nb, mb, ml, win, sinks, wp,
                          ws_bytes, errs, stream);
+      if (fp4)
+        return arguments(op, qp, p.k, p.v, tp, lens, sc, hkv, B, hq, ql, d, bs, nb, mb, ml, win, sinks, wp, ws_bytes,
+                         errs, stream);
       return arguments(op, qp, p.k, p.v, tp, lens, sc, hkv, B, hq, ql, d, bs, nb, mb, ml, win, sinks, dtype, wp,
                        ws_bytes, errs, stream);
     }
@@ -338,8 +357,91 @@ PyObject* span_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (fp8)
         return pa_decode_fp8_block(op, qp, p.k, p.v, tp, lens, sc, s0, s1, hkv, B, hq, ql, d, bs, nb, mb, ml, win,
                                    sinks, wp, ws_bytes, errs, stream);
+      if (fp4)
+        return pa_decode_fp4(op, qp, p.k, p.v, tp, lens, sc, hkv, B, hq, ql, d, bs, nb, mb, ml, win, sinks, wp,
+                             ws_bytes, errs, stream);
       return pa_decode_window(op, qp, p.k, p.v, tp, lens, sc, hkv, B, hq, ql, d, bs, nb, mb, ml, win, sinks, dtype, wp,
                               ws_bytes, errs, stream);
+    });
+  });
+}
+
+// read_pages(k_out, v_out, k_cache, v_cache, src_dst_pairs, device_errors, stream, prepare)
+PyObject* read_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 8) refuse_type("read_pages takes 8 arguments");
+    const Pools p = pools(a[2], a[3], kE2m1);
+    const at::Tensor &ko = tensor(a[0], "k_out"), &vo = tensor(a[1], "v_out"), &pairs = tensor(a[4], "src_dst_pairs");
+    on_device(ko, "k_out", p.device);
+    on_device(vo, "v_out", p.device);
+    if (ko.scalar_type() != at::kBFloat16 || vo.scalar_type() != at::kBFloat16)
+      refuse_type("k_out and v_out must be bf16");
+    if (ko.dim() != 4 || vo.sizes() != ko.sizes() || ko.size(1) != p.heads || ko.size(2) != p.block_size ||
+        ko.size(3) != p.head_dim)
+      refuse("k_out and v_out must be [blocks, kv heads, block size, 128], alike");
+    on_device(pairs, "src_dst_pairs", p.device);
+    if (pairs.scalar_type() != at::kLong) refuse_type("src_dst_pairs must be int64");
+    if (pairs.dim() != 2 || pairs.size(1) != 2) refuse("src_dst_pairs must be [pairs, 2]");
+    int32_t* errs = error_word(a[5], p.device);
+    void* stream = stream_of(a[6], p.device);
+    void *kp = ko.data_ptr(), *vp = vo.data_ptr();
+    const int64_t* pp = static_cast<const int64_t*>(pairs.data_ptr());
+    const int np = int32(pairs.size(0), "pairs"), hkv = int32(p.heads, "kv heads"), d = int32(p.head_dim, "head_dim"),
+              bs = int32(p.block_size, "block_size"), ns = int32(p.blocks, "blocks"), nd = int32(ko.size(0), "blocks");
+    if (truth(a[7])) return arguments(kp, vp, p.k, p.v, pp, np, hkv, d, bs, ns, nd, errs, stream);
+    return issue(p.device, [&] {
+      return pa_read_pages_fp4(kp, vp, p.k, p.v, pp, np, hkv, d, bs, ns, nd, errs, stream);
+    });
+  });
+}
+
+// prefill(out, q, k_cache, v_cache, block_tables, context_lens, q_starts, scale, num_kv_heads,
+//         max_context_len, window, sinks, workspace, device_errors, stream, prepare)
+PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 16) refuse_type("prefill takes 16 arguments");
+    const at::Tensor &out = tensor(a[0], "out"), &q = tensor(a[1], "q");
+    const Pools p = pools(a[2], a[3], kNoCodes);
+    on_device(q, "q", p.device);
+    on_device(out, "out", p.device);
+    const at::ScalarType type = q.scalar_type();
+    const pa_dtype dtype = code_of(type);
+    if (p.type != type) refuse_type("the pools must have the type of q");
+    if (q.dim() != 3) refuse("q must be [tokens, Hq, D]");
+    if (out.scalar_type() != type) refuse_type("out must have q's type");
+    if (out.sizes() != q.sizes()) refuse("out must have q's shape");
+    if (q.size(2) != p.head_dim) refuse("the pools have another head_dim than q");
+    const int64_t heads = integer(a[8], "num_kv_heads");
+    if (heads != p.heads) refuse("num_kv_heads does not match the cache shape");
+    const at::Tensor& tables = tensor(a[4], "block_tables");
+    on_device(tables, "block_tables", p.device);
+    if (tables.scalar_type() != at::kInt) refuse_type("block_tables must be int32");
+    if (tables.dim() != 2) refuse("block_tables must be [sequences, pages]");
+    const int64_t seqs = tables.size(0);
+    const int32_t* lens = static_cast<const int32_t*>(vector(a[5], "context_lens", p.device, at::kInt, seqs));
+    const int32_t* starts = static_cast<const int32_t*>(vector(a[6], "q_starts", p.device, at::kInt, seqs + 1));
+    const double scale = PyFloat_AsDouble(a[7]);
+    if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
+    const at::Tensor& ws = tensor(a[12], "workspace");
+    on_device(ws, "workspace", p.device);
+    const size_t ws_bytes = ws.nbytes();
+    int32_t* errs = error_word(a[13], p.device);
+    void* stream = stream_of(a[14], p.device);
+    const int B = int32(seqs, "sequences"), T = int32(q.size(0), "tokens"), hq = int32(q.size(1), "heads"),
+              hkv = int32(heads, "num_kv_heads"), d = int32(p.head_dim, "head_dim"),
+              bs = int32(p.block_size, "block_size"), nb = int32(p.blocks, "blocks"),
+              mb = int32(tables.size(1), "block_tables"), ml = int32(integer(a[9], "max_context_len"), "max_context_len"),
+              win = int32(integer(a[10], "window"), "window"), sinks = int32(integer(a[11], "sinks"), "sinks");
+    const float sc = static_cast<float>(scale);
+    void *op = out.data_ptr(), *wp = ws.data_ptr();
+    const void* qp = q.data_ptr();
+    const int32_t* tp = static_cast<const int32_t*>(tables.data_ptr());
+    if (truth(a[15]))
+      return arguments(op, qp, p.k, p.v, tp, lens, starts, sc, hkv, B, T, hq, d, bs, nb, mb, ml, win, sinks, dtype, wp,
+                       ws_bytes, errs, stream);
+    return issue(p.device, [&] {
+      return pa_prefill(op, qp, p.k, p.v, tp, lens, starts, sc, hkv, B, T, hq, d, bs, nb, mb, ml, win, sinks, dtype, wp,
+                        ws_bytes, errs, stream);
     });
   });
 }
@@ -347,6 +449,8 @@ PyObject* span_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {
     {"rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(rope_append)), METH_FASTCALL, nullptr},
     {"span_decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(span_decode)), METH_FASTCALL, nullptr},
+    {"read_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(read_pages)), METH_FASTCALL, nullptr},
+    {"prefill", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(prefill)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_step", "Checked per-step calls of libpagedattn.", -1, methods,
