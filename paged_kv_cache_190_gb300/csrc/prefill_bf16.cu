@@ -27,8 +27,10 @@
 //   * V rows that no row of the tile sees (past its last key, behind the window) may hold
 //     anything; where a tile has such rows beside others a warp clears them before the
 //     product.  Their weights are zeros.
-//   * The reference maximum moves only when a score passes it by more than 8 (weights then
-//     stay below 2^8, and bf16 keeps its relative step), so O is hardly ever rescaled.
+//   * The reference is the first step's maximum and moves only when the weights of a row's
+//     step come to more than 2^16 (bf16 has float32's range, so they may pass 1), so O is
+//     hardly ever rescaled, and the other steps take no maximum: 128 keys of 32 rows cost a
+//     warp alone 750 clocks instead of 1030.
 //   * Every wait is bounded; on expiry the kernel reports PA_DEVERR_TIMEOUT, waits for its
 //     own copies and products, frees its tensor memory and returns.
 #include <cuda.h>
@@ -44,8 +46,9 @@ namespace pa {
 namespace {
 
 constexpr int kSoftmaxWarps = 8;                           // four for each half of the rows
-constexpr int kProducer = 8, kIssuer = 9, kCleaner = 10;   // (warp 11 only fills its warpgroup)
+constexpr int kProducer = 8, kIssuer = 9, kCleaner = 10, kIssuerStep = 2;   // issuers: warps 9 and 11
 constexpr int kThreadsPrefill = 12 * 32;
+constexpr float kMostSum = 65536.f;                        // of a row's weights in one step
 constexpr int kBadRing = 8;
 constexpr uint32_t kTmemO = 256;                           // column of O0; S0 is column 0
 
@@ -59,11 +62,19 @@ struct PrefillLayout {
   static constexpr int OFF_RING = 2 * Q_HALF;
   static constexpr int OFF_BAD = OFF_RING + RING * TILE;
   static constexpr int OFF_BARS = OFF_BAD + kBadRing * 4;
-  // full, empty, raw [RING]; q_full, q_empty; s_full, p_full, pv_done, o_free [2]; end
-  static constexpr int NUM_BARS = 3 * RING + 2 + 8 + 1;
+  // full, empty, raw [RING]; q_full, q_empty; s_full, p_full, pv_done, o_free, turn [2]; end
+  static constexpr int NUM_BARS = 3 * RING + 2 + 10 + 1;
   static constexpr int SMEM = OFF_BARS + NUM_BARS * 8 + 16 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory over budget");
 };
+
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(kFull, x, 0); }
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return (static_cast<uint64_t>(hi) << 32) | lo; }
 
 // The wait before tcgen05.ld's registers are used, tied to them.
 template <int N>
@@ -71,6 +82,32 @@ __device__ __forceinline__ void tmem_landed(float (&v)[N]) {
   tmem_wait_ld();
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+// Two floats at once (half the instructions; a warp's scheduler is as busy as its
+// exponentials otherwise), and the largest of three.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // The lowest n bits of a word, n of any size.
@@ -92,7 +129,8 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 2;
   uint64_t* o_free = pv_done + 2;
-  uint64_t* end = o_free + 2;
+  uint64_t* turn = o_free + 2;                             // which half's products are next
+  uint64_t* end = turn + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(end + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -101,18 +139,19 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
   if (threadIdx.x == 0) {
     for (int i = 0; i < R; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 2);                             // both halves
       mbar_init(&raw[i], 1);
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
       mbar_init(&o_free[i], 4);
+      mbar_init(&turn[i], 1);
     }
-    mbar_init(end, 1);
+    mbar_init(end, 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -137,7 +176,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
     }
   };
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return !*abort_flag && mbar_wait(bar, parity, p.wait_limit);
+    return mbar_try_wait(bar, parity) || (!*abort_flag && mbar_wait(bar, parity, p.wait_limit));
   };
   // item k of this CTA: false past the last
   struct Item {
@@ -286,86 +325,145 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
       }
     }
     if (!ok && lane == 0) fail();
-  } else if (warp == kIssuer) {
-    // ------------------------------------------------------------ products: one thread
-    if (lane == 0) {
-      const uint32_t ring = smem_addr(smem + Ly::OFF_RING), q_base = smem_addr(smem);
-      const int bs = p.block_size;
-      constexpr uint32_t kIdPV = umma_idesc_bf16(128, D, true);
-      uint32_t c = 0, kp[2] = {0, 0}, ko[2] = {0, 0};      // ring slots taken; weights, items of each half
-      bool ok = true;
-      int items_done = 0;
-      Item it;
-      // S of half i = its rows of q times the K tile in `slot`
-      auto scores = [&](int i, int slot, int keys) {
-        const uint64_t qd = umma_desc(q_base + i * Ly::Q_HALF, 16, 1024);
-        const uint64_t kd = umma_desc(ring + slot * Ly::TILE, 16, 1024);
-        const uint32_t id = umma_idesc_bf16(128, (keys + 15) & ~15, false);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint64_t off = ((ks >> 2) * Ly::Q_SLAB + (ks & 3) * 32) >> 4;
-          umma_bf16(tmem + 128 * i, qd + off, kd + off, id, ks > 0 ? 1u : 0u);
+  } else if (warp == kIssuer || warp == kIssuer + kIssuerStep) {
+    // ------------------------------------------------------------ products: a thread for each half
+    // (What is done between two products is not hidden behind them: the queue is short.  So
+    // there are two issuers, slots are counted up instead of divided, descriptors differ from
+    // ready ones by an addition.  The warp runs as one and a lane of it issues, with values
+    // that the compiler knows to be the warp's: they stay in uniform registers.)
+    {
+      const int half = warp == kIssuer ? 0 : 1;
+      const bool issues = elect_lane();
+      const uint32_t ring = smem_addr(smem + Ly::OFF_RING);
+      constexpr uint32_t kIdS = umma_idesc_bf16(128, kPrefillKeys, false), kIdPV = umma_idesc_bf16(128, D, true);
+      const uint64_t qd0 = umma_desc(smem_addr(smem) + half * Ly::Q_HALF, 16, 1024);
+      const uint64_t kd0 = umma_desc(ring, 16, 1024), vd0 = umma_desc(ring, p.block_size * 128, 1024);
+      const uint32_t q_lo = uniform(static_cast<uint32_t>(qd0)), sbo = static_cast<uint32_t>(kd0 >> 32);
+      const uint32_t k_lo0 = uniform(static_cast<uint32_t>(kd0)), v_lo0 = uniform(static_cast<uint32_t>(vd0));
+      const uint32_t s_at = uniform(tmem + 128 * half), o_at = uniform(tmem + kTmemO + 128 * half);
+      // from 16 keys to the next within V's tile: bs 16, a page; bs 32, 16 rows and then a page
+      const uint32_t v_odd = (p.block_size == 16 ? 16 * D * 2 : 16 * 128) >> 4, v_even = (2 * 16 * D * 2) >> 4;
+      struct Slot {
+        uint32_t i, parity;
+        __device__ __forceinline__ void next() {
+          if (++i == R) {
+            i = 0;
+            parity ^= 1;
+          }
         }
-        umma_commit(&s_full[i]);
+      } at{0, 0};
+      uint32_t p_parity = 0, o_parity = 1, q_parity = 0, t_parity = half ^ 1;
+      bool ok = true;
+      Item it;
+      // (the lanes agree on giving up)
+      auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, wait(bar, parity)) != 0; };
+      // S = this half's rows of q times the K tile in `slot`
+      auto scores = [&](uint32_t slot, uint32_t id) {
+        const uint32_t k_lo = uniform(k_lo0 + slot * (Ly::TILE >> 4));
+        if (issues) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * Ly::Q_SLAB + (ks & 3) * 32) >> 4;
+            umma_bf16(s_at, desc_of(q_lo + off, sbo), desc_of(k_lo + off, sbo), id, ks > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[half]);
+        }
+        __syncwarp();
+      };
+      // O += the weights times the V tile in `slot`
+      auto values = [&](uint32_t slot, int keys, uint32_t accumulate) {
+        const uint32_t v_lo = uniform(v_lo0 + slot * (Ly::TILE >> 4));
+        if (issues) {
+          if (keys == kPrefillKeys) {
+#pragma unroll
+            for (int g = 0; g < kPrefillKeys / 16; ++g)
+              umma_bf16_ts(o_at, s_at + 8 * g, desc_of(v_lo + (g >> 1) * v_even + (g & 1) * v_odd, sbo), kIdPV,
+                           g > 0 ? 1u : accumulate);
+          } else {
+            for (int g = 0; 16 * g < keys; ++g)
+              umma_bf16_ts(o_at, s_at + 8 * g, desc_of(v_lo + (g >> 1) * v_even + (g & 1) * v_odd, sbo), kIdPV,
+                           g > 0 ? 1u : accumulate);
+          }
+          umma_commit(&pv_done[half]);
+        }
+        __syncwarp();
       };
       for (int k = 0; ok && more(k); ++k) {
         if (!take(k, it) || it.t.steps <= 0) continue;
-        const int halves = (it.t.tokens << p.group_log2) > 128 ? 2 : 1;
-        auto keys_of = [&](int v) {
-          return min(kPrefillKeys, it.t.end - (v + (v >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys);
+        const int steps = it.t.steps;
+        const bool two = (it.t.tokens << p.group_log2) > 128;
+        // Products in turns, a step's of one half and then of the other: both halves' at once
+        // would end, and their softmaxes begin, together, with the tensor cores idle meanwhile.
+        auto my_turn = [&] {
+          if (!two) return true;
+          const bool mine = all_wait(&turn[half], t_parity);
+          t_parity ^= 1;
+          return mine;
         };
-        ok = wait(q_full, items_done & 1) && wait(&full[c % R], (c / R) & 1);
-        if (!ok) break;
-        ++items_done;
-        tmem_fence_after();
-        for (int i = 0; i < halves; ++i) scores(i, c % R, keys_of(0));
-        umma_commit(&empty[c % R]);
-        if (it.t.steps == 1) umma_commit(q_empty);
-        ++c;
-        for (int v = 0; v < it.t.steps && ok; ++v) {
-          const uint32_t cv = c, ck = c + 1;               // V of this step, K of the next
-          const bool next = v + 1 < it.t.steps;
-          const int keys = keys_of(v);
-          for (int i = 0; i < halves && ok; ++i) {
-            if (i == 0) ok = wait(&full[cv % R], (cv / R) & 1);
-            ok = ok && wait(&p_full[i], kp[i] & 1);
-            if (v == 0) ok = ok && wait(&o_free[i], (ko[i] & 1) ^ 1);
-            if (!ok) break;
-            ++kp[i];
-            tmem_fence_after();
-            const uint32_t vt = ring + (cv % R) * Ly::TILE;
-            for (int g = 0; 16 * g < keys; ++g) {
-              const int page = (16 * g) >> p.block_log2, r = (16 * g) & (bs - 1);
-              const uint64_t vd = umma_desc(vt + page * bs * D * 2 + r * 128, bs * 128, 1024);
-              umma_bf16_ts(tmem + kTmemO + 128 * i, tmem + 128 * i + 8 * g, vd, kIdPV, v > 0 || g > 0 ? 1u : 0u);
-            }
-            umma_commit(&pv_done[i]);
-            if (next) {
-              if (i == 0) {
-                ok = wait(&full[ck % R], (ck / R) & 1);
-                if (!ok) break;
-                tmem_fence_after();
-              }
-              // (after the product that reads the weights that stand where S goes: the
-              // tensor cores take one thread's products in their order)
-              scores(i, ck % R, keys_of(v + 1));
-            }
+        auto pass_turn = [&] {
+          if (two && issues) mbar_arrive(&turn[half ^ 1]);
+        };
+        if (half == 1 && !two) {
+          // no rows for this half: the slots are given back as they come
+          for (int i = 0; i < 2 * steps && ok; ++i) {
+            ok = all_wait(&full[at.i], at.parity);
+            if (ok && issues) mbar_arrive(&empty[at.i]);
+            at.next();
           }
-          if (!ok) break;
-          umma_commit(&empty[cv % R]);
-          if (next) umma_commit(&empty[ck % R]);
-          if (v + 2 == it.t.steps) umma_commit(q_empty);
-          c += next ? 2 : 1;
+          if (ok) {
+            ok = all_wait(q_full, q_parity);
+            if (issues) mbar_arrive(q_empty);
+          }
+          q_parity ^= 1;
+          continue;
         }
-        ++ko[0];
-        if (halves == 2) ++ko[1];
+        // (the last step is the only one that may be short)
+        const int tail = it.t.end - (steps - 1 + (steps - 1 >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys;
+        const uint32_t id_tail = umma_idesc_bf16(128, (tail + 15) & ~15, false);
+        ok = all_wait(q_full, q_parity) && all_wait(&full[at.i], at.parity) && my_turn();
+        if (!ok) break;
+        q_parity ^= 1;
+        tmem_fence_after();
+        scores(at.i, steps == 1 ? id_tail : kIdS);
+        pass_turn();
+        if (issues) {
+          umma_commit(&empty[at.i]);
+          if (steps == 1) umma_commit(q_empty);
+        }
+        at.next();
+        for (int v = 0; v < steps; ++v) {
+          Slot kn = at;                                    // V of this step; K of the next
+          kn.next();
+          const bool next = v + 1 < steps;
+          ok = all_wait(&full[at.i], at.parity) && (v > 0 || all_wait(&o_free[half], o_parity)) && my_turn() &&
+               all_wait(&p_full[half], p_parity);
+          if (!ok) break;
+          tmem_fence_after();
+          values(at.i, next ? kPrefillKeys : tail, v > 0 ? 1u : 0u);
+          if (next && !(ok = all_wait(&full[kn.i], kn.parity))) break;
+          // (S goes where the weights stand that the product before reads: the tensor cores
+          // take one thread's products in their order)
+          if (next) scores(kn.i, v + 2 == steps ? id_tail : kIdS);
+          pass_turn();
+          if (issues) {
+            umma_commit(&empty[at.i]);
+            if (next) umma_commit(&empty[kn.i]);
+            if (v + 2 == steps) umma_commit(q_empty);
+          }
+          p_parity ^= 1;
+          at = kn;
+          if (next) at.next();
+        }
+        o_parity ^= 1;
       }
-      if (!ok) fail();
+      if (!ok && issues) fail();
       // nothing may be in flight when the columns are released
-      umma_commit(end);
-      mbar_wait(end, 0);
+      if (issues) {
+        umma_commit(end);
+        mbar_wait(end, 0);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else if (warp < kSoftmaxWarps) {
     // ------------------------------------------------------------ softmax: a row a thread
     const int half = warp >> 2;
@@ -413,48 +511,65 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
               if (!((sees >> i) & 1u)) s[32 * w + i] = -INFINITY;
           }
         }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
+        // The reference is the first step's maximum.  Weights need not be below 1 (bf16 has the
+        // range of float32), so it is only where a row's weights of a step come to more than
+        // 2^16, and so a score has passed it by far, that the reference follows, O is rescaled,
+        // and the weights are made again; no maximum is taken otherwise.
+        float sum_l = 0.f;
+        for (bool refer = v == 0;; refer = true) {
+          if (refer) {
+            float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-        const float x = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-        const bool grow = x > m + 8.f;
-        float alpha = 1.f;
-        if (grow) {
-          alpha = fast_exp2(m - x);
-          m = x;
-        }
-        l *= alpha;
-        if (v > 0 && __any_sync(kFull, grow)) {
-          ok = wait(&pv_done[half], (n - 1) & 1);          // O holds the steps so far
-          ok = __all_sync(kFull, ok);
-          if (!ok) break;
-          tmem_fence_after();
+            for (int i = 4; i + 8 <= 128; i += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[124 + e]);
+            const float x = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
+            float alpha = 1.f;
+            if (v == 0) {
+              m = fmaxf(x, kNoScore);
+            } else {
+              if (sum_l > kMostSum) {
+                alpha = fast_exp2(m - x);
+                m = x;
+              }
+              l *= alpha;
+              // (O holds the steps so far: S came after their products)
 #pragma unroll 1
-          for (int i = 0; i < D / 16; ++i) {
-            float o[16];
-            tmem_ld16(o_at + 16 * i, o);
-            tmem_landed(o);
+              for (int i = 0; i < D / 16; ++i) {
+                float o[16];
+                tmem_ld16(o_at + 16 * i, o);
+                tmem_landed(o);
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
+                tmem_st16(o_at + 16 * i, w);
+              }
+            }
+          }
+          uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+          const uint64_t sc2 = pair(sc, sc), nm2 = pair(-m, -m);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
             uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
-            tmem_st16(o_at + 16 * i, w);
+            for (int e = 0; e < 16; ++e) {
+              float a, b;
+              unpair(fma2(pair(s[32 * i + 2 * e], s[32 * i + 2 * e + 1]), sc2, nm2), a, b);
+              a = fast_exp2(a);
+              b = fast_exp2(b);
+              sum[e & 1] = add2(sum[e & 1], pair(a, b));
+              w[e] = pack_bf16x2(a, b);
+            }
+            tmem_st16(s_at + 16 * i, w);
           }
+          float l0, l1;
+          unpair(add2(sum[0], sum[1]), l0, l1);
+          sum_l = l0 + l1;
+          if (refer || !__any_sync(kFull, sum_l > kMostSum)) break;
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        const float nm = -m;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float a = fast_exp2(fmaf(s[32 * i + 2 * e], sc, nm)), b = fast_exp2(fmaf(s[32 * i + 2 * e + 1], sc, nm));
-            sum[(2 * e) & 3] += a;
-            sum[(2 * e + 1) & 3] += b;
-            w[e] = pack_bf16x2(a, b);
-          }
-          tmem_st16(s_at + 16 * i, w);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l += sum_l;
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
