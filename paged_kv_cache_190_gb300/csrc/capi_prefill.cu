@@ -15,7 +15,8 @@ size_t pa_prefill_workspace_size(int num_tokens, int num_seqs, int num_q_heads, 
   if (num_tokens < 0 || num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
       num_q_heads % num_kv_heads != 0 || (head_dim != 64 && head_dim != 128))
     return 0;
-  return pa::prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim);
+  const int sms = pa::current_sm_count();
+  return sms <= 0 ? 0 : pa::prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, sms);
 }
 
 int pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -49,7 +50,7 @@ int pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cach
   const int sms = pa::current_sm_count();
   if (sms <= 0) return PA_ERR_CUDA;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-      workspace_bytes < pa::prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim))
+      workspace_bytes < pa::prefill_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, sms))
     return PA_ERR_WORKSPACE;
   pa::PrefillArgs a = {};
   a.out = out;

@@ -25,9 +25,14 @@ struct PrefillParams {
   const int32_t* tables;
   const int32_t* lens;
   const int32_t* starts;
-  int32_t* header;                                // [0] tiles in the list
-  int2* list;                                     // {sequence, tile}, the longest first
+  int32_t* header;                                // the plan: see prefill_launch.cu
+  int4* list;                                     // {sequence, tile, steps (at least 1), steps before}
+  int4* begin;                                    // shares: {list entry, kv head, step} that each CTA begins with
   int room;                                       // entries that the list has room for
+  int may_share, ctas;                            // the host's leave to cut items; CTAs
+  float* part_out;                                // shares: [2 ctas][slot_rows][head_dim]
+  float* part_lse;                                // shares: [2 ctas][slot_rows]
+  int slot_rows;
   float scale_log2;                               // scale * log2(e): logits in base 2
   int num_seqs, num_tokens, group, group_log2, num_q_heads, num_kv_heads, block_size, block_log2;
   int num_blocks, max_blocks, max_len, window, sinks;
@@ -53,7 +58,8 @@ struct PrefillArgs {
   int64_t wait_limit;
 };
 
-size_t prefill_workspace_size(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim);
+size_t prefill_workspace_size(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                              int num_sms);
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t run_prefill_bf16(int head_dim, const PrefillParams& p, int grid, cudaStream_t stream);
 cudaError_t run_prefill_f32(int head_dim, const PrefillParams& p, int grid, cudaStream_t stream);
@@ -97,10 +103,67 @@ __device__ __forceinline__ PrefillTile prefill_tile(const PrefillParams& p, cons
   t.steps = (t.end + KEYS - 1) / KEYS - t.shift;
   return t;
 }
-// Item k of CTA c of `ctas`: there and back, so that a CTA's long items and short ones add up.
-__device__ __forceinline__ int prefill_item(int k, int c, int ctas) {
-  return k * ctas + ((k & 1) ? ctas - 1 - c : c);
-}
+// The items of a CTA, one after another: a kv head and a tile of rows, with steps v0 .. v1 - 1
+// of its keys.  Whole items are dealt out there and back, so that a CTA's long ones and short
+// ones add up; in shares a CTA goes on from where it begins.
+struct PrefillItem {
+  int b, h, v0, v1;
+  int slot;                                       // of its partial result, -1: whole
+  PrefillTile t;
+};
+template <int KEYS>
+struct PrefillWalk {
+  const PrefillParams& p;
+  int tile_tokens, items, share, k, e, h, v, left;
+  __device__ __forceinline__ PrefillWalk(const PrefillParams& p_, int tile_tokens_) : p(p_), tile_tokens(tile_tokens_) {
+    items = p.header[0] * p.num_kv_heads;
+    share = p.header[1];
+    k = 0;
+    e = h = v = left = 0;
+    if (share > 0) {
+      left = min(share, p.header[2] - static_cast<int>(blockIdx.x) * share);
+      if (left > 0) {
+        const int4 at = p.begin[blockIdx.x];
+        e = at.x;
+        h = at.y;
+        v = at.z;
+      }
+    }
+  }
+  __device__ __forceinline__ bool next(PrefillItem& it) {
+    int4 entry;
+    it.slot = -1;
+    if (share > 0) {
+      if (left <= 0) return false;
+      entry = p.list[e];
+      it.h = h;
+      it.v0 = v;
+      it.v1 = min(entry.z, v + left);
+      left -= it.v1 - it.v0;
+      if (it.v0 > 0 || it.v1 < entry.z) it.slot = 2 * blockIdx.x + (k > 0 ? 1 : 0);
+      v = 0;
+      if (++h == p.num_kv_heads) {
+        h = 0;
+        ++e;
+      }
+    } else {
+      const int ctas = gridDim.x;
+      int i = k * ctas + ((k & 1) ? ctas - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
+      if (i >= items) {
+        // (the last round may leave this CTA out; no later one has an item for it)
+        return false;
+      }
+      entry = p.list[i / p.num_kv_heads];
+      it.h = i % p.num_kv_heads;
+      it.v0 = 0;
+      it.v1 = entry.z;
+    }
+    ++k;
+    it.b = entry.x;
+    it.t = prefill_tile<KEYS>(p, prefill_seq(p, entry.x), entry.y, tile_tokens);
+    return true;
+  }
+};
 #endif
 
 }  // namespace pa

@@ -58,9 +58,10 @@ struct PrefillLayout {
   static constexpr int Q_SLAB = 128 * 128;                 // 128 rows of 64 columns
   static constexpr int Q_HALF = SLABS * Q_SLAB;
   static constexpr int TILE = kPrefillKeys * D * 2;
-  static constexpr int RING = D == 128 ? 5 : 8;
+  static constexpr int RING = D == 128 ? 4 : 8;            // (5 of 32 KiB are no faster)
   static constexpr int OFF_RING = 2 * Q_HALF;
-  static constexpr int OFF_BAD = OFF_RING + RING * TILE;
+  static constexpr int OFF_STAGE = OFF_RING + RING * TILE; // 32 rows of 128 bytes a softmax warp
+  static constexpr int OFF_BAD = OFF_STAGE + kSoftmaxWarps * 32 * 128;
   static constexpr int OFF_BARS = OFF_BAD + kBadRing * 4;
   // full, empty, raw [RING]; q_full, q_empty; s_full, p_full, pv_done, o_free, turn [2]; end
   static constexpr int NUM_BARS = 3 * RING + 2 + 10 + 1;
@@ -168,7 +169,6 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
   const uint32_t tmem = *tmem_slot;
   wait_prior_grids();                                      // the plan's list
   allow_next_grid();
-  const int items = p.header[0] * p.num_kv_heads;
   auto fail = [&]() {
     if (!*abort_flag) {
       report(p.device_errors, PA_DEVERR_TIMEOUT);
@@ -178,21 +178,8 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_try_wait(bar, parity) || (!*abort_flag && mbar_wait(bar, parity, p.wait_limit));
   };
-  // item k of this CTA: false past the last
-  struct Item {
-    int b, h;
-    PrefillTile t;
-  };
-  auto take = [&](int k, Item& it) {
-    const int i = prefill_item(k, blockIdx.x, gridDim.x);
-    if (k * static_cast<int>(gridDim.x) >= items || i >= items) return false;
-    const int2 e = p.list[i / p.num_kv_heads];
-    it.b = e.x;
-    it.h = i % p.num_kv_heads;
-    it.t = prefill_tile<kPrefillKeys>(p, prefill_seq(p, e.x), e.y, tile_tokens);
-    return true;
-  };
-  auto more = [&](int k) { return k * static_cast<int>(gridDim.x) < items; };
+  PrefillWalk<kPrefillKeys> walk(p, tile_tokens);
+  PrefillItem it;
   // keys [x, y) of a step that starts at key t0 are behind the window and no sinks
   auto hidden = [&](const PrefillTile& t, int t0, int hi, int& x, int& y) {
     x = max(t0, p.sinks);
@@ -200,6 +187,10 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
     return x < y;
   };
 
+  // A softmax thread holds a row's 128 scores.  The block has 384 * 168 = 64512 registers:
+  // 256 * 184 + 128 * 136.
+  if (warp >= kSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
   if (warp == kProducer) {
     // ------------------------------------------------------------ copies
     const int bs = p.block_size, pages_of_step = kPrefillKeys >> p.block_log2;
@@ -207,10 +198,9 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
     uint32_t c = 0, steps = 0, raw_used = 0, raw_parity = 0;   // ring slots filled; raw: a bit a slot
     bool ok = true;
     int items_done = 0;
-    Item it;
-    for (int k = 0; ok && more(k); ++k) {
-      if (!take(k, it) || it.t.steps <= 0) continue;
-      if (lane == 0) {
+    while (ok && walk.next(it)) {
+      if (it.t.steps <= 0) continue;
+      if (lane == 0) {                                     // q, once the last item's is no longer read
         ok = wait(q_empty, (items_done & 1) ^ 1);
         if (ok) {
           const int halves = (it.t.tokens << p.group_log2) > 128 ? 2 : 1;
@@ -228,14 +218,14 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
       // lane l: page l of a step, as a row of the pool's map (-1: not there, reads zeros;
       // -2: nobody sees it, not read); the next step's is looked up ahead
       auto look = [&](int v) {
-        if (v >= it.t.steps || lane >= pages_of_step) return -2;
+        if (v >= it.v1 || lane >= pages_of_step) return -2;
         const int first = (v + (v >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys + lane * bs;
         if (first >= it.t.end || (first >= p.sinks && first + bs <= it.t.lo)) return -2;
         const int page = table[first >> p.block_log2];
         return page >= 0 && page < p.num_blocks ? page * p.num_kv_heads + it.h : -1;
       };
-      int ahead = look(0);
-      for (int v = 0; v < it.t.steps; ++v, ++steps) {
+      int ahead = look(it.v0);
+      for (int v = it.v0; v < it.v1; ++v, ++steps) {
         const int z = ahead;
         ahead = look(v + 1);
         const int t0 = (v + (v >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys, hi = min(it.t.end, t0 + kPrefillKeys);
@@ -295,10 +285,9 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
     // ------------------------------------------------------------ V rows that nobody sees
     uint32_t c = 0, raw_parity = 0;
     bool ok = true;
-    Item it;
-    for (int k = 0; ok && more(k); ++k) {
-      if (!take(k, it)) continue;
-      for (int v = 0; v < it.t.steps && ok; ++v, c += 2) {
+    while (ok && walk.next(it)) {
+      if (it.t.steps <= 0) continue;
+      for (int v = it.v0; v < it.v1 && ok; ++v, c += 2) {
         const int slot = (c + 1) % R;
         const int t0 = (v + (v >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys, hi = min(it.t.end, t0 + kPrefillKeys);
         int x, y;
@@ -354,8 +343,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
       } at{0, 0};
       uint32_t p_parity = 0, o_parity = 1, q_parity = 0, t_parity = half ^ 1;
       bool ok = true;
-      Item it;
-      // (the lanes agree on giving up)
+        // (the lanes agree on giving up)
       auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, wait(bar, parity)) != 0; };
       // S = this half's rows of q times the K tile in `slot`
       auto scores = [&](uint32_t slot, uint32_t id) {
@@ -388,9 +376,9 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
         }
         __syncwarp();
       };
-      for (int k = 0; ok && more(k); ++k) {
-        if (!take(k, it) || it.t.steps <= 0) continue;
-        const int steps = it.t.steps;
+      while (ok && walk.next(it)) {
+        if (it.t.steps <= 0) continue;
+        const int steps = it.v1 - it.v0;
         const bool two = (it.t.tokens << p.group_log2) > 128;
         // Products in turns, a step's of one half and then of the other: both halves' at once
         // would end, and their softmaxes begin, together, with the tensor cores idle meanwhile.
@@ -418,7 +406,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
           continue;
         }
         // (the last step is the only one that may be short)
-        const int tail = it.t.end - (steps - 1 + (steps - 1 >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys;
+        const int tail = min(kPrefillKeys, it.t.end - (it.v1 - 1 + (it.v1 - 1 >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys);
         const uint32_t id_tail = umma_idesc_bf16(128, (tail + 15) & ~15, false);
         ok = all_wait(q_full, q_parity) && all_wait(&full[at.i], at.parity) && my_turn();
         if (!ok) break;
@@ -464,7 +452,9 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
       }
       __syncwarp();
     }
-  } else if (warp < kSoftmaxWarps) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ------------------------------------------------------------ softmax: a row a thread
     const int half = warp >> 2;
     const int r = half * 128 + (warp & 3) * 32 + lane;     // row of the item
@@ -473,12 +463,10 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
     const float sc = p.scale_log2;
     uint32_t n = 0, steps = 0;                             // this half's steps; the CTA's
     bool ok = true;
-    Item it;
-    for (int k = 0; ok && more(k); ++k) {
-      if (!take(k, it)) continue;
+    while (ok && walk.next(it)) {
       const PrefillTile& t = it.t;
       if (half == 1 && (t.tokens << p.group_log2) <= 128) {
-        steps += t.steps;
+        steps += t.steps > 0 ? it.v1 - it.v0 : 0;
         continue;
       }
       const int j = r >> p.group_log2;
@@ -486,7 +474,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
       const int first_pos = t.pos0 + ((r & ~31) >> p.group_log2);
       const int last_pos = t.pos0 + min((r | 31) >> p.group_log2, t.tokens - 1);
       float m = kNoScore, l = 0.f;
-      for (int v = 0; v < t.steps; ++v, ++n, ++steps) {
+      for (int v = it.v0; v < (t.steps > 0 ? it.v1 : it.v0); ++v, ++n, ++steps) {
         const int t0 = (v + (v >= t.ns ? t.shift : 0)) * kPrefillKeys;
         ok = wait(&s_full[half], n & 1);
         ok = __all_sync(kFull, ok);
@@ -516,7 +504,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
         // 2^16, and so a score has passed it by far, that the reference follows, O is rescaled,
         // and the weights are made again; no maximum is taken otherwise.
         float sum_l = 0.f;
-        for (bool refer = v == 0;; refer = true) {
+        for (bool refer = v == it.v0;; refer = true) {
           if (refer) {
             float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -527,7 +515,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
             for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[124 + e]);
             const float x = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
             float alpha = 1.f;
-            if (v == 0) {
+            if (v == it.v0) {
               m = fmaxf(x, kNoScore);
             } else {
               if (sum_l > kMostSum) {
@@ -576,13 +564,31 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
         if (lane == 0) mbar_arrive(&p_full[half]);
       }
       if (!ok) break;
-      // ---- the rows
-      const bool valid = j < t.tokens;
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
-          ((static_cast<int64_t>(t.row0) + j) * p.num_q_heads + it.h * p.group + (r & (p.group - 1))) * D);
+      // ---- the rows, 128 bytes of each at a time: through shared memory, so that a store
+      // has whole lines of 4 rows (a lane's own row in 16-byte pieces is 32 lines an
+      // instruction: all stores together took a tenth of the kernel's time)
+      unsigned char* stage = smem + Ly::OFF_STAGE + warp * (32 * 128);
+      const int r0 = r & ~31, line = lane >> 3, chunk = lane & 7;
+      auto put = [&](const uint32_t (&w)[32], unsigned char* to, int64_t token_bytes, int64_t head_bytes) {
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(stage + sw128(lane, c)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = r0 + 4 * i + line, jj = rr >> p.group_log2;
+          if (jj < t.tokens)
+            *reinterpret_cast<uint4*>(to + jj * token_bytes + (rr & (p.group - 1)) * head_bytes + 16 * chunk) =
+                *reinterpret_cast<const uint4*>(stage + sw128(4 * i + line, chunk));
+        }
+      };
+      unsigned char* out = static_cast<unsigned char*>(p.out) +
+          (static_cast<int64_t>(t.row0) * p.num_q_heads + it.h * p.group) * (2 * D);
+      const int64_t out_token = static_cast<int64_t>(p.num_q_heads) * (2 * D);
       if (t.steps <= 0) {                                  // nothing to see
-        if (valid)
-          for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t zeros[32] = {};
+        for (int i = 0; i < D / 64; ++i) put(zeros, out + 128 * i, out_token, 2 * D);
         continue;
       }
       ok = wait(&pv_done[half], (n - 1) & 1);
@@ -590,18 +596,32 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
       if (!ok) break;
       tmem_fence_after();
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      if (it.slot < 0) {
+#pragma unroll 1
+        for (int i = 0; i < D / 64; ++i) {
+          float o[64];
+          tmem_ld32(o_at + 64 * i, o);
+          tmem_ld32(o_at + 64 * i + 32, o + 32);
+          tmem_landed(o);
+          uint32_t w[32];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        float o[32];
-        tmem_ld32(o_at + 32 * i, o);
-        tmem_landed(o);
-        if (valid)
+          for (int e = 0; e < 32; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+          put(w, out + 128 * i, out_token, 2 * D);
+        }
+      } else {
+        const int64_t row = static_cast<int64_t>(it.slot) * p.slot_rows;
+        if (j < t.tokens) p.part_lse[row + r] = l > 0.f ? m + __log2f(l) : (l != l ? l : -INFINITY);
+        unsigned char* part = reinterpret_cast<unsigned char*>(p.part_out + row * D);
+#pragma unroll 1
+        for (int i = 0; i < D / 32; ++i) {
+          float o[32];
+          tmem_ld32(o_at + 32 * i, o);
+          tmem_landed(o);
+          uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[4 * i + e] = make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                        pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                        pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                        pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * inv);
+          put(w, part + 128 * i, static_cast<int64_t>(p.group) * (4 * D), 4 * D);
+        }
       }
       tmem_fence_before();
       __syncwarp();

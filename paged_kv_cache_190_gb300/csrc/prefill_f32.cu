@@ -49,15 +49,13 @@ __global__ void __launch_bounds__(kThreadsF32, D == 128 ? 1 : 2) prefill_f32_ker
   allow_next_grid();
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int tile_tokens = kRowsF32 >> p.group_log2;
-  const int items = p.header[0] * p.num_kv_heads;
   const float* q = static_cast<const float*>(p.q);
-  for (int k = 0; k * static_cast<int>(gridDim.x) < items; ++k) {
-    const int item = prefill_item(k, blockIdx.x, gridDim.x);
-    if (item >= items) continue;
-    const int2 e = p.list[item / p.num_kv_heads];
-    const int h = item % p.num_kv_heads;
-    const PrefillTile t = prefill_tile<kKeysF32>(p, prefill_seq(p, e.x), e.y, tile_tokens);
-    const int32_t* table = p.tables + static_cast<int64_t>(e.x) * p.max_blocks;
+  PrefillWalk<kKeysF32> walk(p, tile_tokens);
+  PrefillItem it;
+  while (walk.next(it)) {
+    const int h = it.h;
+    const PrefillTile& t = it.t;
+    const int32_t* table = p.tables + static_cast<int64_t>(it.b) * p.max_blocks;
     auto row_of = [&](int r) {                             // of q and out
       return ((static_cast<int64_t>(t.row0) + (r >> p.group_log2)) * p.num_q_heads + h * p.group + (r & (p.group - 1))) * D;
     };

@@ -65,3 +65,31 @@ def test_ragged_batches(dtype, hq, hkv, d, bs, window, sinks):
     dv.call()
     assert dv.errors() == 0
     check(c, dv.out)
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs", [(8, 2, 128, 16), (8, 1, 128, 32), (4, 4, 64, 16), (1, 1, 128, 16), (32, 8, 128, 16)])
+@pytest.mark.parametrize("new,had", [([1], [5000]), ([64, 3, 200], [3000, 7000, 0]), ([130], [20000]),
+                                     ([700, 1, 0, 33], [900, 600, 700, 5000])])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1500, 70)])
+def test_few_rows_of_long_contexts(hq, hkv, d, bs, new, had, window, sinks):
+    """Items too few to fill the GPU: their keys are cut into shares and joined."""
+    c = Prompts(hq + sum(had), "bf16", new, had, hq, hkv, d, bs, window, sinks, before=1, behind=2)
+    dv = Dev(c)
+    dv.call()
+    assert dv.errors() == 0
+    check(c, dv.out)
+    again = torch.full_like(dv.out, 7.0)
+    size = pa.pa_prefill_workspace_size(c.rows, len(new), hq, hkv, d)
+    dv.call(again, workspace=torch.full((size,), 0x7F, dtype=torch.uint8, device=DEV))
+    assert torch.equal(again.view(torch.int16), dv.out.view(torch.int16)), "not the same bits twice"
+
+
+def test_workspace_size():
+    f = pa.pa_prefill_workspace_size
+    assert f(0, 0, 8, 8, 128) >= 256 and f(1000, 3, 32, 8, 128) >= f(1000, 3, 8, 8, 128) >= f(10, 3, 8, 8, 128)
+    c = Prompts(1, "bf16", [40], [10], 8, 2, 128, 16)
+    dv = Dev(c)
+    with pytest.raises(pa.PaError):
+        dv.call(workspace=torch.empty(f(c.rows, 1, 8, 2, 128) - 1, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError):
+        dv.call(prepare=True)
