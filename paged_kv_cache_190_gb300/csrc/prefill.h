@@ -26,9 +26,9 @@ struct PrefillParams {
   const int32_t* lens;
   const int32_t* starts;
   int32_t* header;                                // the plan: see prefill_launch.cu
-  int4* list;                                     // {sequence, tile, steps (at least 1), steps before}
-  int4* begin;                                    // shares: {list entry, kv head, step} that each CTA begins with
-  int room;                                       // entries that the list has room for
+  int4* tiles;                                    // {sequence, tile, steps (at least 1)}, the longest first
+  int room;                                       // entries that it has room for
+  int4* begin;                                    // shares: {item, its first step, steps} of each CTA
   int may_share, ctas;                            // the host's leave to cut items; CTAs
   float* part_out;                                // shares: [2 ctas][slot_rows][head_dim]
   float* part_lse;                                // shares: [2 ctas][slot_rows]
@@ -69,13 +69,15 @@ cudaError_t run_prefill_f32(int head_dim, const PrefillParams& p, int grid, cuda
 struct PrefillSeq {
   int q0, n, len;
 };
-__device__ __forceinline__ PrefillSeq prefill_seq(const PrefillParams& p, int b) {
+__device__ __forceinline__ PrefillSeq prefill_seq(const PrefillParams& p, int a, int e, int len) {
   PrefillSeq s;
-  const int a = p.starts[b], e = p.starts[b + 1];
   s.q0 = min(max(a, 0), p.num_tokens);
   s.n = (a < 0 || e > p.num_tokens) ? 0 : max(e - s.q0, 0);
-  s.len = min(max(p.lens[b], 0), p.max_len);
+  s.len = min(max(len, 0), p.max_len);
   return s;
+}
+__device__ __forceinline__ PrefillSeq prefill_seq(const PrefillParams& p, int b) {
+  return prefill_seq(p, p.starts[b], p.starts[b + 1], p.lens[b]);
 }
 
 // What a tile of rows has to read: keys [0, end) without those that no row sees, as a list
@@ -103,9 +105,12 @@ __device__ __forceinline__ PrefillTile prefill_tile(const PrefillParams& p, cons
   t.steps = (t.end + KEYS - 1) / KEYS - t.shift;
   return t;
 }
+// Item k of CTA c: item i is kv head i % heads of the list's tile i / heads.  Dealt out there and
+// back, so that a CTA's long ones and short ones add up.
+__device__ __forceinline__ int prefill_deal(int k, int c, int ctas) { return k * ctas + ((k & 1) ? ctas - 1 - c : c); }
+
 // The items of a CTA, one after another: a kv head and a tile of rows, with steps v0 .. v1 - 1
-// of its keys.  Whole items are dealt out there and back, so that a CTA's long ones and short
-// ones add up; in shares a CTA goes on from where it begins.
+// of its keys; whole ones, and then those of its share.
 struct PrefillItem {
   int b, h, v0, v1;
   int slot;                                       // of its partial result, -1: whole
@@ -114,51 +119,43 @@ struct PrefillItem {
 template <int KEYS>
 struct PrefillWalk {
   const PrefillParams& p;
-  int tile_tokens, items, share, k, e, h, v, left;
+  int tile_tokens, items, k, rounds, left;        // left: steps of the share, -1: not begun
+  int e;
   __device__ __forceinline__ PrefillWalk(const PrefillParams& p_, int tile_tokens_) : p(p_), tile_tokens(tile_tokens_) {
     items = p.header[0] * p.num_kv_heads;
-    share = p.header[1];
-    k = 0;
-    e = h = v = left = 0;
-    if (share > 0) {
-      left = min(share, p.header[2] - static_cast<int>(blockIdx.x) * share);
-      if (left > 0) {
-        const int4 at = p.begin[blockIdx.x];
-        e = at.x;
-        h = at.y;
-        v = at.z;
-      }
-    }
+    k = e = 0;
+    left = p.header[1] ? -1 : 0;
+    rounds = left ? items / static_cast<int>(gridDim.x) : 1 << 30;
   }
   __device__ __forceinline__ bool next(PrefillItem& it) {
-    int4 entry;
+    int i, n;
     it.slot = -1;
-    if (share > 0) {
-      if (left <= 0) return false;
-      entry = p.list[e];
-      it.h = h;
-      it.v0 = v;
-      it.v1 = min(entry.z, v + left);
-      left -= it.v1 - it.v0;
-      if (it.v0 > 0 || it.v1 < entry.z) it.slot = 2 * blockIdx.x + (k > 0 ? 1 : 0);
-      v = 0;
-      if (++h == p.num_kv_heads) {
-        h = 0;
-        ++e;
-      }
+    it.v0 = 0;
+    if (k < rounds) {
+      i = prefill_deal(k++, blockIdx.x, gridDim.x);
+      if (i >= items) return false;               // (no later round has one for this CTA)
+      n = 1 << 30;
     } else {
-      const int ctas = gridDim.x;
-      int i = k * ctas + ((k & 1) ? ctas - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
-      if (i >= items) {
-        // (the last round may leave this CTA out; no later one has an item for it)
-        return false;
+      int slot = 2 * blockIdx.x + 1;
+      if (left < 0) {
+        const int4 at = p.begin[blockIdx.x];
+        e = at.x;
+        it.v0 = at.y;
+        left = at.z;
+        slot = 2 * blockIdx.x;
       }
-      entry = p.list[i / p.num_kv_heads];
-      it.h = i % p.num_kv_heads;
-      it.v0 = 0;
-      it.v1 = entry.z;
+      if (left <= 0) return false;
+      i = e++;
+      n = left;
+      it.slot = slot;
     }
-    ++k;
+    const int4 entry = p.tiles[i / p.num_kv_heads];
+    it.h = i % p.num_kv_heads;
+    it.v1 = entry.z - it.v0 > n ? it.v0 + n : entry.z;
+    if (it.slot >= 0) {
+      left -= it.v1 - it.v0;
+      if (it.v0 == 0 && it.v1 == entry.z) it.slot = -1;
+    }
     it.b = entry.x;
     it.t = prefill_tile<KEYS>(p, prefill_seq(p, entry.x), entry.y, tile_tokens);
     return true;

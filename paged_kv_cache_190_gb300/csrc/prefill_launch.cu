@@ -16,167 +16,229 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBuckets = 256;
+constexpr int kPlanSeqs = 1024, kPlanTiles = 1536;          // kept in shared memory
+
+template <int CPL>
+__device__ __forceinline__ void load_cols(const float* p, float* v) {
+  if constexpr (CPL == 4) {
+    const float4 t = *reinterpret_cast<const float4*>(p);
+    v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+  } else {
+    const float2 t = *reinterpret_cast<const float2*>(p);
+    v[0] = t.x; v[1] = t.y;
+  }
+}
+
+// Exclusive sum of a block's values; `all` is their sum in every thread.
+__device__ __forceinline__ int block_before(int x, int* sums, int& all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int y = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
+  }
+  __syncthreads();                                         // (the last sums have been read)
+  if (lane == 31) sums[warp] = y;
+  __syncthreads();
+  int before = y - x;
+  all = 0;
+#pragma unroll
+  for (int i = 0; i < kPlanThreads / 32; ++i) {
+    if (i < warp) before += sums[i];
+    all += sums[i];
+  }
+  return before;
+}
 
 // One block: the tiles of all sequences, sorted by how many steps they take (a counting
 // sort over 256 lengths), the longest first: dealt out in turns they then end together.
-// Which of two equally long tiles comes first is left open; no result depends on it.
-//   header: [0] tiles, [1] the steps of a share (0: items stay whole), [2] steps in all
-// Few long items do not come out even: where the busiest CTA would take kShareCost steps more
-// than its part, all steps are laid end to end and every CTA takes an equal run of them; an
-// item that a run's end cuts leaves partial results for prefill_join_kernel (which cost about
-// as much as those steps).
-constexpr int kWholeRounds = 6;                            // items of a CTA that come out even
+//   header: [0] tiles, [1] whether there are shares
+// Whole items are dealt out in rounds.  Where the busiest CTA would take kShareCost steps more
+// than its part that way, the items of the last, incomplete round are laid end to end and each
+// CTA takes a run of them that makes up for what it has less than the others; an item that a
+// run's end cuts leaves partial results for prefill_join_kernel (which cost about as much as
+// those steps).  (Shares of all items even out no better, and the tiles of one sequence and
+// head, which whole rounds read together, then read their keys from HBM again and again: 6
+// chunks behind up to 15000 tokens 1.1 GB and 260 us, kRoundsMeasured.)
 constexpr int kShareCost = 12;
+constexpr int kMostRounds = 8;                             // (at most kPlanTiles tiles then)
 constexpr int kMostShared = 1 << 27;                       // keys: steps of all items within 31 bits
 constexpr int kLeastShare = 4;                             // steps: less is not worth a partial
 template <int KEYS>
 __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PrefillParams p, int tile_rows) {
-  __shared__ int most, tiles, count[kPlanBuckets], next[kPlanBuckets], sums[kPlanThreads / 32], busiest;
-  wait_prior_grids();
+  __shared__ int most, count[kPlanBuckets], next[kPlanBuckets], sums[kPlanThreads / 32], busiest;
+  __shared__ int item_from[kPlanThreads];
+  __shared__ PrefillSeq seqs[kPlanSeqs];
+  __shared__ int2 unsorted[kPlanTiles];
+  __shared__ int sorted[kPlanTiles];                       // steps
   allow_next_grid();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int me = threadIdx.x, warp = me >> 5, lane = me & 31;
   const int tokens = tile_rows >> p.group_log2;
-  if (threadIdx.x == 0) most = 1;
-  if (threadIdx.x < kPlanBuckets) count[threadIdx.x] = 0;
+  if (me == 0) most = 1;
+  if (me < kPlanBuckets) count[me] = 0;
+  wait_prior_grids();
   __syncthreads();
   bool bad = false;
   int longest = 1;
-  for (int b = threadIdx.x; b < p.num_seqs; b += kPlanThreads) {
-    const PrefillSeq s = prefill_seq(p, b);
+  for (int b = me; b < p.num_seqs; b += kPlanThreads) {
     const int a = p.starts[b], e = p.starts[b + 1], len = p.lens[b];
+    const PrefillSeq s = prefill_seq(p, a, e, len);
+    if (b < kPlanSeqs) seqs[b] = s;
     bad |= a < 0 || e < a || e > p.num_tokens || len < 0 || len > p.max_len || s.n > s.len;
     // (a sequence's last tile has the most steps, but for one more at a window's border)
     if (s.n > 0) longest = max(longest, prefill_tile<KEYS>(p, s, (s.n - 1) / tokens, tokens).steps);
   }
   if (bad) report(p.device_errors, PA_DEVERR_BAD_LENGTH);
-  atomicMax(&most, longest);
-  __syncthreads();
-  auto bucket = [&](int steps) {
-    return static_cast<int>(min(static_cast<long long>(kPlanBuckets - 1),
-                                static_cast<long long>(steps) * (kPlanBuckets - 1) / most));
-  };
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int b = warp; b < p.num_seqs; b += kPlanThreads / 32) {
-      const PrefillSeq s = prefill_seq(p, b);
-      for (int t = lane; t * tokens < s.n; t += 32) {
-        const int k = kPlanBuckets - 1 - bucket(prefill_tile<KEYS>(p, s, t, tokens).steps);
-        if (pass == 0) atomicAdd(&count[k], 1);
-        else {
-          // (room enough but for q_starts that decrease, whose last tiles are left out)
-          const int at = atomicAdd(&next[k], 1);
-          if (at < p.room) p.list[at] = make_int4(b, t, max(1, prefill_tile<KEYS>(p, s, t, tokens).steps), 0);
-        }
-      }
-    }
-    __syncthreads();
-    if (pass == 0) {
-      if (threadIdx.x < 32) {                              // where each bucket begins
-        int sum = 0;
-        for (int i = lane * (kPlanBuckets / 32); i < (lane + 1) * (kPlanBuckets / 32); ++i) sum += count[i];
-        int x = sum;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
-        }
-        int at = x - sum;
-        for (int i = lane * (kPlanBuckets / 32); i < (lane + 1) * (kPlanBuckets / 32); ++i) {
-          next[i] = at;
-          at += count[i];
-        }
-        if (lane == 31) {
-          tiles = min(x, p.room);
-          p.header[0] = tiles;
-        }
-      }
-      __syncthreads();
+  for (int o = 1; o < 32; o <<= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+  if (lane == 0) atomicMax(&most, longest);
+  __syncthreads();
+  const float buckets = static_cast<float>(kPlanBuckets - 1) / static_cast<float>(most);
+  auto bucket = [&](int steps) { return kPlanBuckets - 1 - min(kPlanBuckets - 1, static_cast<int>(static_cast<float>(steps) * buckets)); };
+  auto tiles_do = [&](auto f) {                            // f(sequence, tile, steps) for all tiles
+    for (int b = warp; b < p.num_seqs; b += kPlanThreads / 32) {
+      const PrefillSeq s = b < kPlanSeqs ? seqs[b] : prefill_seq(p, b);
+      for (int t = lane; t * tokens < s.n; t += 32) f(b, t, prefill_tile<KEYS>(p, s, t, tokens).steps);
     }
-  }
-  // ---- shares
-  const int heads = p.num_kv_heads, n = tiles;
-  const long long items = static_cast<long long>(n) * heads;
-  const bool few = p.may_share && n <= kPlanThreads && items < static_cast<long long>(kWholeRounds) * p.ctas;
-  if (!few) {
-    if (threadIdx.x == 0) p.header[1] = 0;
+  };
+  tiles_do([&](int, int, int steps) { atomicAdd(&count[bucket(steps)], 1); });
+  __syncthreads();
+  int all;
+  const int before = block_before(me < kPlanBuckets ? count[me] : 0, sums, all);   // where each bucket begins
+  if (me < kPlanBuckets) next[me] = before;
+  const int tiles = min(all, p.room);                      // (room enough but for q_starts that decrease)
+  if (me == 0) p.header[0] = tiles;
+  __syncthreads();
+  const bool here = all <= kPlanTiles && all <= p.room;
+  tiles_do([&](int b, int t, int steps) {
+    const int at = atomicAdd(&next[bucket(steps)], 1);
+    if (here) unsorted[at] = make_int2(b, t);
+    else if (at < p.room) p.tiles[at] = make_int4(b, t, max(1, steps), 0);
+  });
+  __syncthreads();
+  // (which of the tiles of a bucket came first is chance, and shares cut items by their place:
+  // in the order of their numbers, so that a call's result is always the same)
+  if (here)
+    for (int i = me; i < all; i += kPlanThreads) {
+      const int2 x = unsorted[i];
+      const PrefillSeq s = x.x < kPlanSeqs ? seqs[x.x] : prefill_seq(p, x.x);
+      const int steps = prefill_tile<KEYS>(p, s, x.y, tokens).steps;
+      const int k = bucket(steps), end = next[k], begin = end - count[k];
+      int at = begin;
+      for (int j = begin; j < end; ++j) {
+        const int2 y = unsorted[j];
+        at += y.x < x.x || (y.x == x.x && y.y < x.y) ? 1 : 0;
+      }
+      sorted[at] = max(1, steps);
+      p.tiles[at] = make_int4(x.x, x.y, max(1, steps), 0);
+    }
+  __syncthreads();
+  // ---- what comes out uneven goes out in shares
+  const int heads = p.num_kv_heads, ctas = p.ctas;
+  const long long items = static_cast<long long>(tiles) * heads;
+  const int rounds = static_cast<int>(items / ctas), whole = rounds * ctas, rest = static_cast<int>(items) - whole;
+  if (!p.may_share || !here || items > static_cast<long long>(kMostRounds) * ctas) {
+    if (me == 0) p.header[1] = 0;
     return;
   }
-  // the steps of the busiest CTA, were the items dealt out whole
-  if (threadIdx.x == 0) busiest = 0;
+  if (me == 0) busiest = 0;
   __syncthreads();
-  if (static_cast<int>(threadIdx.x) < p.ctas) {
-    int sum = 0;
-    for (int k = 0; k * p.ctas < items; ++k) {
-      const int i = k * p.ctas + ((k & 1) ? p.ctas - 1 - static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x));
-      if (i < items) sum += p.list[i / heads].z;
+  int mine = 0;                                            // steps of CTA `me`'s whole items
+  if (me < ctas) {
+    int last = 0;
+    for (int k = 0; k <= rounds; ++k) {
+      const int i = prefill_deal(k, me, ctas);
+      const int steps = i < items ? sorted[i / heads] : 0;
+      if (k < rounds) mine += steps; else last = steps;
     }
-    atomicMax(&busiest, sum);
+    atomicMax(&busiest, mine + last);
   }
-  const int w = static_cast<int>(threadIdx.x) < n ? p.list[threadIdx.x].z : 0;
-  int x = w;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) sums[warp] = x;
-  __syncthreads();
-  int before = x - w, total = 0;
-  for (int i = 0; i < kPlanThreads / 32; ++i) {
-    if (i < warp) before += sums[i];
-    total += sums[i];
-  }
-  total *= heads;
-  const int each = max(kLeastShare, (total + p.ctas - 1) / p.ctas);
+  const int w = me < rest ? sorted[(whole + me) / heads] : 0;
+  int rest_steps, whole_steps, all_room;
+  const int from = block_before(w, sums, rest_steps);
+  block_before(mine, sums, whole_steps);
+  const int each = (rest_steps + whole_steps + ctas - 1) / ctas;
   const bool share = busiest > each + kShareCost;
-  if (threadIdx.x == 0) {
-    p.header[1] = share ? each : 0;
-    p.header[2] = total;
-  }
-  if (share && w > 0) {
-    const int from = before * heads, to = from + w * heads;
-    p.list[threadIdx.x].w = before;
-    for (int c = (from + each - 1) / each; c * each < to; ++c)
-      p.begin[c] = make_int4(threadIdx.x, (c * each - from) / w, (c * each - from) % w, 0);
+  if (me == 0) p.header[1] = share ? 1 : 0;
+  if (!share) return;
+  // CTA `me` has room for so many steps of the rest (rooms under kLeastShare are left out:
+  // the others' are larger by that)
+  int room = me < ctas ? max(0, each + kLeastShare - mine) : 0;
+  if (room < kLeastShare) room = 0;
+  const int at = block_before(room, sums, all_room);
+  if (me < rest) item_from[me] = from;
+  __syncthreads();
+  if (me < ctas) {
+    int lo = 0, hi = rest - 1;                             // the last item that begins at or before `at`
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (item_from[mid] <= at) lo = mid; else hi = mid - 1;
+    }
+    p.begin[me] = make_int4(whole + lo, at - item_from[lo], max(0, min(room, rest_steps - at)), 0);
   }
 }
 
-// The items that shares have cut: block (x, y) has 8 rows of the item that share x ends but
-// does not begin, a warp each:  out = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).
+// The items that shares have cut: block (c, y) has 8 rows of the item that CTA c ends but does
+// not begin, a warp each:  out = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).
 constexpr int kJoinWarps = 8;
 template <int CPL>
 __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const PrefillParams p) {
   constexpr int D = CPL * 32;
   wait_prior_grids();
   allow_next_grid();
-  const int share = p.header[1], total = p.header[2], c = blockIdx.x;
-  if (share == 0 || c * share >= total) return;
-  const int4 at = p.begin[c], entry = p.list[at.x];
-  if (at.z == 0 || entry.z - at.z > min(share, total - c * share)) return;   // nothing cut before, or it goes on
+  if (p.header[1] == 0) return;
+  const int c = blockIdx.x;
+  const int4 at = p.begin[c];
+  if (at.z == 0 || at.y == 0) return;                      // no share, or it begins with an item
+  const int4 entry = p.tiles[at.x / p.num_kv_heads];
+  if (entry.z - at.y > at.z) return;                       // the item goes on
+  const int h = at.x % p.num_kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = blockIdx.y * kJoinWarps + warp;
   const int tile_tokens = kPrefillRows >> p.group_log2;
   const PrefillTile t = prefill_tile<kPrefillKeys>(p, prefill_seq(p, entry.x), entry.y, tile_tokens);
   if ((r >> p.group_log2) >= t.tokens) return;
-  const int from = (entry.w * p.num_kv_heads) + at.y * entry.z;              // where the item begins
-  const int c1 = from / share;
-  // a share's first item is its slot 2 c, any other that it leaves unfinished 2 c + 1
-  const int first = 2 * c1 + (from == c1 * share ? 0 : 1);
   float M = -3.0e38f, S = 0.f, acc[CPL] = {};
-  for (int i = c1; i <= c; ++i) {
-    const int64_t row = static_cast<int64_t>(i == c1 ? first : 2 * i) * p.slot_rows + r;
-    const float lse = p.part_lse[row];
-    float v[CPL];
+  // partials of up to 32 CTAs at a time, c itself and those before it
+  for (int back = c; back >= 0; back -= 32) {
+    const int cc = back - lane;
+    int4 b = make_int4(-1, 0, 0, 0);
+    if (cc >= 0) b = p.begin[cc];
+    const bool has = b.z > 0, same = b.x == at.x;
+    // (a share that begins with another item has this one as its last)
+    const uint32_t ends = __ballot_sync(0xffffffffu, has && (!same || b.y == 0));
+    const int n = ends ? __ffs(ends) : 32;
+    const bool in = has && lane < n;
+    const int64_t row = static_cast<int64_t>(2 * cc + (same ? 0 : 1)) * p.slot_rows + r;
+    const float lse = in ? p.part_lse[row] : -INFINITY;
+    float mx = lse;
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) v[k] = p.part_out[row * D + lane * CPL + k];
-    const float mn = fmaxf(M, lse), keep = fast_exp2(M - mn), w = fast_exp2(lse - mn);
+    for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float mn = fmaxf(M, mx), keep = fast_exp2(M - mn), f = in ? fast_exp2(lse - mn) : 0.f;
+    float sum = f;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     M = mn;
-    S = fmaf(S, keep, w);
+    S = fmaf(S, keep, sum);
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) acc[k] = fmaf(acc[k], keep, w * v[k]);
+    for (int k = 0; k < CPL; ++k) acc[k] *= keep;
+    uint32_t todo = __ballot_sync(0xffffffffu, in);
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      if (!((todo >> j) & 1u)) continue;
+      const int64_t rj = __shfl_sync(0xffffffffu, row, j);
+      const float fj = __shfl_sync(0xffffffffu, f, j);
+      float v[CPL];
+      load_cols<CPL>(p.part_out + rj * D + lane * CPL, v);
+#pragma unroll
+      for (int k = 0; k < CPL; ++k) acc[k] = fmaf(fj, v[k], acc[k]);
+    }
+    if (ends) break;
   }
   const float inv = S > 0.f || S != S ? 1.f / S : 0.f;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
-      ((static_cast<int64_t>(t.row0) + (r >> p.group_log2)) * p.num_q_heads + at.y * p.group + (r & (p.group - 1))) * D + lane * CPL);
+      ((static_cast<int64_t>(t.row0) + (r >> p.group_log2)) * p.num_q_heads + h * p.group + (r & (p.group - 1))) * D + lane * CPL);
 #pragma unroll
   for (int k = 0; k < CPL / 2; ++k) {
     const __nv_bfloat162 b2 = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
@@ -194,15 +256,15 @@ int64_t most_tiles(int64_t num_tokens, int64_t num_seqs, int group, int tile_row
 // Offsets of a call's scratch: header, list (room for the smaller tile: enough for every
 // type), each CTA's start, the partial results of shares.
 struct Scratch {
-  size_t list, begin, lse, out, total;
+  size_t tiles, begin, lse, out, total;
   int slot_rows;
 };
 Scratch scratch(int64_t num_tokens, int64_t num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int ctas) {
   const int group = num_q_heads / num_kv_heads;
   Scratch s;
   s.slot_rows = static_cast<int>(std::min<int64_t>(kPrefillRows, num_tokens * group));
-  s.list = 256;
-  s.begin = s.list + align256(16 * static_cast<size_t>(most_tiles(num_tokens, num_seqs, group, kPrefillRowsF32)));
+  s.tiles = 256;
+  s.begin = s.tiles + align256(16 * static_cast<size_t>(most_tiles(num_tokens, num_seqs, group, kPrefillRowsF32)));
   s.lse = s.begin + align256(16 * static_cast<size_t>(ctas));
   s.out = s.lse + align256(2 * static_cast<size_t>(ctas) * s.slot_rows * 4);
   s.total = s.out + 2 * static_cast<size_t>(ctas) * s.slot_rows * head_dim * 4;
@@ -230,7 +292,7 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   char* ws = static_cast<char*>(a.workspace);
   p.header = reinterpret_cast<int32_t*>(ws);
   const Scratch at = scratch(a.num_tokens, a.num_seqs, a.num_q_heads, a.num_kv_heads, D, a.num_sms);
-  p.list = reinterpret_cast<int4*>(ws + at.list);
+  p.tiles = reinterpret_cast<int4*>(ws + at.tiles);
   p.begin = reinterpret_cast<int4*>(ws + at.begin);
   p.part_lse = reinterpret_cast<float*>(ws + at.lse);
   p.part_out = reinterpret_cast<float*>(ws + at.out);
@@ -238,7 +300,8 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   p.ctas = a.num_sms;
   // (cut items only where the sequences may have items too few and long enough for it)
   const int64_t least_items = static_cast<int64_t>(a.num_tokens) * group / kPrefillRows * a.num_kv_heads;
-  p.may_share = !a.f32 && a.max_len > kLeastShare * kPrefillKeys && a.max_len <= kMostShared && least_items < static_cast<int64_t>(kWholeRounds) * a.num_sms;
+  p.may_share = !a.f32 && a.max_len > kLeastShare * kPrefillKeys && a.max_len <= kMostShared && least_items <= static_cast<int64_t>(kMostRounds) * a.num_sms &&
+                a.num_sms * kMostRounds <= kPlanTiles;
   p.room = static_cast<int>(most_tiles(a.num_tokens, a.num_seqs, group, a.f32 ? kPrefillRowsF32 : kPrefillRows));
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.num_seqs = a.num_seqs;
