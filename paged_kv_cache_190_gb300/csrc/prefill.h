@@ -8,6 +8,10 @@
 #include <cstddef>
 #include <cstdint>
 
+#ifdef __CUDACC__
+#include "pa_device.cuh"
+#endif
+
 namespace pa {
 
 constexpr int kPrefillKeys = 128;                 // keys of a step
@@ -30,6 +34,7 @@ struct PrefillParams {
   int room;                                       // entries that it has room for
   int4* begin;                                    // shares: {item, its first step, steps} of each CTA
   int may_share, ctas;                            // the host's leave to cut items; CTAs
+  int direct;                                     // no plan: CTA i takes item i
   float* part_out;                                // shares: [2 ctas][slot_rows][head_dim]
   float* part_lse;                                // shares: [2 ctas][slot_rows]
   int slot_rows;
@@ -122,12 +127,56 @@ struct PrefillWalk {
   int tile_tokens, items, k, rounds, left;        // left: steps of the share, -1: not begun
   int e;
   __device__ __forceinline__ PrefillWalk(const PrefillParams& p_, int tile_tokens_) : p(p_), tile_tokens(tile_tokens_) {
-    items = p.header[0] * p.num_kv_heads;
     k = e = 0;
+    if (p.direct) {
+      items = left = rounds = 0;
+      return;
+    }
+    items = p.header[0] * p.num_kv_heads;
     left = p.header[1] ? -1 : 0;
     rounds = left ? items / static_cast<int>(gridDim.x) : 1 << 30;
   }
+  // The CTA's only item, found by each warp from the sequences' starts.
+  __device__ __forceinline__ bool own(PrefillItem& it) {
+    if (k++ > 0) return false;
+    const int lane = threadIdx.x & 31, tile = blockIdx.x / p.num_kv_heads;
+    int before = 0;
+    for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
+      PrefillSeq s{0, 0, 0};
+      if (b0 + lane < p.num_seqs) {
+        const int a = p.starts[b0 + lane], e2 = p.starts[b0 + lane + 1], len = p.lens[b0 + lane];
+        s = prefill_seq(p, a, e2, len);
+        if (blockIdx.x == 0 && threadIdx.x < 32 && (a < 0 || e2 < a || e2 > p.num_tokens || len < 0 || len > p.max_len || s.n > s.len))
+          report(p.device_errors, PA_DEVERR_BAD_LENGTH);
+      }
+      const int nt = (s.n + tile_tokens - 1) / tile_tokens;
+      int x = nt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const uint32_t mine = __ballot_sync(0xffffffffu, before + x > tile);
+      if (mine) {
+        const int l = __ffs(mine) - 1;
+        s.q0 = __shfl_sync(0xffffffffu, s.q0, l);
+        s.n = __shfl_sync(0xffffffffu, s.n, l);
+        s.len = __shfl_sync(0xffffffffu, s.len, l);
+        const int t = tile - before - __shfl_sync(0xffffffffu, x - nt, l);
+        it.b = b0 + l;
+        it.h = blockIdx.x % p.num_kv_heads;
+        it.slot = -1;
+        it.t = prefill_tile<KEYS>(p, s, t, tile_tokens);
+        it.v0 = 0;
+        it.v1 = max(1, it.t.steps);
+        return true;
+      }
+      before += __shfl_sync(0xffffffffu, x, 31);
+    }
+    return false;
+  }
   __device__ __forceinline__ bool next(PrefillItem& it) {
+    if (p.direct) return own(it);
     int i, n;
     it.slot = -1;
     it.v0 = 0;

@@ -14,7 +14,6 @@
 namespace pa {
 namespace {
 
-constexpr int kPlanThreads = 1024;
 constexpr int kPlanBuckets = 256;
 constexpr int kPlanSeqs = 1024, kPlanTiles = 1536;          // kept in shared memory
 
@@ -30,6 +29,7 @@ __device__ __forceinline__ void load_cols(const float* p, float* v) {
 }
 
 // Exclusive sum of a block's values; `all` is their sum in every thread.
+template <int THREADS>
 __device__ __forceinline__ int block_before(int x, int* sums, int& all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int y = x;
@@ -44,7 +44,7 @@ __device__ __forceinline__ int block_before(int x, int* sums, int& all) {
   int before = y - x;
   all = 0;
 #pragma unroll
-  for (int i = 0; i < kPlanThreads / 32; ++i) {
+  for (int i = 0; i < THREADS / 32; ++i) {
     if (i < warp) before += sums[i];
     all += sums[i];
   }
@@ -65,10 +65,10 @@ constexpr int kShareCost = 12;
 constexpr int kMostRounds = 8;                             // (at most kPlanTiles tiles then)
 constexpr int kMostShared = 1 << 27;                       // keys: steps of all items within 31 bits
 constexpr int kLeastShare = 4;                             // steps: less is not worth a partial
-template <int KEYS>
-__global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const PrefillParams p, int tile_rows) {
-  __shared__ int most, count[kPlanBuckets], next[kPlanBuckets], sums[kPlanThreads / 32], busiest;
-  __shared__ int item_from[kPlanThreads];
+template <int KEYS, int THREADS>
+__global__ void __launch_bounds__(THREADS) prefill_plan_kernel(const PrefillParams p, int tile_rows) {
+  __shared__ int most, count[kPlanBuckets], next[kPlanBuckets], sums[THREADS / 32], busiest;
+  __shared__ int item_from[THREADS];
   __shared__ PrefillSeq seqs[kPlanSeqs];
   __shared__ int2 unsorted[kPlanTiles];
   __shared__ int sorted[kPlanTiles];                       // steps
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
   __syncthreads();
   bool bad = false;
   int longest = 1;
-  for (int b = me; b < p.num_seqs; b += kPlanThreads) {
+  for (int b = me; b < p.num_seqs; b += THREADS) {
     const int a = p.starts[b], e = p.starts[b + 1], len = p.lens[b];
     const PrefillSeq s = prefill_seq(p, a, e, len);
     if (b < kPlanSeqs) seqs[b] = s;
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
   const float buckets = static_cast<float>(kPlanBuckets - 1) / static_cast<float>(most);
   auto bucket = [&](int steps) { return kPlanBuckets - 1 - min(kPlanBuckets - 1, static_cast<int>(static_cast<float>(steps) * buckets)); };
   auto tiles_do = [&](auto f) {                            // f(sequence, tile, steps) for all tiles
-    for (int b = warp; b < p.num_seqs; b += kPlanThreads / 32) {
+    for (int b = warp; b < p.num_seqs; b += THREADS / 32) {
       const PrefillSeq s = b < kPlanSeqs ? seqs[b] : prefill_seq(p, b);
       for (int t = lane; t * tokens < s.n; t += 32) f(b, t, prefill_tile<KEYS>(p, s, t, tokens).steps);
     }
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
   tiles_do([&](int, int, int steps) { atomicAdd(&count[bucket(steps)], 1); });
   __syncthreads();
   int all;
-  const int before = block_before(me < kPlanBuckets ? count[me] : 0, sums, all);   // where each bucket begins
+  const int before = block_before<THREADS>(me < kPlanBuckets ? count[me] : 0, sums, all);   // where each bucket begins
   if (me < kPlanBuckets) next[me] = before;
   const int tiles = min(all, p.room);                      // (room enough but for q_starts that decrease)
   if (me == 0) p.header[0] = tiles;
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
   // (which of the tiles of a bucket came first is chance, and shares cut items by their place:
   // in the order of their numbers, so that a call's result is always the same)
   if (here)
-    for (int i = me; i < all; i += kPlanThreads) {
+    for (int i = me; i < all; i += THREADS) {
       const int2 x = unsorted[i];
       const PrefillSeq s = x.x < kPlanSeqs ? seqs[x.x] : prefill_seq(p, x.x);
       const int steps = prefill_tile<KEYS>(p, s, x.y, tokens).steps;
@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
   }
   const int w = me < rest ? sorted[(whole + me) / heads] : 0;
   int rest_steps, whole_steps, all_room;
-  const int from = block_before(w, sums, rest_steps);
-  block_before(mine, sums, whole_steps);
+  const int from = block_before<THREADS>(w, sums, rest_steps);
+  block_before<THREADS>(mine, sums, whole_steps);
   const int each = (rest_steps + whole_steps + ctas - 1) / ctas;
   const bool share = busiest > each + kShareCost;
   if (me == 0) p.header[1] = share ? 1 : 0;
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
   // the others' are larger by that)
   int room = me < ctas ? max(0, each + kLeastShare - mine) : 0;
   if (room < kLeastShare) room = 0;
-  const int at = block_before(room, sums, all_room);
+  const int at = block_before<THREADS>(room, sums, all_room);
   if (me < rest) item_from[me] = from;
   __syncthreads();
   if (me < ctas) {
@@ -179,9 +179,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Prefil
   }
 }
 
-// The items that shares have cut: block (c, y) has 8 rows of the item that CTA c ends but does
-// not begin, a warp each:  out = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).
-constexpr int kJoinWarps = 8;
+// The items that shares have cut: block (c, y) has 16 rows of the item that CTA c ends but does
+// not begin, one after another a warp:  out = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M).
+constexpr int kJoinWarps = 8, kJoinRows = 16;
 template <int CPL>
 __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const PrefillParams p) {
   constexpr int D = CPL * 32;
@@ -195,54 +195,55 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Pre
   if (entry.z - at.y > at.z) return;                       // the item goes on
   const int h = at.x % p.num_kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.y * kJoinWarps + warp;
   const int tile_tokens = kPrefillRows >> p.group_log2;
   const PrefillTile t = prefill_tile<kPrefillKeys>(p, prefill_seq(p, entry.x), entry.y, tile_tokens);
-  if ((r >> p.group_log2) >= t.tokens) return;
-  float M = -3.0e38f, S = 0.f, acc[CPL] = {};
-  // partials of up to 32 CTAs at a time, c itself and those before it
-  for (int back = c; back >= 0; back -= 32) {
-    const int cc = back - lane;
-    int4 b = make_int4(-1, 0, 0, 0);
-    if (cc >= 0) b = p.begin[cc];
-    const bool has = b.z > 0, same = b.x == at.x;
-    // (a share that begins with another item has this one as its last)
-    const uint32_t ends = __ballot_sync(0xffffffffu, has && (!same || b.y == 0));
-    const int n = ends ? __ffs(ends) : 32;
-    const bool in = has && lane < n;
-    const int64_t row = static_cast<int64_t>(2 * cc + (same ? 0 : 1)) * p.slot_rows + r;
-    const float lse = in ? p.part_lse[row] : -INFINITY;
-    float mx = lse;
+  for (int r = blockIdx.y * kJoinRows + warp; r < (blockIdx.y + 1) * kJoinRows; r += kJoinWarps) {
+    if ((r >> p.group_log2) >= t.tokens) return;
+    float M = -3.0e38f, S = 0.f, acc[CPL] = {};
+    // partials of up to 32 CTAs at a time, c itself and those before it
+    for (int back = c; back >= 0; back -= 32) {
+      const int cc = back - lane;
+      int4 b = make_int4(-1, 0, 0, 0);
+      if (cc >= 0) b = p.begin[cc];
+      const bool has = b.z > 0, same = b.x == at.x;
+      // (a share that begins with another item has this one as its last)
+      const uint32_t ends = __ballot_sync(0xffffffffu, has && (!same || b.y == 0));
+      const int n = ends ? __ffs(ends) : 32;
+      const bool in = has && lane < n;
+      const int64_t row = static_cast<int64_t>(2 * cc + (same ? 0 : 1)) * p.slot_rows + r;
+      const float lse = in ? p.part_lse[row] : -INFINITY;
+      float mx = lse;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float mn = fmaxf(M, mx), keep = fast_exp2(M - mn), f = in ? fast_exp2(lse - mn) : 0.f;
-    float sum = f;
+      for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float mn = fmaxf(M, mx), keep = fast_exp2(M - mn), f = in ? fast_exp2(lse - mn) : 0.f;
+      float sum = f;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    M = mn;
-    S = fmaf(S, keep, sum);
+      for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      M = mn;
+      S = fmaf(S, keep, sum);
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) acc[k] *= keep;
-    uint32_t todo = __ballot_sync(0xffffffffu, in);
+      for (int k = 0; k < CPL; ++k) acc[k] *= keep;
+      uint32_t todo = __ballot_sync(0xffffffffu, in);
 #pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      if (!((todo >> j) & 1u)) continue;
-      const int64_t rj = __shfl_sync(0xffffffffu, row, j);
-      const float fj = __shfl_sync(0xffffffffu, f, j);
-      float v[CPL];
-      load_cols<CPL>(p.part_out + rj * D + lane * CPL, v);
+      for (int j = 0; j < n; ++j) {
+        if (!((todo >> j) & 1u)) continue;
+        const int64_t rj = __shfl_sync(0xffffffffu, row, j);
+        const float fj = __shfl_sync(0xffffffffu, f, j);
+        float v[CPL];
+        load_cols<CPL>(p.part_out + rj * D + lane * CPL, v);
 #pragma unroll
-      for (int k = 0; k < CPL; ++k) acc[k] = fmaf(fj, v[k], acc[k]);
+        for (int k = 0; k < CPL; ++k) acc[k] = fmaf(fj, v[k], acc[k]);
+      }
+      if (ends) break;
     }
-    if (ends) break;
-  }
-  const float inv = S > 0.f || S != S ? 1.f / S : 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
-      ((static_cast<int64_t>(t.row0) + (r >> p.group_log2)) * p.num_q_heads + h * p.group + (r & (p.group - 1))) * D + lane * CPL);
+    const float inv = S > 0.f || S != S ? 1.f / S : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
+        ((static_cast<int64_t>(t.row0) + (r >> p.group_log2)) * p.num_q_heads + h * p.group + (r & (p.group - 1))) * D + lane * CPL);
 #pragma unroll
-  for (int k = 0; k < CPL / 2; ++k) {
-    const __nv_bfloat162 b2 = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-    dst[k] = *reinterpret_cast<const uint32_t*>(&b2);
+    for (int k = 0; k < CPL / 2; ++k) {
+      const __nv_bfloat162 b2 = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+      dst[k] = *reinterpret_cast<const uint32_t*>(&b2);
+    }
   }
 }
 
@@ -338,22 +339,30 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   }
   const int rows = a.f32 ? kPrefillRowsF32 : kPrefillRows;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kPlanThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = a.f32 ? cudaLaunchKernelEx(&cfg, prefill_plan_kernel<kPrefillKeysF32>, p, rows)
-                              : cudaLaunchKernelEx(&cfg, prefill_plan_kernel<kPrefillKeys>, p, rows);
-  if (e != cudaSuccess) return e;
   const int64_t items = most_tiles(a.num_tokens, a.num_seqs, group, rows) * a.num_kv_heads;
+  // one item a CTA at most, and none long enough to be cut: each CTA finds its own, without
+  // a plan (37 tokens of one prompt: kDirectMeasured)
+  p.direct = !p.may_share && items <= a.num_sms;
+  cudaError_t e = cudaSuccess;
+  if (!p.direct) {
+    const bool small = a.num_seqs <= 256 && most_tiles(a.num_tokens, a.num_seqs, group, rows) <= 1024 && a.num_sms <= 256;
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(small ? 256 : 1024);
+    auto plan = a.f32 ? (small ? prefill_plan_kernel<kPrefillKeysF32, 256> : prefill_plan_kernel<kPrefillKeysF32, 1024>)
+                      : (small ? prefill_plan_kernel<kPrefillKeys, 256> : prefill_plan_kernel<kPrefillKeys, 1024>);
+    e = cudaLaunchKernelEx(&cfg, plan, p, rows);
+    if (e != cudaSuccess) return e;
+  }
   if (a.f32) return run_prefill_f32(D, p, static_cast<int>(std::min<int64_t>(items, 2 * a.num_sms)), stream);
   e = run_prefill_bf16(D, p, p.may_share ? a.num_sms : static_cast<int>(std::min<int64_t>(items, a.num_sms)), stream);
   if (e != cudaSuccess || !p.may_share) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.num_sms), static_cast<unsigned>((at.slot_rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.gridDim = dim3(static_cast<unsigned>(a.num_sms), static_cast<unsigned>((at.slot_rows + kJoinRows - 1) / kJoinRows));
   cfg.blockDim = dim3(kJoinWarps * 32);
   return D == 128 ? cudaLaunchKernelEx(&cfg, prefill_join_kernel<4>, p) : cudaLaunchKernelEx(&cfg, prefill_join_kernel<2>, p);
 }
