@@ -37,10 +37,8 @@ __device__ __forceinline__ float scale4_value(uint32_t byte) {
 // x / s, correctly rounded, from r = 1 / s correctly rounded: the product with r, corrected
 // by its exact remainder (P. Markstein, "Computation of elementary functions on the IBM
 // RISC System/6000 processor", 1990).  A product alone would take some of the many bf16
-// elements that lie on the border of two codes to the wrong one.  |x| <= 8 s: beyond that a
-// code saturates, and an infinity has no remainder.
+// elements that lie on the border of two codes to the wrong one.
 __device__ __forceinline__ float quotient4(float x, float s, float r) {
-  x = fminf(fmaxf(x, -8.f * s), 8.f * s);
   const float z = __fmul_rn(x, r);
   return __fmaf_rn(__fmaf_rn(-z, s, x), r, z);
 }
@@ -48,9 +46,12 @@ __device__ __forceinline__ float quotient4(float x, float s, float r) {
 // Eight floats over s as codes: nearest, ties to even, magnitudes above 6 s saturate.
 __device__ __forceinline__ uint32_t codes4_of(const float* x, float s) {
   const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+  // (beyond 8 s a code saturates, and an infinity has no remainder: only the largest scale
+  // has such elements)
+  const bool over = s == kMostScale4;
   float z[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] = quotient4(x[i], s, r);
+  for (int i = 0; i < 8; ++i) z[i] = quotient4(over ? fminf(fmaxf(x[i], -8.f * s), 8.f * s) : x[i], s, r);
   uint32_t w;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"

@@ -315,8 +315,8 @@ __device__ __forceinline__ void rows_of_token(const RopeArgs& a, int t, Kind kin
   }
 }
 
-// A group of D / (2 N) lanes takes HPT heads of one token and kind.
-template <typename E, int D, bool INTER, Held HELD, int HPT>
+// A group of D / (2 N) lanes takes HPT heads of one token and kind, of K and V KVH.
+template <typename E, int D, bool INTER, Held HELD, int HPT, int KVH>
 __global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const RopeArgs a, unsigned groups,
                                                                   int uq, int uk) {
   wait_prior_grids();
@@ -330,9 +330,9 @@ __global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const RopeArgs
   if (u < uq)
     rows_of_token<E, D, INTER, HELD, HPT>(a, t, kQ, u * HPT, l);
   else if (u < uq + uk)
-    rows_of_token<E, D, INTER, HELD, HPT>(a, t, kK, (u - uq) * HPT, l);
+    rows_of_token<E, D, INTER, HELD, KVH>(a, t, kK, (u - uq) * KVH, l);
   else
-    rows_of_token<E, D, INTER, HELD, HPT>(a, t, kV, (u - uq - uk) * HPT, l);
+    rows_of_token<E, D, INTER, HELD, KVH>(a, t, kV, (u - uq - uk) * KVH, l);
 }
 
 // ------------------------------------------------ a scale for each page and head
@@ -822,8 +822,8 @@ constexpr int64_t kMostGroups = int64_t{1} << 31;
 template <typename E, int D, Held HELD>
 cudaError_t run_rope(const RopeArgs& a, cudaStream_t stream) {
   constexpr int per_block = kThreads / (D / Vec<E>::N / 2);
-  auto go = [&](auto kernel, int hpt) {
-    const int uq = ceil_div(a.num_q_heads, hpt), uk = ceil_div(a.num_kv_heads, hpt);
+  auto go = [&](auto kernel, int hpt, int kvh) {
+    const int uq = ceil_div(a.num_q_heads, hpt), uk = ceil_div(a.num_kv_heads, kvh);
     const int64_t groups = static_cast<int64_t>(a.num_tokens) * (uq + 2 * uk);
     if (groups >= kMostGroups) return cudaErrorInvalidValue;
     return launch(kernel, (groups + per_block - 1) / per_block, kThreads, 0, stream, a, groups, uq, uk);
@@ -831,9 +831,10 @@ cudaError_t run_rope(const RopeArgs& a, cudaStream_t stream) {
   // one head a thread while the rows are too few to fill the GPU
   const bool few = static_cast<int64_t>(a.num_tokens) * (a.num_q_heads + 2 * a.num_kv_heads) < 8192;
   constexpr int H = kHeadsAtOnce;
+  constexpr int KV = HELD == Held::kE2m1 ? 1 : H;
   if (a.interleaved)
-    return few ? go(rope_and_cache_kernel<E, D, true, HELD, 1>, 1) : go(rope_and_cache_kernel<E, D, true, HELD, H>, H);
-  return few ? go(rope_and_cache_kernel<E, D, false, HELD, 1>, 1) : go(rope_and_cache_kernel<E, D, false, HELD, H>, H);
+    return few ? go(rope_and_cache_kernel<E, D, true, HELD, 1, 1>, 1, 1) : go(rope_and_cache_kernel<E, D, true, HELD, H, KV>, H, KV);
+  return few ? go(rope_and_cache_kernel<E, D, false, HELD, 1, 1>, 1, 1) : go(rope_and_cache_kernel<E, D, false, HELD, H, KV>, H, KV);
 }
 
 }  // namespace
