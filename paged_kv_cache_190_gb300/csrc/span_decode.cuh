@@ -485,15 +485,35 @@ struct Fp8Rows {
   }
 };
 
+// Loads of shared memory at a constant offset from an address.
+__device__ __forceinline__ uint2 lds64(uint32_t a, int off) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a + off));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a, int off) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a + off));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
 // 4-bit rows (fp4.cuh): a code times its scale is exact as a half, so K and V become halves
 // on the way into mma.sync m16n8k16, two a conversion, and one product of two of them
 // brings the scale in; q and the weights as for e4m3 (the scales differ within a row, so
 // they cannot go into the weights; nor need they, for a half holds the values).
 //   * A row of 72 bytes is loaded as it stands, 8 bytes of 16 columns a time: piece p of
 //     rows 4 c + i of 16 tokens falls on banks 8 c + 2 p, a half-warp's on all 32.
-//   * Scores: a lane has pieces c and c + 4 of its token's row; q's columns go with them.
-//   * Column 2 j of a score tile is token 4 c + 2 (tile & 1) of its 16 and column 2 j + 1 the
-//     next, so that a lane's weights are those of 4 tokens in a row.
+//   * Scores: a lane has pieces c and c + 4 of its tokens' rows; q's columns go with them.
+//   * S^T = K q^T, with the tokens as rows (half the products of Q K^T, which would leave half
+//     of its 16 rows empty); movmatrix turns a tile of weights into P^T's fragment.  Tokens 2 j
+//     and 2 j + 1 of a tile of 8 are tokens 4 j and 4 j + 1 of their 16 (of the second tile
+//     4 j + 2 and 4 j + 3), so that a lane's weights are those of 4 tokens in a row.
 //   * Values: lane (g, c) has piece g of those 4 tokens.  The codes of a column of two
 //     tokens are put into one byte (two shifts and two selections for 16 codes), which one
 //     conversion makes the pair of halves that the product wants; the columns 16 g + 2 t
@@ -504,14 +524,15 @@ struct Fp4Rows {
   static constexpr float kPLog2 = 10.f;      // weights are carried times 2^10
   uint32_t qa[KS][2];
   float o[MT][4];
-  float m, l, qinv;
-  int lane, rows;
+  float m[2], l[2], qinv[2];                  // of rows 2 (lane & 3) and the next
+  int lane, rows, later;                     // later: new tokens between the two
 
   __device__ __forceinline__ void init(const SpanParams& p, int lane_, float*, float*) {
     lane = lane_;
     rows = p.rows;
+    later = p.group == 1 ? 1 : 0;
   }
-  __device__ __forceinline__ int row() const { return lane >> 2; }
+  __device__ __forceinline__ int row() const { return 2 * (lane & 3); }
 
   __device__ __forceinline__ void load(const SpanParams& p, int b, int head) {
     const int g = lane >> 2, c = lane & 3;
@@ -526,9 +547,11 @@ struct Fp4Rows {
     }
   }
   __device__ __forceinline__ void begin(const SpanParams&) {
-    qinv = halves_of_q<KS>(qa);
-    m = kNoScore;
-    l = 0.f;
+    const float back = halves_of_q<KS>(qa);                 // of row lane / 4
+    qinv[0] = __shfl_sync(kFull, back, 8 * (lane & 3));
+    qinv[1] = __shfl_sync(kFull, back, 8 * (lane & 3) + 4);
+    m[0] = m[1] = kNoScore;
+    l[0] = l[1] = 0.f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
   }
@@ -538,86 +561,97 @@ struct Fp4Rows {
   __device__ __forceinline__ void unit(uint32_t kb, uint32_t vb, int, int half, const Sight& see,
                                        float scale_log2, const float2*, int, Release release) {
     const int g = lane >> 2, c = lane & 3;
-    const char* kt = static_cast<const char*>(__cvta_shared_to_generic(kb)) + (4 * (g >> 1) + (g & 1)) * kRow4Bytes;
-    const char* vt = static_cast<const char*>(__cvta_shared_to_generic(vb)) + 4 * c * kRow4Bytes;
-    float sh[NT][4];
+    const uint32_t kt = kb + (4 * (g >> 1) + (g & 1)) * kRow4Bytes;
+    const uint32_t vt = vb + 4 * c * kRow4Bytes;
+    const uint32_t kp = kt + 8 * c, ks = kt + kRow4Codes + c, vp = vt + 8 * g, vq = vt + kRow4Codes + g;
+    float sh[2][4];                                         // [16 tokens]: (token, row) as in O^T
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      sh[n][0] = sh[n][1] = sh[n][2] = sh[n][3] = 0.f;
-      const char* row = kt + (n >> 1) * half + 2 * (n & 1) * kRow4Bytes;
+    for (int hf = 0; hf < 2; ++hf) {
+      sh[hf][0] = sh[hf][1] = sh[hf][2] = sh[hf][3] = 0.f;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const uint2 w = *reinterpret_cast<const uint2*>(row + 8 * c + 32 * k);
-        const uint32_t s = *reinterpret_cast<const unsigned char*>(row + kRow4Codes + c + 4 * k) * 0x00800080u;
-        uint32_t b[8];
-        halves4_of(w.x, b[0], b[1], b[2], b[3]);
-        halves4_of(w.y, b[4], b[5], b[6], b[7]);
+        uint32_t b[2][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = mul_half2(b[i], s);
+        for (int n = 0; n < 2; ++n) {
+          const uint2 w = lds64(kp + hf * half, 2 * n * kRow4Bytes + 32 * k);
+          const uint32_t s = lds8(ks + hf * half, 2 * n * kRow4Bytes + 4 * k) * 0x00800080u;
+          halves4_of(w.x, b[n][0], b[n][1], b[n][2], b[n][3]);
+          halves4_of(w.y, b[n][4], b[n][5], b[n][6], b[n][7]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mma_f16(sh[n], qa[4 * k + i][0], 0u, qa[4 * k + i][1], 0u, b[2 * i], b[2 * i + 1]);
+          for (int i = 0; i < 8; ++i) b[n][i] = mul_half2(b[n][i], s);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mma_f16(sh[hf], b[0][2 * i], b[1][2 * i], b[0][2 * i + 1], b[1][2 * i + 1], qa[4 * k + i][0], qa[4 * k + i][1]);
       }
     }
-    // V's codes come in while the scores are worked on
-    uint2 vw[2][4];
-    uint32_t vs[2][4];
+    const float qs[2] = {qinv[0] * scale_log2, qinv[1] * scale_log2};
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const char* row = vt + hf * half + i * kRow4Bytes;
-        vw[hf][i] = *reinterpret_cast<const uint2*>(row + 8 * g);
-        vs[hf][i] = *reinterpret_cast<const unsigned char*>(row + kRow4Codes + g);
-      }
-    release();
-    const float qs = qinv * scale_log2;
-    float sv[2 * NT];
+      for (int e = 0; e < 4; ++e) sh[hf][e] *= qs[e & 1];
+    if (!see.all) {
+      Sight next = see;
+      next.last += later;
+      next.first += later;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!((e & 1) ? next : see).sees(16 * hf + 4 * (g >> 1) + (g & 1) + (e & 2))) sh[hf][e] = -INFINITY;
+    }
+    float alpha[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float mx = fmaxf(fmaxf(sh[0][h], sh[0][2 + h]), fmaxf(sh[1][h], sh[1][2 + h]));
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+      const float mn = fmaxf(m[h], mx);
+      alpha[h] = fast_exp2(m[h] - mn);
+      m[h] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          sh[hf][e + h] = fast_exp2(sh[hf][e + h] - mn);
+          sum += sh[hf][e + h];
+        }
+      l[h] = l[h] * alpha[h] + sum;
+    }
+    // the rows' weights of a token, turned into the tokens' of a row: P^T's fragment
+    uint32_t pb[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) sv[2 * n + e] = sh[n][e] * qs;
-    if (!see.all) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (!see.sees(16 * (n >> 1) + 4 * c + 2 * (n & 1) + e)) sv[2 * n + e] = -INFINITY;
-    }
-    float mx = fmaxf(fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3])), fmaxf(fmaxf(sv[4], sv[5]), fmaxf(sv[6], sv[7])));
-    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-    const float mn = fmaxf(m, mx);
-    const float alpha = fast_exp2(m - mn);
-    m = mn;
-    uint32_t pb[NT];
-    float psum = 0.f;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float p0 = fast_exp2(sv[2 * n] - mn), p1 = fast_exp2(sv[2 * n + 1] - mn);
-      psum += p0 + p1;
-      pb[n] = pack_half2(p0 * 1024.f, p1 * 1024.f);
-    }
-    l = l * alpha + psum;
-    if (__any_sync(kFull, alpha != 1.f)) {
-      const float a_even = __shfl_sync(kFull, alpha, 8 * c), a_odd = __shfl_sync(kFull, alpha, 8 * c + 4);
+      pb[n] = transpose8x8(pack_half2(sh[n >> 1][2 * (n & 1)] * 1024.f, sh[n >> 1][2 * (n & 1) + 1] * 1024.f));
+    if (__any_sync(kFull, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        o[mt][0] *= a_even;
-        o[mt][1] *= a_odd;
-        o[mt][2] *= a_even;
-        o[mt][3] *= a_odd;
+        o[mt][0] *= alpha[0];
+        o[mt][1] *= alpha[1];
+        o[mt][2] *= alpha[0];
+        o[mt][3] *= alpha[1];
       }
     }
     constexpr uint32_t kLow = 0x0f0f0f0fu;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      const uint32_t s01 = (vs[hf][0] << 7) + vs[hf][1] * 0x00800000u;
-      const uint32_t s23 = (vs[hf][2] << 7) + vs[hf][3] * 0x00800000u;
+      uint2 vw[4];
+      uint32_t vs[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        vw[i] = lds64(vp + hf * half, i * kRow4Bytes);
+        vs[i] = lds8(vq + hf * half, i * kRow4Bytes);
+      }
+      if (hf == 1) release();
+      const uint32_t s01 = (vs[0] << 7) + vs[1] * 0x00800000u;
+      const uint32_t s23 = (vs[2] << 7) + vs[3] * 0x00800000u;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         uint32_t x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = j ? vw[hf][i].y : vw[hf][i].x;
+        for (int i = 0; i < 4; ++i) x[i] = j ? vw[i].y : vw[i].x;
         uint32_t a0[4], a1[4], a2[4], a3[4];                // of tiles 4 j .. 4 j + 3
         halves4_of((x[0] & kLow) | ((x[1] << 4) & ~kLow), a0[0], a0[1], a0[2], a0[3]);
         halves4_of(((x[0] >> 4) & kLow) | (x[1] & ~kLow), a1[0], a1[1], a1[2], a1[3]);
@@ -632,12 +666,16 @@ struct Fp4Rows {
   }
 
   __device__ __forceinline__ void store(float* macc, float* ml) {
-    float lt = l + __shfl_xor_sync(kFull, l, 1);
-    lt += __shfl_xor_sync(kFull, lt, 2);
     const int g = lane >> 2, c = lane & 3;
-    if (g < rows && c == 0) {
-      ml[g * 2] = m;
-      ml[g * 2 + 1] = lt;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float lt = l[h] + __shfl_xor_sync(kFull, l[h], 4);
+      lt += __shfl_xor_sync(kFull, lt, 8);
+      lt += __shfl_xor_sync(kFull, lt, 16);
+      if (g == 0 && 2 * c + h < rows) {
+        ml[(2 * c + h) * 2] = m[h];
+        ml[(2 * c + h) * 2 + 1] = lt;
+      }
     }
     constexpr float kBack = 1.f / 1024.f;
 #pragma unroll
