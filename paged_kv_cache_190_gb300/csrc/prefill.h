@@ -16,7 +16,7 @@ namespace pa {
 
 constexpr int kPrefillKeys = 128;                 // keys of a step
 constexpr int kPrefillRows = 256;                 // query rows of an item: two products of 128
-constexpr int kPrefillRowsF32 = 64;               // float32 pools
+constexpr int kPrefillRowsF32 = 32;               // float32 pools: the smaller of their two tiles
 constexpr int kPrefillKeysF32 = 64;
 constexpr int kPrefillNoWindow = 1 << 30;
 
@@ -67,7 +67,7 @@ size_t prefill_workspace_size(int num_tokens, int num_seqs, int num_q_heads, int
                               int num_sms);
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t run_prefill_bf16(int head_dim, const PrefillParams& p, int grid, cudaStream_t stream);
-cudaError_t run_prefill_f32(int head_dim, const PrefillParams& p, int grid, cudaStream_t stream);
+cudaError_t run_prefill_f32(int head_dim, int rows, const PrefillParams& p, int grid, cudaStream_t stream);
 
 #ifdef __CUDACC__
 // A sequence's part of the call: rows q0 .. q0 + n - 1, the last n of `len` tokens.

@@ -303,7 +303,10 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   const int64_t least_items = static_cast<int64_t>(a.num_tokens) * group / kPrefillRows * a.num_kv_heads;
   p.may_share = !a.f32 && a.max_len > kLeastShare * kPrefillKeys && a.max_len <= kMostShared && least_items <= static_cast<int64_t>(kMostRounds) * a.num_sms &&
                 a.num_sms * kMostRounds <= kPlanTiles;
-  p.room = static_cast<int>(most_tiles(a.num_tokens, a.num_seqs, group, a.f32 ? kPrefillRowsF32 : kPrefillRows));
+  // float32: tiles of 64 rows, of 32 where those leave SMs without one
+  const int rows = !a.f32 ? kPrefillRows
+      : most_tiles(a.num_tokens, a.num_seqs, group, 64) * a.num_kv_heads > 2 * a.num_sms ? 64 : kPrefillRowsF32;
+  p.room = static_cast<int>(most_tiles(a.num_tokens, a.num_seqs, group, rows));
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.num_seqs = a.num_seqs;
   p.num_tokens = a.num_tokens;
@@ -337,7 +340,6 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
     if (e == cudaSuccess) e = make_bf16_map(&p.map_q, a.q, 4, q_dims, q_strides, q_box);
     if (e != cudaSuccess) return e;
   }
-  const int rows = a.f32 ? kPrefillRowsF32 : kPrefillRows;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -348,7 +350,7 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   const int64_t items = most_tiles(a.num_tokens, a.num_seqs, group, rows) * a.num_kv_heads;
   // one item a CTA at most, and none long enough to be cut: each CTA finds its own, without
   // a plan (37 tokens of one prompt: kDirectMeasured)
-  p.direct = !p.may_share && items <= a.num_sms;
+  p.direct = !p.may_share && items <= (a.f32 ? 2 : 1) * a.num_sms;
   cudaError_t e = cudaSuccess;
   if (!p.direct) {
     const bool small = a.num_seqs <= 256 && most_tiles(a.num_tokens, a.num_seqs, group, rows) <= 1024 && a.num_sms <= 256;
@@ -359,7 +361,7 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
     e = cudaLaunchKernelEx(&cfg, plan, p, rows);
     if (e != cudaSuccess) return e;
   }
-  if (a.f32) return run_prefill_f32(D, p, static_cast<int>(std::min<int64_t>(items, 2 * a.num_sms)), stream);
+  if (a.f32) return run_prefill_f32(D, rows, p, static_cast<int>(std::min<int64_t>(items, 2 * a.num_sms)), stream);
   e = run_prefill_bf16(D, p, p.may_share ? a.num_sms : static_cast<int>(std::min<int64_t>(items, a.num_sms)), stream);
   if (e != cudaSuccess || !p.may_share) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(a.num_sms), static_cast<unsigned>((at.slot_rows + kJoinRows - 1) / kJoinRows));
