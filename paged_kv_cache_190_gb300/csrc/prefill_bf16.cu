@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
     }
   };
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return mbar_try_wait(bar, parity) || (!*abort_flag && mbar_wait(bar, parity, p.wait_limit));
+    // (the flag is not looked at where the first poll says yes, as it nearly always does)
+    return p.wait_limit != 0 && (mbar_try_wait(bar, parity) || (!*abort_flag && mbar_wait(bar, parity, p.wait_limit - 1)));
   };
   PrefillWalk<kPrefillKeys> walk(p, tile_tokens);
   PrefillItem it;

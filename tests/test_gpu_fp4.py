@@ -255,3 +255,102 @@ def test_decode_rows_of_the_largest_and_smallest_scales():
     dv.call()
     assert dv.errors() == 0
     check(c, dv.out)
+
+
+def test_decode_captured_and_replayed_on_two_streams():
+    cs = [Decode4(50 + i, [100, 700, 5], 1, 8, 2, 16) for i in range(2)]
+    dvs = [Dev(c) for c in cs]
+    graphs = []
+    for dv in dvs:
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(s):
+            dv.call(workspace=ws)
+            with torch.cuda.graph(g, stream=s):
+                dv.call(workspace=ws)
+        graphs.append((s, g, ws))
+    torch.cuda.synchronize()
+    for dv in dvs:
+        dv.out.fill_(float("nan"))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, g, _ in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for c, dv in zip(cs, dvs):
+        assert dv.errors() == 0
+        check(c, dv.out)
+
+
+@pytest.mark.parametrize("limit", [0, 64])
+def test_decode_expired_waits_report_and_leave_the_context_usable(limit):
+    c = Decode4(60, [100, 2000, 900] * 20, 1, 8, 2, 16)
+    dv = Dev(c)
+    try:
+        pa.pa_debug_set_wait_limit(limit)
+        for _ in range(3):
+            dv.call()
+        flags = dv.errors()
+    finally:
+        pa.pa_debug_set_wait_limit(-1)
+    assert flags & ~pa.PA_DEVERR_TIMEOUT == 0 and (limit or flags)
+    dv.call()
+    assert dv.errors() == 0
+    check(c, dv.out)
+
+
+def test_pools_past_32_bits():
+    """Append, read back and decode in the last pages of pools of more than 2^32 bytes."""
+    hkv, bs, T = 8, 16, 40
+    nb = (1 << 32) // (hkv * bs * 72) + 60
+    r = np.random.default_rng(61)
+    kc, vc = (torch.empty(nb, hkv, bs, 72, dtype=torch.uint8, device=DEV) for _ in range(2))
+    pages = nb - 1 - np.arange(3)
+    qkv = torch.from_numpy(r.standard_normal((T, 3 * hkv, 128))).bfloat16().to(DEV)
+    q, k, v = qkv.split([hkv, hkv, hkv], 1)
+    slots = torch.from_numpy((pages[np.arange(T) // bs] * bs + np.arange(T) % bs).astype(np.int64)).to(DEV)
+    errs = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pa.pa_rope_and_cache_fp4(None, None, k, v, kc, vc, slots, None, None, device_errors=errs)
+    host = [oracle.pack_rows(x.float().cpu().numpy()) for x in (k, v)]
+    back = torch.zeros(2, 3, hkv, bs, 128, dtype=torch.bfloat16, device=DEV)
+    pairs = torch.from_numpy(np.stack([pages, np.arange(3)], 1).astype(np.int64)).to(DEV)
+    pa.pa_read_pages_fp4(back[0], back[1], kc, vc, pairs, device_errors=errs)
+    for got, want in zip(back, host):
+        rows = got.transpose(1, 2).reshape(-1, hkv, 128)[:T].double().cpu().numpy()
+        np.testing.assert_array_equal(rows, oracle.unpack_rows(want))
+    out = torch.empty(1, hkv, 128, dtype=torch.bfloat16, device=DEV)
+    table = torch.from_numpy(pages.astype(np.int32))[None].to(DEV)
+    pa.pa_decode_fp4(out, q[-1:].contiguous(), kc, vc, table, torch.tensor([T], dtype=torch.int32, device=DEV), 128 ** -0.5,
+                     hkv, T, device_errors=errs)
+    kk, vv = (oracle.unpack_rows(x) for x in host)
+    for h in range(hkv):
+        s = 128 ** -0.5 * (kk[:, h] @ q[-1, h].double().cpu().numpy())
+        w = np.exp(s - s.max())
+        w /= w.sum()
+        np.testing.assert_allclose(out_as_f64(out)[0, h], w @ vv[:, h], rtol=2.0 ** -8, atol=2.0 ** -11 * 8 * np.abs(vv[:, h]).max())
+    assert pa.pa_read_device_errors(errs) == 0
+
+
+def test_python_refusals():
+    c = Decode4(62, [40, 30], 1, 8, 2, 16)
+    for name, bad, err in (("kc", None, TypeError), ("q", "float", TypeError), ("tables", "long", TypeError)):
+        dv = Dev(c)
+        setattr(dv, name, getattr(getattr(dv, name), bad)() if bad else dv.kc.view(torch.int8))
+        with pytest.raises(err):
+            dv.call()
+    dv = Dev(c)
+    dv.kc, dv.vc = dv.kc[..., :64].contiguous(), dv.vc[..., :64].contiguous()
+    with pytest.raises(ValueError):
+        dv.call()
+    out = torch.zeros(2, 4, 2, 16, 128, dtype=torch.bfloat16, device=DEV)
+    dv, pairs = Dev(c), torch.zeros(1, 2, dtype=torch.int64, device=DEV)
+    for args, err in (((out[0], out[1].float(), dv.kc, dv.vc, pairs), TypeError),
+                      ((out[0], out[1, :3], dv.kc, dv.vc, pairs), ValueError),
+                      ((out[0], out[1], dv.kc, dv.vc, pairs.int()), TypeError),
+                      ((out[0], out[1], dv.kc, dv.vc, pairs[0]), ValueError),
+                      ((out[0, :, :1], out[1, :, :1], dv.kc, dv.vc, pairs), ValueError)):
+        with pytest.raises(err):
+            pa.pa_read_pages_fp4(*args)
