@@ -136,6 +136,11 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile_tokens = kPrefillRows >> p.group_log2;
+  if (p.wait_limit == 0) {                                 // no wait may succeed: nothing is begun
+    if (threadIdx.x == 0) report(p.device_errors, PA_DEVERR_TIMEOUT);
+    wait_prior_grids();
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < R; ++i) {
@@ -177,7 +182,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
   };
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     // (the flag is not looked at where the first poll says yes, as it nearly always does)
-    return p.wait_limit != 0 && (mbar_try_wait(bar, parity) || (!*abort_flag && mbar_wait(bar, parity, p.wait_limit - 1)));
+    return mbar_try_wait(bar, parity) || (!*abort_flag && mbar_wait(bar, parity, p.wait_limit));
   };
   PrefillWalk<kPrefillKeys> walk(p, tile_tokens);
   PrefillItem it;
