@@ -349,12 +349,12 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
       } at{0, 0};
       uint32_t p_parity = 0, o_parity = 1, q_parity = 0, t_parity = half ^ 1;
       bool ok = true;
-        // (the lanes agree on giving up)
-      auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, wait(bar, parity)) != 0; };
+        // (the lanes agree on giving up, once a step: a vote takes as long as the wait before it)
+      auto agreed = [&] { return ok = __all_sync(kFull, ok) != 0; };
       // S = this half's rows of q times the K tile in `slot`
       auto scores = [&](uint32_t slot, uint32_t id) {
         const uint32_t k_lo = uniform(k_lo0 + slot * (Ly::TILE >> 4));
-        if (issues) {
+        if (issues && ok) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = ((ks >> 2) * Ly::Q_SLAB + (ks & 3) * 32) >> 4;
@@ -365,9 +365,8 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
         __syncwarp();
       };
       // O += the weights times the V tile in `slot`
-      auto values = [&](uint32_t slot, int keys, uint32_t accumulate) {
-        const uint32_t v_lo = uniform(v_lo0 + slot * (Ly::TILE >> 4));
-        if (issues) {
+      auto values = [&](uint32_t v_lo, int keys, uint32_t accumulate) {
+        if (issues && ok) {
           if (keys == kPrefillKeys) {
 #pragma unroll
             for (int g = 0; g < kPrefillKeys / 16; ++g)
@@ -390,7 +389,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
         // would end, and their softmaxes begin, together, with the tensor cores idle meanwhile.
         auto my_turn = [&] {
           if (!two) return true;
-          const bool mine = all_wait(&turn[half], t_parity);
+          const bool mine = wait(&turn[half], t_parity);
           t_parity ^= 1;
           return mine;
         };
@@ -400,13 +399,13 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
         if (half == 1 && !two) {
           // no rows for this half: the slots are given back as they come
           for (int i = 0; i < 2 * steps && ok; ++i) {
-            ok = all_wait(&full[at.i], at.parity);
-            if (ok && issues) mbar_arrive(&empty[at.i]);
+            ok = wait(&full[at.i], at.parity);
+            if (agreed() && issues) mbar_arrive(&empty[at.i]);
             at.next();
           }
           if (ok) {
-            ok = all_wait(q_full, q_parity);
-            if (issues) mbar_arrive(q_empty);
+            ok = wait(q_full, q_parity);
+            if (agreed() && issues) mbar_arrive(q_empty);
           }
           q_parity ^= 1;
           continue;
@@ -414,8 +413,8 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
         // (the last step is the only one that may be short)
         const int tail = min(kPrefillKeys, it.t.end - (it.v1 - 1 + (it.v1 - 1 >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys);
         const uint32_t id_tail = umma_idesc_bf16(128, (tail + 15) & ~15, false);
-        ok = all_wait(q_full, q_parity) && all_wait(&full[at.i], at.parity) && my_turn();
-        if (!ok) break;
+        ok = wait(q_full, q_parity) && wait(&full[at.i], at.parity) && my_turn();
+        if (!agreed()) break;
         q_parity ^= 1;
         tmem_fence_after();
         scores(at.i, steps == 1 ? id_tail : kIdS);
@@ -429,12 +428,13 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
           Slot kn = at;                                    // V of this step; K of the next
           kn.next();
           const bool next = v + 1 < steps;
-          ok = all_wait(&full[at.i], at.parity) && (v > 0 || all_wait(&o_free[half], o_parity)) && my_turn() &&
-               all_wait(&p_full[half], p_parity);
-          if (!ok) break;
+          const uint32_t v_lo = uniform(v_lo0 + at.i * (Ly::TILE >> 4));
+          ok = wait(&full[at.i], at.parity) && (v > 0 || wait(&o_free[half], o_parity)) && my_turn() &&
+               wait(&p_full[half], p_parity);
           tmem_fence_after();
-          values(at.i, next ? kPrefillKeys : tail, v > 0 ? 1u : 0u);
-          if (next && !(ok = all_wait(&full[kn.i], kn.parity))) break;
+          values(v_lo, next ? kPrefillKeys : tail, v > 0 ? 1u : 0u);
+          if (next) ok = ok && wait(&full[kn.i], kn.parity);
+          if (!agreed()) break;
           // (S goes where the weights stand that the product before reads: the tensor cores
           // take one thread's products in their order)
           if (next) scores(kn.i, v + 2 == steps ? id_tail : kIdS);
@@ -482,19 +482,17 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
       float m = kNoScore, l = 0.f;
       for (int v = it.v0; v < (t.steps > 0 ? it.v1 : it.v0); ++v, ++n, ++steps) {
         const int t0 = (v + (v >= t.ns ? t.shift : 0)) * kPrefillKeys;
-        ok = wait(&s_full[half], n & 1);
-        ok = __all_sync(kFull, ok);
-        if (!ok) break;
+        // does every row of this warp see every key of the step?
+        const bool sees_all = t0 + kPrefillKeys <= first_pos + 1 &&
+                              (t0 + p.window > last_pos || t0 + kPrefillKeys <= p.sinks);
+        const bool got = wait(&s_full[half], n & 1);
         tmem_fence_after();
         float s[128];
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s + 32 * i);
-        tmem_landed(s);
         const uint32_t bad = bad_ring[steps % kBadRing];
-        // does every row of this warp see every key of the step?
-        const bool all = bad == 0 && t0 + kPrefillKeys <= first_pos + 1 &&
-                         (t0 + p.window > last_pos || t0 + kPrefillKeys <= p.sinks);
-        if (!all) {
+        tmem_landed(s);
+        if (!sees_all || bad != 0) {
           const int last = pos - t0, first = pos - p.window + 1 - t0, sinks = p.sinks - t0;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {                    // a bit for each of 32 keys
@@ -561,8 +559,12 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
           float l0, l1;
           unpair(add2(sum[0], sum[1]), l0, l1);
           sum_l = l0 + l1;
-          if (refer || !__any_sync(kFull, sum_l > kMostSum)) break;
+          // (the lanes agree on giving up here: one vote a step)
+          if (!__any_sync(kFull, !got || (!refer && sum_l > kMostSum))) break;
+          ok = __all_sync(kFull, got);
+          if (!ok) break;
         }
+        if (!ok) break;
         l += sum_l;
         tmem_wait_st();
         tmem_fence_before();
