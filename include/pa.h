@@ -464,7 +464,8 @@ int pa_copy_scales(const float* src_k_scales, const float* src_v_scales, float* 
  * written to k_out[dst] and v_out[dst], bf16 [num_dst_blocks][num_kv_heads][block_size]
  * [128].  With a table of the dst pages, pa_prefill attends to them.  Ids outside
  * [0, num_src_blocks) or [0, num_dst_blocks) set PA_DEVERR_BAD_BLOCK and that pair is
- * skipped.  Destinations must be distinct; the pools must not overlap.
+ * skipped.  Destinations must be distinct; the pools must not overlap.  k_out and v_out are
+ * aligned to 32 bytes (16 are refused).
  *
  * pa_decode_fp4: pa_decode_window over such pools (window 0, sinks 0 for none): q and out
  * bf16; workspace of pa_decode_window_workspace_size.  Elements enter the products exactly,

@@ -157,8 +157,9 @@ int pa_read_pages_fp4(void* k_out, void* v_out, const void* k_cache, const void*
     return PA_ERR_INVALID_ARG;
   if (num_pairs == 0) return PA_OK;
   if (!k_out || !v_out || !k_cache || !v_cache || !src_dst_pairs) return PA_ERR_INVALID_ARG;
-  using pa::aligned16;
-  if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_cache) || !aligned16(v_cache))
+  // rows are written 32 bytes at a time
+  if (!pa::aligned32(k_out) || !pa::aligned32(v_out) || !pa::aligned16(k_cache) ||
+      !pa::aligned16(v_cache))
     return PA_ERR_INVALID_ARG;
   const cudaError_t e = pa::launch_read_pages_fp4(
       k_out, v_out, k_cache, v_cache, src_dst_pairs, num_pairs, num_kv_heads * block_size,

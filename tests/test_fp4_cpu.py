@@ -131,6 +131,13 @@ def test_misaligned_buffers_are_refused():
         assert _prefill(**{name: p + 8}) == -1
 
 
+@pytest.mark.parametrize("name", ["ko", "vo"])
+def test_read_wants_destinations_on_32_bytes(name):
+    buf, p = _buffer()
+    assert p % 32 == 0
+    assert _read(**{name: p + 16}) == -1
+
+
 def _decode(**over):
     buf, p = _buffer()
     a = dict(out=p, q=p, k=p, v=p, bt=p, cl=p, scale=1.0, hkv=8, b=2, hq=32, ql=1, d=128, bs=16, nb=64, mbps=8,
