@@ -507,15 +507,19 @@ int pa_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_c
  * that none sees does not matter; a NaN or infinity in a V row reaches other rows of its kv
  * head near the tokens that see it, as a product with the weight 0.
  * A length below 0 or above max_context_len, a sequence shorter than its new tokens and
- * q_starts that decrease or leave the rows set PA_DEVERR_BAD_LENGTH (lengths are clamped,
- * such rows are left as they were); block ids outside the pool set PA_DEVERR_BAD_BLOCK and
+ * q_starts that decrease or leave the rows set PA_DEVERR_BAD_LENGTH.  Lengths are clamped;
+ * the first rows of a sequence shorter than its new tokens see nothing and are zeros; a
+ * sequence whose starts leave the rows, or decrease, is left out.  Where q_starts decrease
+ * anywhere, rows of other sequences may be left as they were too, and rows that two
+ * sequences claim are either's.  Block ids outside the pool set PA_DEVERR_BAD_BLOCK and
  * their tokens are not seen.
  *
  * Logits, maxima and sums are float32, the result is rounded once.  Over bf16 pools the
  * weights are rounded to bf16 for the product with V (2^-8 of each; the sum is that of the
  * unrounded ones), as is usual for whole prompts, where the products are the cost: a second
- * bf16 part of each weight would take half as long again.  Over float32 pools nothing is
- * rounded.
+ * bf16 part of each weight would take half as long again.  They are relative to a reference
+ * that a step of 128 keys may pass by 2^16, so elements of V beyond 2^96 may overflow (up to
+ * 2^23 keys a row).  Over float32 pools nothing is rounded, and the reference is the maximum.
  *
  * workspace: device scratch of pa_prefill_workspace_size bytes, 256-byte aligned; it
  * carries no state between calls, but two calls in flight at once must not share it.

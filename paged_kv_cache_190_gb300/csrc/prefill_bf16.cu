@@ -9,7 +9,13 @@
 // beside the two).
 //
 // What bounds it: the products.  A step of 128 keys for 256 rows of 128 columns is 16.8
-// MFLOP, 64 KiB of K and V and 32768 exponentials.
+// MFLOP (2048 clocks of the tensor cores), 64 KiB of K and V and 32768 exponentials (1024
+// clocks).  On a GB300 (1990 TFLOP/s of bf16 products measured, 1738 in a long run), 32 query
+// and 8 kv heads of 128: one prompt of 16384 tokens 1323 us, 1660 TFLOP/s of what causality
+// leaves; 12 ragged prompts, 17569 tokens, 231 us, 1240; 6 chunks of 200 to 512 tokens behind
+// up to 15000 248 us, 1290; one prompt of 37 tokens 6.5 us.  Heads of 64 have the same
+// exponentials for half the products: 4 prompts, 12802 tokens of 16 heads, in windows of 1024
+// take 116 us.
 //
 // Layout of the work:
 //   * An item is a kv head and a tile of 256 rows: 256 / G consecutive new tokens of a
@@ -17,6 +23,9 @@
 //     Its rows are two products of 128 (M = 128).  While one half's scores are in softmax
 //     the tensor cores work for the other: S0, S1 (128 columns each), O0 and O1 fill the
 //     512 columns of tensor memory.
+//   * A warp for each half issues its products, in turns, through one of its lanes.  (A warp
+//     whose values stay uniform: 1492 us for the prompt of 16384 when a single thread took
+//     1588.)
 //   * The weights are written back to tensor memory over the scores they came from (bf16, 64
 //     columns) and enter the second product from there: shared memory feeds V alone then,
 //     while both operands of the first product come from it, which is just its rate.
@@ -197,268 +206,268 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
   // 256 * 184 + 128 * 136.
   if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
-  if (warp == kProducer) {
-    // ------------------------------------------------------------ copies
-    const int bs = p.block_size, pages_of_step = kPrefillKeys >> p.block_log2;
-    const int j = lane / Ly::SLABS, slab = lane % Ly::SLABS;   // of K: page of the step, slab
-    uint32_t c = 0, steps = 0, raw_used = 0, raw_parity = 0;   // ring slots filled; raw: a bit a slot
-    bool ok = true;
-    int items_done = 0;
-    while (ok && walk.next(it)) {
-      if (it.t.steps <= 0) continue;
-      if (lane == 0) {                                     // q, once the last item's is no longer read
-        ok = wait(q_empty, (items_done & 1) ^ 1);
-        if (ok) {
-          const int halves = (it.t.tokens << p.group_log2) > 128 ? 2 : 1;
-          mbar_arrive_expect_tx(q_full, halves * Ly::Q_HALF);
-          for (int i = 0; i < halves; ++i)
-            for (int s = 0; s < Ly::SLABS; ++s)
-              tma_load_4d(smem + i * Ly::Q_HALF + s * Ly::Q_SLAB, &p.map_q, 64 * s, 0, it.h,
-                          it.t.row0 + i * (tile_tokens / 2), q_full);
-        }
-      }
-      ok = __shfl_sync(kFull, ok, 0);
-      if (!ok) break;
-      ++items_done;
-      const int32_t* table = p.tables + static_cast<int64_t>(it.b) * p.max_blocks;
-      // lane l: page l of a step, as a row of the pool's map (-1: not there, reads zeros;
-      // -2: nobody sees it, not read); the next step's is looked up ahead
-      auto look = [&](int v) {
-        if (v >= it.v1 || lane >= pages_of_step) return -2;
-        const int first = (v + (v >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys + lane * bs;
-        if (first >= it.t.end || (first >= p.sinks && first + bs <= it.t.lo)) return -2;
-        const int page = table[first >> p.block_log2];
-        return page >= 0 && page < p.num_blocks ? page * p.num_kv_heads + it.h : -1;
-      };
-      int ahead = look(it.v0);
-      for (int v = it.v0; v < it.v1; ++v, ++steps) {
-        const int z = ahead;
-        ahead = look(v + 1);
-        const int t0 = (v + (v >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys, hi = min(it.t.end, t0 + kPrefillKeys);
-        const uint32_t there = __ballot_sync(kFull, z != -2), gone = __ballot_sync(kFull, z == -1);
-        const int bytes = __popc(there) * bs * D * 2;
-        // ---- K
-        int slot = c % R;
-        if (lane == 0) ok = wait(&empty[slot], ((c / R) & 1) ^ 1);
-        ok = __shfl_sync(kFull, ok, 0);
-        if (!ok) break;
-        if (lane == 0) {
-          if (gone) report(p.device_errors, PA_DEVERR_BAD_BLOCK);
-          uint32_t word = gone;                            // a bit for each 16 keys
-          if (bs == 32) {
-            word = 0;
-            for (int i = 0; i < 4; ++i)
-              if ((gone >> i) & 1) word |= 3u << (2 * i);
-          }
-          bad_ring[steps % kBadRing] = word;
-          mbar_arrive_expect_tx(&full[slot], bytes);
-        }
-        raw_used &= ~(1u << slot);
-        __syncwarp();
-        const int zk = __shfl_sync(kFull, z, j < pages_of_step ? j : 0);
-        if (j < pages_of_step && zk != -2)
-          tma_load_4d(smem + Ly::OFF_RING + slot * Ly::TILE + slab * Ly::Q_SLAB + j * bs * 128, &p.map_k, 0, 0, zk,
-                      slab, &full[slot]);
-        ++c;
-        // ---- V
-        slot = c % R;
-        if (lane == 0) ok = wait(&empty[slot], ((c / R) & 1) ^ 1);
-        ok = __shfl_sync(kFull, ok, 0);
-        if (!ok) break;
-        int x, y;
-        const bool clear = (hi & 15) != 0 || hidden(it.t, t0, hi, x, y);
-        uint64_t* bar = clear ? &raw[slot] : &full[slot];
-        raw_used = clear ? raw_used | 1u << slot : raw_used & ~(1u << slot);
-        if (clear) raw_parity ^= 1u << slot;
-        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-        __syncwarp();
-        if (z >= -1)
-          tma_load_4d(smem + Ly::OFF_RING + slot * Ly::TILE + lane * bs * D * 2, &p.map_v, 0, 0, z, 0, bar);
-        ++c;
-      }
-    }
-    if (!ok && lane == 0) fail();
-    // the copies still in flight must land before the shared memory is released
-    if (lane == 0) {
-      for (uint32_t i = c > R ? c - R : 0; i < c; ++i) {
-        const int slot = i % R;
-        if ((raw_used >> slot) & 1) mbar_wait(&raw[slot], ((raw_parity >> slot) & 1) ^ 1);
-        else mbar_wait(&full[slot], (i / R) & 1);
-      }
-      if (items_done > 0) mbar_wait(q_full, (items_done - 1) & 1);
-    }
-  } else if (warp == kCleaner) {
-    // ------------------------------------------------------------ V rows that nobody sees
-    uint32_t c = 0, raw_parity = 0;
-    bool ok = true;
-    while (ok && walk.next(it)) {
-      if (it.t.steps <= 0) continue;
-      for (int v = it.v0; v < it.v1 && ok; ++v, c += 2) {
-        const int slot = (c + 1) % R;
-        const int t0 = (v + (v >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys, hi = min(it.t.end, t0 + kPrefillKeys);
-        int x, y;
-        const bool behind = hidden(it.t, t0, hi, x, y);
-        if ((hi & 15) == 0 && !behind) continue;
-        ok = wait(&raw[slot], (raw_parity >> slot) & 1);
-        ok = __all_sync(kFull, ok);
-        if (!ok) break;
-        raw_parity ^= 1u << slot;
-        const uint32_t base = smem_addr(smem + Ly::OFF_RING + slot * Ly::TILE);
-        const int bs = p.block_size;
-        auto clear = [&](int from, int to) {
-          for (int i = lane; i < (to - from) * (D / 8); i += 32) {
-            const int t = from + i / (D / 8), ch = i % (D / 8), page = t >> p.block_log2, r = t & (bs - 1);
-            const uint32_t a = base + page * bs * D * 2 + (ch >> 3) * bs * 128 + r * 128 + (ch & 7) * 16;
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
-          }
-        };
-        clear(hi - t0, (hi - t0 + 15) & ~15);
-        if (behind) clear(x - t0, y - t0);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[slot]);
-      }
-    }
-    if (!ok && lane == 0) fail();
-  } else if (warp == kIssuer || warp == kIssuer + kIssuerStep) {
-    // ------------------------------------------------------------ products: a thread for each half
-    // (What is done between two products is not hidden behind them: the queue is short.  So
-    // there are two issuers, slots are counted up instead of divided, descriptors differ from
-    // ready ones by an addition.  The warp runs as one and a lane of it issues, with values
-    // that the compiler knows to be the warp's: they stay in uniform registers.)
-    {
-      const int half = warp == kIssuer ? 0 : 1;
-      const bool issues = elect_lane();
-      const uint32_t ring = smem_addr(smem + Ly::OFF_RING);
-      constexpr uint32_t kIdS = umma_idesc_bf16(128, kPrefillKeys, false), kIdPV = umma_idesc_bf16(128, D, true);
-      const uint64_t qd0 = umma_desc(smem_addr(smem) + half * Ly::Q_HALF, 16, 1024);
-      const uint64_t kd0 = umma_desc(ring, 16, 1024), vd0 = umma_desc(ring, p.block_size * 128, 1024);
-      const uint32_t q_lo = uniform(static_cast<uint32_t>(qd0)), sbo = static_cast<uint32_t>(kd0 >> 32);
-      const uint32_t k_lo0 = uniform(static_cast<uint32_t>(kd0)), v_lo0 = uniform(static_cast<uint32_t>(vd0));
-      const uint32_t s_at = uniform(tmem + 128 * half), o_at = uniform(tmem + kTmemO + 128 * half);
-      // from 16 keys to the next within V's tile: bs 16, a page; bs 32, 16 rows and then a page
-      const uint32_t v_odd = (p.block_size == 16 ? 16 * D * 2 : 16 * 128) >> 4, v_even = (2 * 16 * D * 2) >> 4;
-      struct Slot {
-        uint32_t i, parity;
-        __device__ __forceinline__ void next() {
-          if (++i == R) {
-            i = 0;
-            parity ^= 1;
-          }
-        }
-      } at{0, 0};
-      uint32_t p_parity = 0, o_parity = 1, q_parity = 0, t_parity = half ^ 1;
+    if (warp == kProducer) {
+      // ------------------------------------------------------------ copies
+      const int bs = p.block_size, pages_of_step = kPrefillKeys >> p.block_log2;
+      const int j = lane / Ly::SLABS, slab = lane % Ly::SLABS;   // of K: page of the step, slab
+      uint32_t c = 0, steps = 0, raw_used = 0, raw_parity = 0;   // ring slots filled; raw: a bit a slot
       bool ok = true;
-        // (the lanes agree on giving up, once a step: a vote takes as long as the wait before it)
-      auto agreed = [&] { return ok = __all_sync(kFull, ok) != 0; };
-      // S = this half's rows of q times the K tile in `slot`
-      auto scores = [&](uint32_t slot, uint32_t id) {
-        const uint32_t k_lo = uniform(k_lo0 + slot * (Ly::TILE >> 4));
-        if (issues && ok) {
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = ((ks >> 2) * Ly::Q_SLAB + (ks & 3) * 32) >> 4;
-            umma_bf16(s_at, desc_of(q_lo + off, sbo), desc_of(k_lo + off, sbo), id, ks > 0 ? 1u : 0u);
-          }
-          umma_commit(&s_full[half]);
-        }
-        __syncwarp();
-      };
-      // O += the weights times the V tile in `slot`
-      auto values = [&](uint32_t v_lo, int keys, uint32_t accumulate) {
-        if (issues && ok) {
-          if (keys == kPrefillKeys) {
-#pragma unroll
-            for (int g = 0; g < kPrefillKeys / 16; ++g)
-              umma_bf16_ts(o_at, s_at + 8 * g, desc_of(v_lo + (g >> 1) * v_even + (g & 1) * v_odd, sbo), kIdPV,
-                           g > 0 ? 1u : accumulate);
-          } else {
-            for (int g = 0; 16 * g < keys; ++g)
-              umma_bf16_ts(o_at, s_at + 8 * g, desc_of(v_lo + (g >> 1) * v_even + (g & 1) * v_odd, sbo), kIdPV,
-                           g > 0 ? 1u : accumulate);
-          }
-          umma_commit(&pv_done[half]);
-        }
-        __syncwarp();
-      };
+      int items_done = 0;
       while (ok && walk.next(it)) {
         if (it.t.steps <= 0) continue;
-        const int steps = it.v1 - it.v0;
-        const bool two = (it.t.tokens << p.group_log2) > 128;
-        // Products in turns, a step's of one half and then of the other: both halves' at once
-        // would end, and their softmaxes begin, together, with the tensor cores idle meanwhile.
-        auto my_turn = [&] {
-          if (!two) return true;
-          const bool mine = wait(&turn[half], t_parity);
-          t_parity ^= 1;
-          return mine;
-        };
-        auto pass_turn = [&] {
-          if (two && issues) mbar_arrive(&turn[half ^ 1]);
-        };
-        if (half == 1 && !two) {
-          // no rows for this half: the slots are given back as they come
-          for (int i = 0; i < 2 * steps && ok; ++i) {
-            ok = wait(&full[at.i], at.parity);
-            if (agreed() && issues) mbar_arrive(&empty[at.i]);
-            at.next();
-          }
+        if (lane == 0) {                                     // q, once the last item's is no longer read
+          ok = wait(q_empty, (items_done & 1) ^ 1);
           if (ok) {
-            ok = wait(q_full, q_parity);
-            if (agreed() && issues) mbar_arrive(q_empty);
+            const int halves = (it.t.tokens << p.group_log2) > 128 ? 2 : 1;
+            mbar_arrive_expect_tx(q_full, halves * Ly::Q_HALF);
+            for (int i = 0; i < halves; ++i)
+              for (int s = 0; s < Ly::SLABS; ++s)
+                tma_load_4d(smem + i * Ly::Q_HALF + s * Ly::Q_SLAB, &p.map_q, 64 * s, 0, it.h,
+                            it.t.row0 + i * (tile_tokens / 2), q_full);
           }
-          q_parity ^= 1;
-          continue;
         }
-        // (the last step is the only one that may be short)
-        const int tail = min(kPrefillKeys, it.t.end - (it.v1 - 1 + (it.v1 - 1 >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys);
-        const uint32_t id_tail = umma_idesc_bf16(128, (tail + 15) & ~15, false);
-        ok = wait(q_full, q_parity) && wait(&full[at.i], at.parity) && my_turn();
-        if (!agreed()) break;
-        q_parity ^= 1;
-        tmem_fence_after();
-        scores(at.i, steps == 1 ? id_tail : kIdS);
-        pass_turn();
-        if (issues) {
-          umma_commit(&empty[at.i]);
-          if (steps == 1) umma_commit(q_empty);
+        ok = __shfl_sync(kFull, ok, 0);
+        if (!ok) break;
+        ++items_done;
+        const int32_t* table = p.tables + static_cast<int64_t>(it.b) * p.max_blocks;
+        // lane l: page l of a step, as a row of the pool's map (-1: not there, reads zeros;
+        // -2: nobody sees it, not read); the next step's is looked up ahead
+        auto look = [&](int v) {
+          if (v >= it.v1 || lane >= pages_of_step) return -2;
+          const int first = (v + (v >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys + lane * bs;
+          if (first >= it.t.end || (first >= p.sinks && first + bs <= it.t.lo)) return -2;
+          const int page = table[first >> p.block_log2];
+          return page >= 0 && page < p.num_blocks ? page * p.num_kv_heads + it.h : -1;
+        };
+        int ahead = look(it.v0);
+        for (int v = it.v0; v < it.v1; ++v, ++steps) {
+          const int z = ahead;
+          ahead = look(v + 1);
+          const int t0 = (v + (v >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys, hi = min(it.t.end, t0 + kPrefillKeys);
+          const uint32_t there = __ballot_sync(kFull, z != -2), gone = __ballot_sync(kFull, z == -1);
+          const int bytes = __popc(there) * bs * D * 2;
+          // ---- K
+          int slot = c % R;
+          if (lane == 0) ok = wait(&empty[slot], ((c / R) & 1) ^ 1);
+          ok = __shfl_sync(kFull, ok, 0);
+          if (!ok) break;
+          if (lane == 0) {
+            if (gone) report(p.device_errors, PA_DEVERR_BAD_BLOCK);
+            uint32_t word = gone;                            // a bit for each 16 keys
+            if (bs == 32) {
+              word = 0;
+              for (int i = 0; i < 4; ++i)
+                if ((gone >> i) & 1) word |= 3u << (2 * i);
+            }
+            bad_ring[steps % kBadRing] = word;
+            mbar_arrive_expect_tx(&full[slot], bytes);
+          }
+          raw_used &= ~(1u << slot);
+          __syncwarp();
+          const int zk = __shfl_sync(kFull, z, j < pages_of_step ? j : 0);
+          if (j < pages_of_step && zk != -2)
+            tma_load_4d(smem + Ly::OFF_RING + slot * Ly::TILE + slab * Ly::Q_SLAB + j * bs * 128, &p.map_k, 0, 0, zk,
+                        slab, &full[slot]);
+          ++c;
+          // ---- V
+          slot = c % R;
+          if (lane == 0) ok = wait(&empty[slot], ((c / R) & 1) ^ 1);
+          ok = __shfl_sync(kFull, ok, 0);
+          if (!ok) break;
+          int x, y;
+          const bool clear = (hi & 15) != 0 || hidden(it.t, t0, hi, x, y);
+          uint64_t* bar = clear ? &raw[slot] : &full[slot];
+          raw_used = clear ? raw_used | 1u << slot : raw_used & ~(1u << slot);
+          if (clear) raw_parity ^= 1u << slot;
+          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+          __syncwarp();
+          if (z >= -1)
+            tma_load_4d(smem + Ly::OFF_RING + slot * Ly::TILE + lane * bs * D * 2, &p.map_v, 0, 0, z, 0, bar);
+          ++c;
         }
-        at.next();
-        for (int v = 0; v < steps; ++v) {
-          Slot kn = at;                                    // V of this step; K of the next
-          kn.next();
-          const bool next = v + 1 < steps;
-          const uint32_t v_lo = uniform(v_lo0 + at.i * (Ly::TILE >> 4));
-          ok = wait(&full[at.i], at.parity) && (v > 0 || wait(&o_free[half], o_parity)) && my_turn() &&
-               wait(&p_full[half], p_parity);
-          tmem_fence_after();
-          values(v_lo, next ? kPrefillKeys : tail, v > 0 ? 1u : 0u);
-          if (next) ok = ok && wait(&full[kn.i], kn.parity);
+      }
+      if (!ok && lane == 0) fail();
+      // the copies still in flight must land before the shared memory is released
+      if (lane == 0) {
+        for (uint32_t i = c > R ? c - R : 0; i < c; ++i) {
+          const int slot = i % R;
+          if ((raw_used >> slot) & 1) mbar_wait(&raw[slot], ((raw_parity >> slot) & 1) ^ 1);
+          else mbar_wait(&full[slot], (i / R) & 1);
+        }
+        if (items_done > 0) mbar_wait(q_full, (items_done - 1) & 1);
+      }
+    } else if (warp == kCleaner) {
+      // ------------------------------------------------------------ V rows that nobody sees
+      uint32_t c = 0, raw_parity = 0;
+      bool ok = true;
+      while (ok && walk.next(it)) {
+        if (it.t.steps <= 0) continue;
+        for (int v = it.v0; v < it.v1 && ok; ++v, c += 2) {
+          const int slot = (c + 1) % R;
+          const int t0 = (v + (v >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys, hi = min(it.t.end, t0 + kPrefillKeys);
+          int x, y;
+          const bool behind = hidden(it.t, t0, hi, x, y);
+          if ((hi & 15) == 0 && !behind) continue;
+          ok = wait(&raw[slot], (raw_parity >> slot) & 1);
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+          raw_parity ^= 1u << slot;
+          const uint32_t base = smem_addr(smem + Ly::OFF_RING + slot * Ly::TILE);
+          const int bs = p.block_size;
+          auto clear = [&](int from, int to) {
+            for (int i = lane; i < (to - from) * (D / 8); i += 32) {
+              const int t = from + i / (D / 8), ch = i % (D / 8), page = t >> p.block_log2, r = t & (bs - 1);
+              const uint32_t a = base + page * bs * D * 2 + (ch >> 3) * bs * 128 + r * 128 + (ch & 7) * 16;
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
+            }
+          };
+          clear(hi - t0, (hi - t0 + 15) & ~15);
+          if (behind) clear(x - t0, y - t0);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[slot]);
+        }
+      }
+      if (!ok && lane == 0) fail();
+    } else if (warp == kIssuer || warp == kIssuer + kIssuerStep) {
+      // ------------------------------------------------------------ products: a warp for each half
+      // (What is done between two products is not hidden behind them: the queue is short.  So
+      // there are two issuers, slots are counted up instead of divided, descriptors differ from
+      // ready ones by an addition.  The warp runs as one and a lane of it issues, with values
+      // that the compiler knows to be the warp's: they stay in uniform registers.)
+      {
+        const int half = warp == kIssuer ? 0 : 1;
+        const bool issues = elect_lane();
+        const uint32_t ring = smem_addr(smem + Ly::OFF_RING);
+        constexpr uint32_t kIdS = umma_idesc_bf16(128, kPrefillKeys, false), kIdPV = umma_idesc_bf16(128, D, true);
+        const uint64_t qd0 = umma_desc(smem_addr(smem) + half * Ly::Q_HALF, 16, 1024);
+        const uint64_t kd0 = umma_desc(ring, 16, 1024), vd0 = umma_desc(ring, p.block_size * 128, 1024);
+        const uint32_t q_lo = uniform(static_cast<uint32_t>(qd0)), sbo = static_cast<uint32_t>(kd0 >> 32);
+        const uint32_t k_lo0 = uniform(static_cast<uint32_t>(kd0)), v_lo0 = uniform(static_cast<uint32_t>(vd0));
+        const uint32_t s_at = uniform(tmem + 128 * half), o_at = uniform(tmem + kTmemO + 128 * half);
+        // from 16 keys to the next within V's tile: bs 16, a page; bs 32, 16 rows and then a page
+        const uint32_t v_odd = (p.block_size == 16 ? 16 * D * 2 : 16 * 128) >> 4, v_even = (2 * 16 * D * 2) >> 4;
+        struct Slot {
+          uint32_t i, parity;
+          __device__ __forceinline__ void next() {
+            if (++i == R) {
+              i = 0;
+              parity ^= 1;
+            }
+          }
+        } at{0, 0};
+        uint32_t p_parity = 0, o_parity = 1, q_parity = 0, t_parity = half ^ 1;
+        bool ok = true;
+        // (the lanes agree on giving up, once a step: a vote takes as long as the wait before it)
+        auto agreed = [&] { return ok = __all_sync(kFull, ok) != 0; };
+        // S = this half's rows of q times the K tile in `slot`
+        auto scores = [&](uint32_t slot, uint32_t id) {
+          const uint32_t k_lo = uniform(k_lo0 + slot * (Ly::TILE >> 4));
+          if (issues && ok) {
+  #pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = ((ks >> 2) * Ly::Q_SLAB + (ks & 3) * 32) >> 4;
+              umma_bf16(s_at, desc_of(q_lo + off, sbo), desc_of(k_lo + off, sbo), id, ks > 0 ? 1u : 0u);
+            }
+            umma_commit(&s_full[half]);
+          }
+          __syncwarp();
+        };
+        // O += the weights times the V tile in `slot`
+        auto values = [&](uint32_t v_lo, int keys, uint32_t accumulate) {
+          if (issues && ok) {
+            if (keys == kPrefillKeys) {
+  #pragma unroll
+              for (int g = 0; g < kPrefillKeys / 16; ++g)
+                umma_bf16_ts(o_at, s_at + 8 * g, desc_of(v_lo + (g >> 1) * v_even + (g & 1) * v_odd, sbo), kIdPV,
+                             g > 0 ? 1u : accumulate);
+            } else {
+              for (int g = 0; 16 * g < keys; ++g)
+                umma_bf16_ts(o_at, s_at + 8 * g, desc_of(v_lo + (g >> 1) * v_even + (g & 1) * v_odd, sbo), kIdPV,
+                             g > 0 ? 1u : accumulate);
+            }
+            umma_commit(&pv_done[half]);
+          }
+          __syncwarp();
+        };
+        while (ok && walk.next(it)) {
+          if (it.t.steps <= 0) continue;
+          const int steps = it.v1 - it.v0;
+          const bool two = (it.t.tokens << p.group_log2) > 128;
+          // Products in turns, a step's of one half and then of the other: both halves' at once
+          // would end, and their softmaxes begin, together, with the tensor cores idle meanwhile.
+          auto my_turn = [&] {
+            if (!two) return true;
+            const bool mine = wait(&turn[half], t_parity);
+            t_parity ^= 1;
+            return mine;
+          };
+          auto pass_turn = [&] {
+            if (two && issues) mbar_arrive(&turn[half ^ 1]);
+          };
+          if (half == 1 && !two) {
+            // no rows for this half: the slots are given back as they come
+            for (int i = 0; i < 2 * steps && ok; ++i) {
+              ok = wait(&full[at.i], at.parity);
+              if (agreed() && issues) mbar_arrive(&empty[at.i]);
+              at.next();
+            }
+            if (ok) {
+              ok = wait(q_full, q_parity);
+              if (agreed() && issues) mbar_arrive(q_empty);
+            }
+            q_parity ^= 1;
+            continue;
+          }
+          // (the last step is the only one that may be short)
+          const int tail = min(kPrefillKeys, it.t.end - (it.v1 - 1 + (it.v1 - 1 >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys);
+          const uint32_t id_tail = umma_idesc_bf16(128, (tail + 15) & ~15, false);
+          ok = wait(q_full, q_parity) && wait(&full[at.i], at.parity) && my_turn();
           if (!agreed()) break;
-          // (S goes where the weights stand that the product before reads: the tensor cores
-          // take one thread's products in their order)
-          if (next) scores(kn.i, v + 2 == steps ? id_tail : kIdS);
+          q_parity ^= 1;
+          tmem_fence_after();
+          scores(at.i, steps == 1 ? id_tail : kIdS);
           pass_turn();
           if (issues) {
             umma_commit(&empty[at.i]);
-            if (next) umma_commit(&empty[kn.i]);
-            if (v + 2 == steps) umma_commit(q_empty);
+            if (steps == 1) umma_commit(q_empty);
           }
-          p_parity ^= 1;
-          at = kn;
-          if (next) at.next();
+          at.next();
+          for (int v = 0; v < steps; ++v) {
+            Slot kn = at;                                    // V of this step; K of the next
+            kn.next();
+            const bool next = v + 1 < steps;
+            const uint32_t v_lo = uniform(v_lo0 + at.i * (Ly::TILE >> 4));
+            ok = wait(&full[at.i], at.parity) && (v > 0 || wait(&o_free[half], o_parity)) && my_turn() &&
+                 wait(&p_full[half], p_parity);
+            tmem_fence_after();
+            values(v_lo, next ? kPrefillKeys : tail, v > 0 ? 1u : 0u);
+            if (next) ok = ok && wait(&full[kn.i], kn.parity);
+            if (!agreed()) break;
+            // (S goes where the weights stand that the product before reads: the tensor cores
+            // take one thread's products in their order)
+            if (next) scores(kn.i, v + 2 == steps ? id_tail : kIdS);
+            pass_turn();
+            if (issues) {
+              umma_commit(&empty[at.i]);
+              if (next) umma_commit(&empty[kn.i]);
+              if (v + 2 == steps) umma_commit(q_empty);
+            }
+            p_parity ^= 1;
+            at = kn;
+            if (next) at.next();
+          }
+          o_parity ^= 1;
         }
-        o_parity ^= 1;
+        if (!ok && issues) fail();
+        // nothing may be in flight when the columns are released
+        if (issues) {
+          umma_commit(end);
+          mbar_wait(end, 0);
+        }
+        __syncwarp();
       }
-      if (!ok && issues) fail();
-      // nothing may be in flight when the columns are released
-      if (issues) {
-        umma_commit(end);
-        mbar_wait(end, 0);
-      }
-      __syncwarp();
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ------------------------------------------------------------ softmax: a row a thread

@@ -4,8 +4,8 @@
 // bytes of a row are read and 256 written.  A thread takes the 16 columns of a scale: 8
 // bytes of codes, a byte, one 32-byte store; eight threads a row, so that a warp writes whole
 // lines (with two 16-byte stores, each in half of every sector, 8 contexts of 1000 to 16384
-// tokens, 419 MB, took 84.1 us; so 66.5, 6.3 TB/s, 92 % of the measured copy rate; 256 pages
-// 6.4 and 3.8; 33 pages 1.9).
+// tokens, 419 MB, took 84.2 us; so 66.4, 6.3 TB/s, 93 % of the measured copy rate; the pages
+// of 256 tokens 6.4 and 3.7; 33 pages 1.9).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -1,6 +1,7 @@
 // Append with rotary positions: q and k rotated on the way, k and v written into
 // their slots of the paged pools -- pools of the inputs' own type, e4m3 pools with
-// a fixed scale per kv head, and e4m3 pools with a scale for each page and head.
+// a fixed scale per kv head, e4m3 pools with a scale for each page and head, and pools of
+// 4-bit rows.
 //
 // Rotation of a pair (a, b) of a head's row at the token's position, in float32:
 //   a' = a cos - b sin,   b' = b cos + a sin
@@ -13,7 +14,8 @@
 // (6.78 TB/s copied), 32 query and 8 kv heads of 128, bf16: 16384 tokens, 409 MB, in 61.6 us
 // (6.64 TB/s); 256 tokens in 2.3 us, one in 1.7 (the kernel's start); into page-scaled e4m3
 // pools 8190 tokens, 188 MB, in 31.8 us (5.9 TB/s), 256 single tokens in 3.7 us; into pools
-// with a fixed scale per head, 16384 tokens, 378 MB, in 81.7 us (4.6 TB/s): divisions.
+// with a fixed scale per head, 16384 tokens, 378 MB, in 81.7 us (4.6 TB/s): divisions;
+// into 4-bit rows 8190 tokens in 33.8 us, of which the issue slots are 59 % busy, and 256 in 2.6.
 // A lane holds the two 16-byte chunks of a row that rotate into each other, and a
 // thread takes the same chunks of several heads of one token, so that the table
 // row (4 bytes per rotated column, twice what a bf16 row is) is loaded once for
