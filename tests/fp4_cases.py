@@ -6,6 +6,15 @@ from rope_cases import Append, values
 from span_cases import Decode
 
 
+def shifted(x, nbytes):
+    """A copy of tensor x that begins nbytes behind a multiple of 256 bytes."""
+    raw = x.new_empty(x.numel() + (nbytes + 256) // x.element_size())
+    skip = (-raw.data_ptr() % 256 + nbytes) // x.element_size()
+    y = raw[skip:skip + x.numel()].view(x.shape).copy_(x)
+    assert y.data_ptr() % 256 == nbytes and y.is_contiguous()
+    return y
+
+
 def pool(r, nb, hkv, bs):
     """Random rows of different sizes, as they are stored."""
     x = r.standard_normal((nb, hkv, bs, 128)) * 2.0 ** r.integers(-6, 7, (nb, hkv, bs, 1))

@@ -6,7 +6,7 @@ import torch
 
 import oracle
 import paged_kv_cache_190_gb300 as pa
-from fp4_cases import Append4, Decode4, pool
+from fp4_cases import Append4, Decode4, pool, shifted
 from gpu_helpers import DEV, out_as_f64, to_dev
 from rope_cases import storage, values
 
@@ -127,6 +127,33 @@ def test_read_pages(hkv, bs, pairs):
         want = np.full((60, hkv, bs, 128), 7.0)
         want[p[:, 1]] = oracle.unpack_rows(c[p[:, 0]])
         np.testing.assert_array_equal(got.double().cpu().numpy(), want)
+
+
+def test_buffers_aligned_to_no_more_than_asked():
+    c = Append4(21, 45, 8, 2, 128, 16, 5)
+    dv = DevAppend(c)
+    dv.kc, dv.vc, dv.q_out = (shifted(x, 16) for x in (dv.kc, dv.vc, dv.q_out))
+    assert dv.call() == 0
+    check_append(c, dv)
+    # read back: destinations on 32 bytes, on 16 refused
+    pairs = to_dev(np.array([[0, 1], [3, 0]]))
+    blank = torch.full((2, 2, 16, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    ko, vo = shifted(blank, 32), shifted(blank, 32)
+    pa.pa_read_pages_fp4(ko, vo, dv.kc, dv.vc, pairs, device_errors=dv.errs)
+    assert pa.pa_read_device_errors(dv.errs) == 0
+    for got, pool_ in ((ko, dv.kc), (vo, dv.vc)):
+        want = oracle.unpack_rows(pool_.cpu().numpy()[[3, 0]])
+        np.testing.assert_array_equal(got.double().cpu().numpy(), want)
+    for outs in ((shifted(blank, 16), vo), (ko, shifted(blank, 16))):
+        with pytest.raises(pa.PaError, match="pa_read_pages_fp4"):
+            pa.pa_read_pages_fp4(*outs, dv.kc, dv.vc, pairs, device_errors=dv.errs)
+    # decode
+    c = Decode4(22, [1, 40, 300], 1, 8, 2, 16, spread=3)
+    dv = Dev(c)
+    dv.q, dv.kc, dv.vc, dv.out = (shifted(x, 16) for x in (dv.q, dv.kc, dv.vc, dv.out))
+    dv.call()
+    assert dv.errors() == 0
+    check(c, dv.out)
 
 
 def test_read_all_codes_under_all_scales():

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import paged_kv_cache_190_gb300 as pa
+from fp4_cases import shifted
 from gpu_helpers import DEV, out_as_f64, to_dev
 from prefill_cases import Prompts
 from rope_cases import storage, values
@@ -113,6 +114,16 @@ def test_prompts_that_fill_the_gpu(dtype, hq, hkv, d, bs):
     """Several rounds of items of every length, the last of them incomplete."""
     c = Prompts(7, dtype, [2300, 500, 1800, 64, 1], [0, 700, 100, 64, 900], hq, hkv, d, bs)
     dv = Dev(c)
+    dv.call()
+    assert dv.errors() == 0
+    check(c, dv.out)
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d,bs", [("bf16", 8, 2, 128, 16), ("bf16", 4, 2, 64, 32), ("f32", 4, 2, 64, 16)])
+def test_buffers_aligned_to_no_more_than_16_bytes(dtype, hq, hkv, d, bs):
+    c = Prompts(12, dtype, [140, 3, 70], [0, 50, 200], hq, hkv, d, bs)
+    dv = Dev(c)
+    dv.q, dv.kc, dv.vc, dv.out = (shifted(x, 16) for x in (dv.q, dv.kc, dv.vc, dv.out))
     dv.call()
     assert dv.errors() == 0
     check(c, dv.out)
