@@ -10,8 +10,8 @@
 // memory are 16 bytes longer than D floats, so that 8 keys' 16 bytes fall on all banks.  The
 // next step's keys are copied while this one's are worked on.  Tiles of 32 rows where 64 would
 // leave SMs without one: a call then ends with its longest sequence (5 prompts of 17 to 200
-// tokens behind up to 100, 8 heads of 64: 22.9 us; tiles of 64 rows, their keys copied when
-// they are needed, 32.8).
+// tokens behind up to 100, 8 heads of 64: 23.0 us; tiles of 64 rows 31.9, and 32.8 with
+// their keys copied when they are needed).
 #include <cuda_runtime.h>
 
 #include <atomic>
