@@ -54,6 +54,9 @@ __device__ __forceinline__ int block_before(int x, int* sums, int& all) {
 // One block: the tiles of all sequences, sorted by how many steps they take (a counting
 // sort over 256 lengths), the longest first: dealt out in turns they then end together.
 //   header: [0] tiles, [1] whether there are shares
+// Starts that decrease let sequences claim the same rows, and so more tiles than the rows have:
+// such a call is left out (its tiles in all may pass 31 bits, and this block would list them for
+// minutes).  Starts that do not decrease never come to more than p.room.
 // Whole items are dealt out in rounds.  Where the busiest CTA would take kShareCost steps more
 // than its part that way, the items of the last, incomplete round are laid end to end and each
 // CTA takes a run of them that makes up for what it has less than the others; an item that a
@@ -69,6 +72,7 @@ constexpr int kLeastShare = 4;                             // steps: less is not
 template <int KEYS, int THREADS>
 __global__ void __launch_bounds__(THREADS) prefill_plan_kernel(const PrefillParams p, int tile_rows) {
   __shared__ int most, count[kPlanBuckets], next[kPlanBuckets], sums[THREADS / 32], busiest;
+  __shared__ unsigned long long claimed;                   // tiles of all sequences
   __shared__ int item_from[THREADS];
   __shared__ PrefillSeq seqs[kPlanSeqs];
   __shared__ int2 unsorted[kPlanTiles];
@@ -76,12 +80,16 @@ __global__ void __launch_bounds__(THREADS) prefill_plan_kernel(const PrefillPara
   allow_next_grid();
   const int me = threadIdx.x, warp = me >> 5, lane = me & 31;
   const int tokens = tile_rows >> p.group_log2;
-  if (me == 0) most = 1;
+  if (me == 0) {
+    most = 1;
+    claimed = 0;
+  }
   if (me < kPlanBuckets) count[me] = 0;
   wait_prior_grids();
   __syncthreads();
   bool bad = false;
   int longest = 1;
+  unsigned long long claims = 0;
   for (int b = me; b < p.num_seqs; b += THREADS) {
     const int a = p.starts[b], e = p.starts[b + 1], len = p.lens[b];
     const PrefillSeq s = prefill_seq(p, a, e, len);
@@ -89,12 +97,23 @@ __global__ void __launch_bounds__(THREADS) prefill_plan_kernel(const PrefillPara
     bad |= a < 0 || e < a || e > p.num_tokens || len < 0 || len > p.max_len || s.n > s.len;
     // (a sequence's last tile has the most steps, but for one more at a window's border)
     if (s.n > 0) longest = max(longest, prefill_tile<KEYS>(p, s, (s.n - 1) / tokens, tokens).steps);
+    claims += static_cast<unsigned long long>((s.n + tokens - 1) / tokens);
   }
   if (bad) report(p.device_errors, PA_DEVERR_BAD_LENGTH);
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-  if (lane == 0) atomicMax(&most, longest);
+  for (int o = 1; o < 32; o <<= 1) {
+    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    claims += __shfl_xor_sync(0xffffffffu, claims, o);
+  }
+  if (lane == 0) {
+    atomicMax(&most, longest);
+    atomicAdd(&claimed, claims);
+  }
   __syncthreads();
+  if (claimed > static_cast<unsigned long long>(p.room)) {
+    if (me < 2) p.header[me] = 0;
+    return;
+  }
   const float buckets = static_cast<float>(kPlanBuckets - 1) / static_cast<float>(most);
   auto bucket = [&](int steps) { return kPlanBuckets - 1 - min(kPlanBuckets - 1, static_cast<int>(static_cast<float>(steps) * buckets)); };
   auto tiles_do = [&](auto f) {                            // f(sequence, tile, steps) for all tiles
@@ -105,23 +124,22 @@ __global__ void __launch_bounds__(THREADS) prefill_plan_kernel(const PrefillPara
   };
   tiles_do([&](int, int, int steps) { atomicAdd(&count[bucket(steps)], 1); });
   __syncthreads();
-  int all;
-  const int before = block_before<THREADS>(me < kPlanBuckets ? count[me] : 0, sums, all);   // where each bucket begins
+  int tiles;
+  const int before = block_before<THREADS>(me < kPlanBuckets ? count[me] : 0, sums, tiles);   // where each bucket begins
   if (me < kPlanBuckets) next[me] = before;
-  const int tiles = min(all, p.room);                      // (room enough but for q_starts that decrease)
   if (me == 0) p.header[0] = tiles;
   __syncthreads();
-  const bool here = all <= kPlanTiles && all <= p.room;
+  const bool here = tiles <= kPlanTiles;
   tiles_do([&](int b, int t, int steps) {
     const int at = atomicAdd(&next[bucket(steps)], 1);
     if (here) unsorted[at] = make_int2(b, t);
-    else if (at < p.room) p.tiles[at] = make_int4(b, t, max(1, steps), 0);
+    else p.tiles[at] = make_int4(b, t, max(1, steps), 0);
   });
   __syncthreads();
   // (which of the tiles of a bucket came first is chance, and shares cut items by their place:
   // in the order of their numbers, so that a call's result is always the same)
   if (here)
-    for (int i = me; i < all; i += THREADS) {
+    for (int i = me; i < tiles; i += THREADS) {
       const int2 x = unsorted[i];
       const PrefillSeq s = x.x < kPlanSeqs ? seqs[x.x] : prefill_seq(p, x.x);
       const int steps = prefill_tile<KEYS>(p, s, x.y, tokens).steps;

@@ -1,0 +1,55 @@
+"""The prompt attention where calls are refused, cut short or very long: starts that make
+sequences claim each other's rows, data errors in any sequence, waits that expire and waits
+that rightly take long."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_190_gb300 as pa
+from gpu_helpers import DEV
+from prefill_cases import Prompts
+from test_gpu_prefill import Dev, check
+
+pytestmark = pytest.mark.gpu
+
+
+def _swinging(tokens, seqs):
+    """0, T, 0, T, ...: each other sequence claims every row, the ones between decrease."""
+    return torch.arange(seqs + 1, dtype=torch.int32, device=DEV) % 2 * tokens
+
+
+# (type, query heads of the one kv head, head_dim, rows of a tile, tokens, sequences)
+CLAIMS = [("bf16", 8, 64, 256, 600, 400), ("f32", 8, 64, 64, 900, 700), ("bf16", 1, 128, 256, 90, 3000),
+          ("bf16", 8, 64, 256, 371000, 371001), ("f32", 8, 64, 64, 186000, 186001)]
+
+
+@pytest.mark.parametrize("dtype,hq,d,rows,tokens,seqs", CLAIMS)
+def test_starts_that_claim_more_tiles_than_there_are_rows(dtype, hq, d, rows, tokens, seqs):
+    """Reported, however many tiles the sequences claim together (the last two cases: more than
+    31 bits), and rows are left as they were or are one of their sequences' (zeros, as the
+    pools are)."""
+    claimed = (seqs + 1) // 2 * -(-tokens * hq // rows)
+    assert tokens < 100000 or claimed > 2 ** 31 - 1
+    tdt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q = torch.zeros(tokens, hq, d, dtype=tdt, device=DEV)
+    out = torch.full_like(q, 7.0)
+    pools = [torch.zeros(2, 1, 16, d, dtype=tdt, device=DEV) for _ in range(2)]
+    tables = torch.zeros(seqs, 1, dtype=torch.int32, device=DEV)
+    lens = torch.full((seqs,), 16, dtype=torch.int32, device=DEV)
+    errs = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pa.pa_prefill(out, q, *pools, tables, lens, _swinging(tokens, seqs), d ** -0.5, 1, 16, device_errors=errs)
+    assert pa.pa_read_device_errors(errs) == pa.PA_DEVERR_BAD_LENGTH
+    assert bool(((out == 7.0) | (out == 0.0)).all())
+
+
+def test_swinging_starts_leave_the_workspace_usable():
+    c = Prompts(70, "bf16", [40, 3, 300, 20], [0, 900, 10, 0], 8, 2, 128, 16)
+    ws = torch.empty(pa.pa_prefill_workspace_size(c.rows, 400, 8, 2, 128), dtype=torch.uint8, device=DEV)
+    dv = Dev(c)
+    pa.pa_prefill(dv.out, dv.q, dv.kc, dv.vc, dv.tables[:1].repeat(400, 1), dv.lens[:1].repeat(400), _swinging(c.rows, 400),
+                  c.scale, c.hkv, int(c.lens.max()), workspace=ws, device_errors=dv.errs)
+    assert dv.errors() == pa.PA_DEVERR_BAD_LENGTH
+    dv.out.fill_(7.0)
+    dv.call(workspace=ws)
+    assert dv.errors() == 0
+    check(c, dv.out)
