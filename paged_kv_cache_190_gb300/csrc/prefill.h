@@ -84,6 +84,11 @@ __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillParams& p, int a,
 __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillParams& p, int b) {
   return prefill_seq(p, p.starts[b], p.starts[b + 1], p.lens[b]);
 }
+// Is a start, a length, or that there are fewer tokens than new ones an error of the data?
+__device__ __forceinline__ bool prefill_bad(const PrefillParams& p, int a, int e, int len) {
+  return a < 0 || e < a || e > p.num_tokens || len < 0 || len > p.max_len ||
+         prefill_seq(p, a, e, len).n > prefill_seq(p, a, e, len).len;
+}
 
 // What a tile of rows has to read: keys [0, end) without those that no row sees, as a list
 // of steps of KEYS keys; step v starts at key (v + (v >= ns ? shift : 0)) * KEYS.
@@ -136,18 +141,23 @@ struct PrefillWalk {
     left = p.header[1] ? -1 : 0;
     rounds = left ? items / static_cast<int>(gridDim.x) : 1 << 30;
   }
-  // The CTA's only item, found by each warp from the sequences' starts.
+  // What is wrong with sequence b's data, if anything is, goes to the caller's error word.
+  __device__ __forceinline__ void look_at(int b) const {
+    const int a = p.starts[b], e2 = p.starts[b + 1], len = p.lens[b];
+    if (prefill_bad(p, a, e2, len)) report(p.device_errors, PA_DEVERR_BAD_LENGTH);
+  }
+  // The CTA's only item, found by each warp from the sequences' starts.  One warp of the first
+  // CTA looks at every sequence's data, those behind its own item's too.
   __device__ __forceinline__ bool own(PrefillItem& it) {
     if (k++ > 0) return false;
     const int lane = threadIdx.x & 31, tile = blockIdx.x / p.num_kv_heads;
+    const bool looks = blockIdx.x == 0 && threadIdx.x < 32;
     int before = 0;
     for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
       PrefillSeq s{0, 0, 0};
       if (b0 + lane < p.num_seqs) {
-        const int a = p.starts[b0 + lane], e2 = p.starts[b0 + lane + 1], len = p.lens[b0 + lane];
-        s = prefill_seq(p, a, e2, len);
-        if (blockIdx.x == 0 && threadIdx.x < 32 && (a < 0 || e2 < a || e2 > p.num_tokens || len < 0 || len > p.max_len || s.n > s.len))
-          report(p.device_errors, PA_DEVERR_BAD_LENGTH);
+        s = prefill_seq(p, b0 + lane);
+        if (looks) look_at(b0 + lane);
       }
       const int nt = (s.n + tile_tokens - 1) / tile_tokens;
       int x = nt;
@@ -169,6 +179,8 @@ struct PrefillWalk {
         it.t = prefill_tile<KEYS>(p, s, t, tile_tokens);
         it.v0 = 0;
         it.v1 = max(1, it.t.steps);
+        if (looks)
+          for (int b = b0 + 32 + lane; b < p.num_seqs; b += 32) look_at(b);
         return true;
       }
       before += __shfl_sync(0xffffffffu, x, 31);

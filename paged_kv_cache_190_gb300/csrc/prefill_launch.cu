@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(THREADS) prefill_plan_kernel(const PrefillPara
     const int a = p.starts[b], e = p.starts[b + 1], len = p.lens[b];
     const PrefillSeq s = prefill_seq(p, a, e, len);
     if (b < kPlanSeqs) seqs[b] = s;
-    bad |= a < 0 || e < a || e > p.num_tokens || len < 0 || len > p.max_len || s.n > s.len;
+    bad |= prefill_bad(p, a, e, len);
     // (a sequence's last tile has the most steps, but for one more at a window's border)
     if (s.n > 0) longest = max(longest, prefill_tile<KEYS>(p, s, (s.n - 1) / tokens, tokens).steps);
     claims += static_cast<unsigned long long>((s.n + tokens - 1) / tokens);

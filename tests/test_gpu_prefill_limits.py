@@ -53,3 +53,42 @@ def test_swinging_starts_leave_the_workspace_usable():
     dv.call(workspace=ws)
     assert dv.errors() == 0
     check(c, dv.out)
+
+
+# ------------------------------------------------- data errors without a plan
+def _single(seed, dtype, seqs, empty=0):
+    """Sequences of one new token each (and `empty` without any) behind a few earlier ones."""
+    r = np.random.default_rng(seed)
+    new = np.concatenate([np.ones(seqs, int), np.zeros(empty, int)])
+    return Prompts(seed, dtype, new, r.integers(0, 30, len(new)), 1, 1, 64, 16, before=1, behind=1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("seqs,empty", [(40, 0), (100, 0), (3, 90), (33, 31)])
+def test_data_errors_in_any_sequence_are_reported(dtype, seqs, empty):
+    """Calls small enough to go without a plan: the last sequence's errors are seen as the
+    first one's are, and the other sequences keep their results."""
+    c = _single(71 + seqs, dtype, seqs, empty)
+    ref = Dev(c)
+    ref.call()
+    assert ref.errors() == 0
+    check(c, ref.out)
+    n, most = len(c.lens), int(c.lens.max())
+    for b in (0, 31, 32, n // 2, n - 1):
+        if b >= n:
+            continue
+        r0, r1 = int(c.starts[b]), int(c.starts[b + 1])
+        others = torch.ones(c.rows, dtype=torch.bool, device=DEV)
+        others[r0:r1] = False
+        for bad in (-1, most + 1) + ((0,) if r1 > r0 else ()):
+            dv = Dev(c)
+            dv.lens[b] = bad
+            dv.call(max_context_len=most)
+            # (a length that is clamped reaches table entries that are no pages)
+            assert dv.errors() & pa.PA_DEVERR_BAD_LENGTH, f"length {bad} of sequence {b}"
+            assert torch.equal(dv.out[others], ref.out[others])
+    for start in (c.rows + 1, int(c.starts[-2]) - 1):
+        dv = Dev(c)
+        dv.starts[-1] = start
+        dv.call()
+        assert dv.errors() == pa.PA_DEVERR_BAD_LENGTH, f"last start {start}"
