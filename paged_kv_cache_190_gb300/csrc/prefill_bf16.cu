@@ -123,6 +123,34 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // The lowest n bits of a word, n of any size.
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
 
+// The ring's words, one for each of the last kBadRing steps: the step's number, from 1, and below it
+// a bit for each 16 of its keys whose page is none.  Their sum says whether the ring has moved on.
+constexpr uint32_t kBadKeys = 0xff;
+constexpr int kStepBits = 24;
+__device__ __forceinline__ uint32_t ring_sum(const volatile uint32_t* words) {
+  uint32_t x = 0;
+  for (int i = 0; i < kBadRing; ++i) x += words[i];
+  return x;
+}
+
+// Two kinds of waits may rightly last as long as whole items take: the clearing warp's, and those of
+// the second half's softmax behind items that have no rows for it.  They are given up after `limit`
+// polls in which the ring has not moved on; it moves as often as there are steps, so they end.
+// This one: until step number `step` has begun, or `bar` has completed the phase.  (Not inlined, for
+// the registers of the softmax loop beside it; and every wait this way would cost 2 to 4 %.)
+__device__ __noinline__ void follow_ring(const volatile uint32_t* words, uint32_t step, uint64_t* bar, uint32_t parity,
+                                         volatile int* abort_flag, uint32_t limit) {
+  uint32_t seen = 0;
+  for (uint32_t polls = 0; polls < limit && !*abort_flag; ++polls) {
+    // (numbers are compared modulo 2^24)
+    const uint32_t ahead = (words[(step - 1) % kBadRing] >> (32 - kStepBits)) - step;
+    if (static_cast<int32_t>(ahead << (32 - kStepBits)) >= 0 || mbar_try_wait(bar, parity)) return;
+    const uint32_t now = ring_sum(words);
+    if (now != seen) polls = 0;
+    seen = now;
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const __grid_constant__ PrefillParams p) {
   using Ly = PrefillLayout<D>;
@@ -168,6 +196,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
     }
     mbar_init(end, 2);
     *abort_flag = 0;
+    for (int i = 0; i < kBadRing; ++i) bad_ring[i] = 0;
     fence_mbar_init();
   }
   if (warp == kIssuer) {
@@ -192,6 +221,14 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     // (the flag is not looked at where the first poll says yes, as it nearly always does)
     return mbar_try_wait(bar, parity) || (!*abort_flag && mbar_wait(bar, parity, p.wait_limit));
+  };
+  auto patient_wait = [&](uint64_t* bar, uint32_t parity) {   // (see follow_ring)
+    for (uint32_t seen = ring_sum(bad_ring);;) {
+      if (wait(bar, parity)) return true;
+      const uint32_t now = ring_sum(bad_ring);
+      if (now == seen || *abort_flag) return false;
+      seen = now;
+    }
   };
   PrefillWalk<kPrefillKeys> walk(p, tile_tokens);
   PrefillItem it;
@@ -259,7 +296,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
               for (int i = 0; i < 4; ++i)
                 if ((gone >> i) & 1) word |= 3u << (2 * i);
             }
-            bad_ring[steps % kBadRing] = word;
+            bad_ring[steps % kBadRing] = ((steps + 1) << (32 - kStepBits)) | word;
             mbar_arrive_expect_tx(&full[slot], bytes);
           }
           raw_used &= ~(1u << slot);
@@ -308,7 +345,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
           int x, y;
           const bool behind = hidden(it.t, t0, hi, x, y);
           if ((hi & 15) == 0 && !behind) continue;
-          ok = wait(&raw[slot], (raw_parity >> slot) & 1);
+          ok = patient_wait(&raw[slot], (raw_parity >> slot) & 1);
           ok = __all_sync(kFull, ok);
           if (!ok) break;
           raw_parity ^= 1u << slot;
@@ -482,6 +519,8 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
       const PrefillTile& t = it.t;
       if (half == 1 && (t.tokens << p.group_log2) <= 128) {
         steps += t.steps > 0 ? it.v1 - it.v0 : 0;
+        // (whether the ring stands still is a later wait's to say)
+        if (t.steps > 0) follow_ring(bad_ring, steps, &s_full[1], n & 1, abort_flag, p.wait_limit);
         continue;
       }
       const int j = r >> p.group_log2;
@@ -499,7 +538,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
         float s[128];
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s + 32 * i);
-        const uint32_t bad = bad_ring[steps % kBadRing];
+        const uint32_t bad = bad_ring[steps % kBadRing] & kBadKeys;
         tmem_landed(s);
         if (!sees_all || bad != 0) {
           const int last = pos - t0, first = pos - p.window + 1 - t0, sinks = p.sinks - t0;

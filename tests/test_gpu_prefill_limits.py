@@ -92,3 +92,62 @@ def test_data_errors_in_any_sequence_are_reported(dtype, seqs, empty):
         dv.starts[-1] = start
         dv.call()
         assert dv.errors() == pa.PA_DEVERR_BAD_LENGTH, f"last start {start}"
+
+
+# ------------------------------------------------------------------ long waits
+@pytest.fixture
+def wait_limit():
+    yield pa.pa_debug_set_wait_limit
+    pa.pa_debug_set_wait_limit(-1)
+
+
+def _pools(hkv, d, pages, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return [torch.empty(pages, hkv, 16, d, dtype=torch.bfloat16, device=DEV).normal_(generator=g) for _ in range(2)]
+
+
+def _limited(wait_limit, polls, out, *args, **kw):
+    errs = torch.zeros(1, dtype=torch.int32, device=DEV)
+    wait_limit(polls)
+    pa.pa_prefill(out, *args, device_errors=errs, **kw)
+    flags = pa.pa_read_device_errors(errs)
+    wait_limit(-1)
+    return flags
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_short_prompt_behind_a_long_document(d, wait_limit):
+    """The document's length is aligned, so no V row of it has to be cleared until the short
+    prompt's turn comes, milliseconds later.  64 polls are about 0.24 ms: more than any single
+    step takes, less than the document."""
+    T, short, h = 65536, 20, 8
+    k, v = _pools(h, d, T // 16 + 2, 74)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    table = torch.full((2, T // 16), -1, dtype=torch.int32, device=DEV)
+    table[0] = torch.arange(T // 16, device=DEV)
+    table[1, :2] = i32(T // 16, T // 16 + 1)
+    q = torch.randn(T + short, h, d, device=DEV).bfloat16()
+    args = (q, k, v, table, i32(T, short), i32(0, T, T + short), d ** -0.5, h, T)
+    want, got = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+    assert _limited(wait_limit, -1, want, *args) == 0
+    assert _limited(wait_limit, 64, got, *args) == 0
+    assert torch.equal(want.view(torch.int16), got.view(torch.int16))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_halves_without_rows_for_long(d, wait_limit):
+    """Chunks of at most 128 rows leave the second half of an item's rows without work until
+    the whole tiles of a fresh prompt come, which are shorter and so last."""
+    n, chunk, had, fresh, h = 160, 100, 8092, 2048, 8
+    pages = (had + chunk + 15) // 16
+    k, v = _pools(h, d, pages + fresh // 16, 75)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).repeat(n + 1, 1)      # (all chunks behind one context)
+    table[n, :fresh // 16] = pages + torch.arange(fresh // 16, dtype=torch.int32, device=DEV)
+    q = torch.randn(n * chunk + fresh, h, d, device=DEV).bfloat16()
+    args = (q, k, v, table, i32([had + chunk] * n + [fresh]), i32([chunk * i for i in range(n + 1)] + [len(q)]),
+            d ** -0.5, h, had + chunk)
+    want, got = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+    assert _limited(wait_limit, -1, want, *args) == 0
+    assert _limited(wait_limit, 64, got, *args) == 0
+    assert torch.equal(want.view(torch.int16), got.view(torch.int16))
