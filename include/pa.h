@@ -535,12 +535,13 @@ int pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cach
                size_t workspace_bytes, int32_t* device_errors, void* stream);
 
 /*
- * Test hook for the failure path.  Every pipeline wait of the decode kernels
- * enqueued after this call gives up after `polls` polls (0: at once) and
+ * Test hook for the failure path.  Every pipeline wait of the decode kernels and of
+ * pa_prefill's over bf16 pools enqueued after this call gives up after `polls` polls (of
+ * up to 3.76 us each; 0: at once, for a prompt with its first copies in flight) and
  * reports PA_DEVERR_TIMEOUT; the kernel then waits for its own copies in flight
  * (with the normal bound) and returns, leaving the context usable.  polls < 0
- * restores the normal bound (well over a second).  Process-wide; meant for
- * tests, not for concurrent use.
+ * restores the normal bound (15.8 s, of a prompt's waits in which its copies stand still).
+ * Process-wide; meant for tests, not for concurrent use.
  */
 int pa_debug_set_wait_limit(int polls);
 

@@ -173,11 +173,6 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile_tokens = kPrefillRows >> p.group_log2;
-  if (p.wait_limit == 0) {                                 // no wait may succeed: nothing is begun
-    if (threadIdx.x == 0) report(p.device_errors, PA_DEVERR_TIMEOUT);
-    wait_prior_grids();
-    return;
-  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < R; ++i) {
@@ -321,6 +316,12 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
           if (z >= -1)
             tma_load_4d(smem + Ly::OFF_RING + slot * Ly::TILE + lane * bs * D * 2, &p.map_v, 0, 0, z, 0, bar);
           ++c;
+          // (no polls: a wait that expires for certain, with a step's copies in flight.  In the first
+          // poll of every wait the question would cost 2 to 3 %.)
+          if (p.wait_limit == 0) {
+            ok = false;
+            break;
+          }
         }
       }
       if (!ok && lane == 0) fail();
@@ -683,7 +684,10 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[half]);
     }
-    if (!ok && lane == 0) fail();
+    if (!ok) {
+      tmem_wait_st();                                      // the weights of a step given up
+      if (lane == 0) fail();
+    }
   }
   tmem_fence_before();
   __syncthreads();

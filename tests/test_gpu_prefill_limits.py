@@ -151,3 +151,36 @@ def test_halves_without_rows_for_long(d, wait_limit):
     assert _limited(wait_limit, -1, want, *args) == 0
     assert _limited(wait_limit, 64, got, *args) == 0
     assert torch.equal(want.view(torch.int16), got.view(torch.int16))
+
+
+# ---------------------------------------------------------------- expired waits
+@pytest.mark.parametrize("d,bs,new,had,window,sinks", [
+    (128, 16, [600, 33], [0, 900], 0, 0), (128, 32, [20], [0], 0, 0), (128, 16, [130], [20000], 0, 0),
+    (64, 16, [100], [6000], 0, 0), (64, 32, [300, 77, 5], [0, 500, 3000], 100, 20)])
+def test_no_polls_at_all(d, bs, new, had, window, sinks, wait_limit):
+    """With a limit of 0 the kernel gives up with its first copies in flight: reported, and the
+    next call as ever."""
+    c = Prompts(72, "bf16", new, had, 8, 2, d, bs, window, sinks)
+    dv = Dev(c)
+    ws = torch.zeros(pa.pa_prefill_workspace_size(c.rows, len(new), 8, 2, d), dtype=torch.uint8, device=DEV)
+    for _ in range(5):
+        wait_limit(0)
+        for _ in range(3):
+            dv.call(workspace=ws)
+        assert dv.errors() == pa.PA_DEVERR_TIMEOUT
+        wait_limit(-1)
+        dv.out.fill_(7.0)
+        dv.call(workspace=ws)
+        assert dv.errors() == 0
+        check(c, dv.out)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_call_that_waits_for_nothing_expires_nowhere(d, wait_limit):
+    """Rows that see nothing need no copy and no product: they are zeros under any limit."""
+    c = Prompts(73, "bf16", [40, 300], [0, 0], 8, 2, d, 16)
+    dv = Dev(c)
+    dv.lens.zero_()
+    wait_limit(0)
+    dv.call()
+    assert dv.errors() == pa.PA_DEVERR_BAD_LENGTH and bool((dv.out == 0).all())
