@@ -456,7 +456,8 @@ int pa_copy_scales(const float* src_k_scales, const float* src_v_scales, float* 
  * For each 16 columns of k' and of v, amax being their largest magnitude:
  *     scale = the nearest to amax / 6 (float32 division; ties to even; at most 10240),
  *     code = the nearest to x / scale (float32 division, ties to the even code),
- * with magnitudes beyond 6 scale (infinities too) at +-6; scale 0 stores zeros.  A NaN
+ * with magnitudes beyond 6 scale (infinities too) at +-6; scale 0 stores codes 0.  An
+ * element 0 of either sign is code 0, a negative one that rounds to 0 keeps its sign.  A NaN
  * makes the scale, and so its 16 columns, NaN.
  *
  * pa_read_pages_fp4: pages read back in bf16, exactly: for each pair (src, dst) of

@@ -43,7 +43,8 @@ __device__ __forceinline__ float quotient4(float x, float s, float r) {
   return __fmaf_rn(__fmaf_rn(-z, s, x), r, z);
 }
 
-// Eight floats over s as codes: nearest, ties to even, magnitudes above 6 s saturate.
+// Eight floats over s as codes: nearest, ties to even, magnitudes above 6 s saturate.  Zeros have no
+// sign (the remainder's sum is +0), and under a scale of 0 nothing has.
 __device__ __forceinline__ uint32_t codes4_of(const float* x, float s) {
   const float r = s > 0.f ? __frcp_rn(s) : 0.f;
   // (beyond 8 s a code saturates, and an infinity has no remainder: only the largest scale
@@ -61,7 +62,7 @@ __device__ __forceinline__ uint32_t codes4_of(const float* x, float s) {
       "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
       : "=r"(w)
       : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]), "f"(z[4]), "f"(z[5]), "f"(z[6]), "f"(z[7]));
-  return w;
+  return s == 0.f ? 0u : w;
 }
 
 // The eight codes of a word as four pairs of halves, unscaled (the lower column in the
