@@ -153,7 +153,7 @@ int pa_read_pages_fp4(void* k_out, void* v_out, const void* k_cache, const void*
                       int32_t* device_errors, void* stream) {
   if (head_dim != 128 || !shape_ok(head_dim, block_size)) return PA_ERR_UNSUPPORTED;
   if (num_pairs < 0 || num_kv_heads <= 0 || num_src_blocks <= 0 || num_dst_blocks <= 0 ||
-      num_kv_heads > 65536)
+      num_kv_heads > pa::kMostReadRows / block_size)
     return PA_ERR_INVALID_ARG;
   if (num_pairs == 0) return PA_OK;
   if (!k_out || !v_out || !k_cache || !v_cache || !src_dst_pairs) return PA_ERR_INVALID_ARG;

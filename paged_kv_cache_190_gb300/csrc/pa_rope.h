@@ -34,7 +34,9 @@ cudaError_t launch_rope_and_cache(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_copy_scales(const float* src_k, const float* src_v, float* dst_k, float* dst_v,
                                const int64_t* pairs, int num_pairs, int num_kv_heads, int num_src,
                                int num_dst, int32_t* device_errors, cudaStream_t stream);
-// Pages of 4-bit rows as bf16 pages (read_pages.cu).
+// Pages of 4-bit rows as bf16 pages (read_pages.cu).  A grid has 65535 parts of a page at the most.
+constexpr int kReadPartRows = 32;
+constexpr int kMostReadRows = 65535 * kReadPartRows;
 cudaError_t launch_read_pages_fp4(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
                                   const int64_t* pairs, int num_pairs, int page_rows, int num_src,
                                   int num_dst, int32_t* device_errors, cudaStream_t stream);

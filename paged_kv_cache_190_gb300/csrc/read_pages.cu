@@ -20,6 +20,7 @@ namespace {
 constexpr int kReadThreads = 128;
 constexpr int kReadRows = 2;                               // rows of K and of V that a thread has in flight
 constexpr int kBlockRows = kReadThreads / 8 * kReadRows;
+static_assert(kBlockRows == kReadPartRows, "what the host's bound counts");
 
 __device__ __forceinline__ uint32_t bf16x2_of(uint32_t halves) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&halves));
@@ -82,7 +83,6 @@ cudaError_t launch_read_pages_fp4(void* k_out, void* v_out, const void* k_cache,
                                   int num_dst, int32_t* device_errors, cudaStream_t stream) {
   if (num_pairs == 0) return cudaSuccess;
   const int parts = (page_rows + kBlockRows - 1) / kBlockRows;
-  if (parts > 65535) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(num_pairs), static_cast<unsigned>(parts));
   cfg.blockDim = dim3(kReadThreads);
