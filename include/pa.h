@@ -501,7 +501,7 @@ int pa_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_c
  * with window > 0 to those with p - t < window or t < sinks:
  *     out[row][i] = softmax_t(scale q[row][i] . K_t) V_t.
  * q and out are [num_tokens][num_q_heads][head_dim] in the pools' type; head_dim, block_size
- * and group sizes as above; scale positive and finite.  A sequence may have no new token.
+ * and group sizes as above; scale positive, scale log2(e) finite.  A sequence may have no new token.
  * Rows of out before q_starts[0] or from q_starts[num_seqs] on are left as they were; rows
  * that see no token are zeros.  Table entries of pages of which no new token sees a
  * position are not read (a window may have given them back), and what stands in positions

@@ -32,7 +32,7 @@ int pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cach
       max_blocks_per_seq < 0 || max_context_len < 0 || window < 0 || sinks < 0)
     return PA_ERR_INVALID_ARG;
   if (num_q_heads % num_kv_heads != 0 || (window == 0 && sinks > 0)) return PA_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(pa::prefill_scale_log2(scale))) return PA_ERR_INVALID_ARG;
   const int group = num_q_heads / num_kv_heads;
   if (group != 1 && group != 2 && group != 4 && group != 8) return PA_ERR_UNSUPPORTED;
   // (rows and items are numbered in 31 bits)

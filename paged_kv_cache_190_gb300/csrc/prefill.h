@@ -63,6 +63,10 @@ struct PrefillArgs {
   int64_t wait_limit;
 };
 
+// Logits are taken in base 2.
+inline float prefill_scale_log2(float scale) {
+  return static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+}
 size_t prefill_workspace_size(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                               int num_sms);
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);

@@ -327,7 +327,7 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   const int rows = !a.f32 ? kPrefillRows
       : most_tiles(a.num_tokens, a.num_seqs, group, 64) * a.num_kv_heads > 2 * a.num_sms ? 64 : kPrefillRowsF32;
   p.room = static_cast<int>(most_tiles(a.num_tokens, a.num_seqs, group, rows));
-  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  p.scale_log2 = prefill_scale_log2(a.scale);
   p.num_seqs = a.num_seqs;
   p.num_tokens = a.num_tokens;
   p.group = group;
