@@ -524,6 +524,8 @@ int pa_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_c
  *
  * workspace: device scratch of pa_prefill_workspace_size bytes, 256-byte aligned; it
  * carries no state between calls, but two calls in flight at once must not share it.
+ * (Mostly room for the partial results of items that are cut, two for each SM: 40 MB for
+ * heads of 128 from 256 rows of a kv head on, for calls that cut none too.)
  * The results do not depend on what else runs, bit for bit.
  */
 size_t pa_prefill_workspace_size(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads,

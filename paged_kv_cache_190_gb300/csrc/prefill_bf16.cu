@@ -11,11 +11,13 @@
 // What bounds it: the products.  A step of 128 keys for 256 rows of 128 columns is 16.8
 // MFLOP (2048 clocks of the tensor cores), 64 KiB of K and V and 32768 exponentials (1024
 // clocks).  On a GB300 (1990 TFLOP/s of bf16 products measured, 1738 in a long run), 32 query
-// and 8 kv heads of 128: one prompt of 16384 tokens 1323 us, 1660 TFLOP/s of what causality
-// leaves; 12 ragged prompts, 17569 tokens, 231 us, 1240; 6 chunks of 200 to 512 tokens behind
-// up to 15000 248 us, 1290; one prompt of 37 tokens 6.5 us.  Heads of 64 have the same
-// exponentials for half the products: 4 prompts, 12802 tokens of 16 heads, in windows of 1024
-// take 116 us.
+// and 8 kv heads of 128, first in a graph of a few calls and then among calls that keep the GPU
+// busy for longer: one prompt of 16384 tokens 1325 to 1360 us and 1406 to 1440, 1530 to 1660
+// TFLOP/s of what causality leaves; 12 ragged prompts, 17569 tokens, 233 and 241 to 243, 1180 to
+// 1230; 6 chunks of 200 to 512 tokens behind up to 15000 251 and 258 to 261, 1230 to 1280; one
+// prompt of 37 tokens 6.5.  Heads of 64 have the same exponentials for half the products, and
+// their steps take about as long: 4 prompts of 4096 tokens of 16 heads 171 us, 806 TFLOP/s; 4
+// prompts, 12802 tokens, in windows of 1024 117.
 //
 // Layout of the work:
 //   * An item is a kv head and a tile of 256 rows: 256 / G consecutive new tokens of a
@@ -40,8 +42,9 @@
 //     step come to more than 2^16 (bf16 has float32's range, so they may pass 1), so O is
 //     hardly ever rescaled, and the other steps take no maximum: 128 keys of 32 rows cost a
 //     warp alone 750 clocks instead of 1030.
-//   * Every wait is bounded; on expiry the kernel reports PA_DEVERR_TIMEOUT, waits for its
-//     own copies and products, frees its tensor memory and returns.
+//   * Every wait is bounded, by polls or by polls in which the ring stands still; on expiry the
+//     kernel reports PA_DEVERR_TIMEOUT, waits for its own copies and products, frees its tensor
+//     memory and returns.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -235,7 +238,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
   };
 
   // A softmax thread holds a row's 128 scores.  The block has 384 * 168 = 64512 registers:
-  // 256 * 184 + 128 * 136.
+  // 256 * 184 + 128 * 136.  (The compiler allots 168 to all and spills 40 bytes.)
   if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
     if (warp == kProducer) {

@@ -62,7 +62,10 @@ __device__ __forceinline__ int block_before(int x, int* sums, int& all) {
 // CTA takes a run of them that makes up for what it has less than the others; an item that a
 // run's end cuts leaves partial results for prefill_join_kernel (which cost about as much as
 // those steps).  6 chunks behind up to 15000 tokens take 248 us this way, 318 in whole items
-// alone.  (Shares of all items even out no better, and the tiles of one sequence and head,
+// alone; 64 tokens behind 8000 36.7 and 98.7, 12 chunks of 300 behind 3000 168 and 183.  The leave
+// to cut costs the plan and the join where nothing is cut in the end: 20 chunks of 256 behind 1000
+// 105.0, without it 101.8; one prompt of 600 tokens 20.2, and 13.9 where it needs no plan either.
+// (Shares of all items even out no better, and the tiles of one sequence and head,
 // which whole rounds read together, then read their keys from HBM again and again: 1.1 GB
 // and 260 us in the kernel alone where this reads 0.3 GB in 240.)
 constexpr int kShareCost = 12;
@@ -323,7 +326,9 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   p.may_share = !a.f32 && a.max_len > kLeastShare * kPrefillKeys && a.max_len <= kMostShared && least_items <= static_cast<int64_t>(kMostRounds) * a.num_sms &&
                 a.num_sms * kMostRounds <= kPlanTiles;
   // float32: tiles of 64 rows, of 32 where two of those an SM are more than there are (5 short
-  // prompts 23.0 us, with tiles of 64 31.9; a tile of 64 reads its keys half as often)
+  // prompts 23.0 us, with tiles of 64 31.9; a tile of 64 reads its keys half as often).  8 heads of
+  // 64, tiles of 32 and 64: one prompt of 100 tokens 11.0 and 13.9, 10 of 120 20.0 and 21.8, 10 of
+  // 240 46.6 and 41.4, 20 of 240 86.4 and 62.7; 5 of 110, on the wrong side of it, 16.4 and 14.3
   const int rows = !a.f32 ? kPrefillRows
       : most_tiles(a.num_tokens, a.num_seqs, group, 64) * a.num_kv_heads > 2 * a.num_sms ? 64 : kPrefillRowsF32;
   p.room = static_cast<int>(most_tiles(a.num_tokens, a.num_seqs, group, rows));
@@ -369,12 +374,14 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   cfg.numAttrs = 1;
   const int64_t items = most_tiles(a.num_tokens, a.num_seqs, group, rows) * a.num_kv_heads;
   // one item a CTA at most, and none long enough to be cut: each CTA finds its own, without
-  // a plan (37 tokens of one prompt 6.5 us, 9.3 with one)
+  // a plan (37 tokens of one prompt 6.3 us, 9.0 with one; 512 tokens 12.0 and 14.7, 2 of 500 12.5
+  // and 15.4; float32, 4 of 64 19.7 and 22.6)
   p.direct = !p.may_share && items <= (a.f32 ? 2 : 1) * a.num_sms;
   cudaError_t e = cudaSuccess;
   if (!p.direct) {
     // (the steps of a plan are barriers of its block: 251 us against 248 for 6 chunks with 1024
-    // threads; more sequences or tiles want them)
+    // threads, 397 against 381 for 4 prompts of 4096; more sequences or tiles want them, from
+    // fewer on than this: 250 sequences of 20 tokens behind 700 take 188 us here, 181 with 1024)
     const bool small = a.num_seqs <= 256 && most_tiles(a.num_tokens, a.num_seqs, group, rows) <= 1024 && a.num_sms <= 256;
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(small ? 256 : 1024);

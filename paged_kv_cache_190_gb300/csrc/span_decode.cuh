@@ -506,12 +506,15 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 // 4-bit rows (fp4.cuh): a code times its scale is exact as a half, so K and V become halves
 // on the way into mma.sync m16n8k16, two a conversion, and one product of two of them
 // brings the scale in; q and the weights as for e4m3 (the scales differ within a row, so
-// they cannot go into the weights; nor need they, for a half holds the values).  What bounds
-// it is instructions, not bytes: 256 ragged sequences of 8 kv heads, 448 MB, take 107.9 us
-// (66 at the measured copy rate) with 52 % of the issue slots busy and the ALU pipe 40 %; a
-// small call takes 5.5.
-//   * A row of 72 bytes is loaded as it stands, 8 bytes of 16 columns a time: piece p of
-//     rows 4 c + i of 16 tokens falls on banks 8 c + 2 p, a half-warp's on all 32.
+// they cannot go into the weights; nor need they, for a half holds the values).  256 ragged
+// sequences of 8 kv heads, 448 MB, take 107.9 us (66 at the measured copy rate).  What bounds
+// them is not known: 52 % of the issue slots are busy, the ALU pipe 40 %, the tensor pipe 22 %;
+// an SM takes a stage in about 1.35 us, of which its bytes are 0.83 and the instructions of two
+// tiles a scheduler about 0.77.  A small call takes 5.5.
+//   * A row of 72 bytes is loaded as it stands, 8 bytes of 16 columns a time.  V: piece p of
+//     rows 4 c + i of 16 tokens falls on banks 8 c + 2 p, a half-warp's on all 32.  K: a
+//     half-warp has four pieces of rows 0, 1, 4 and 5, on banks 0 to 7, 18 to 25, 8 to 15 and
+//     26 to 1, so one pair of banks twice and one not at all (rows 8, 9, 12 and 13 alike).
 //   * Scores: a lane has pieces c and c + 4 of its tokens' rows; q's columns go with them.
 //   * S^T = K q^T, with the tokens as rows (half the products of Q K^T, which would leave half
 //     of its 16 rows empty); movmatrix turns a tile of weights into P^T's fragment.  Tokens 2 j

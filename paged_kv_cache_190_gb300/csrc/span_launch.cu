@@ -239,7 +239,8 @@ int heads_together(int num_kv_heads, int most) {
 // bytes: e4m3 pages of 16 tokens, 885 MB, take 144 us with 8 heads a box (16 KiB), 152 with
 // 4, 171 with 2, 213 with 1.  bf16 rows are twice as long, and with 2 heads a segment leaves
 // a quarter of the partials: 129.4 us against 132.2 with 8 (833 MB), 49.5 against 52.0
-// (269 MB, 8 rows a head).
+// (269 MB, 8 rows a head).  4-bit rows as e4m3: 256 ragged sequences of up to 8192 tokens 118.4 us
+// with 8 heads, 129.7 with 4, 145.1 with 2, 187.1 with 1.
 bool codes(SpanPool pool) { return pool == SpanPool::kFp8 || pool == SpanPool::kFp4; }
 int share_heads(SpanPool pool, int num_kv_heads) {
   return heads_together(num_kv_heads, codes(pool) ? 8 : 2);
@@ -266,6 +267,10 @@ int ring_stages(SpanPool pool, int head_dim, int rows, int hg, int splits) {
 // 72; bf16: 4 of 4096 10.7 and 13.4, 16 windows of 4096 44.4 and 49.5, 64 of 256 9.9 and 14.2.)
 // Clusters of any size up to 8, not of powers of two alone (e4m3: 10 sequences of 1024 8.8 us
 // in clusters of 3, 9.9 without; 12 of 2048 13.4 in 5s, 14.5; bf16: 10 of 1024 8.9 and 10.3).
+// 4-bit rows take the e4m3 costs by their bytes, which choose between clusters and shares as the
+// clock does but for many tiny sequences (clusters and shares: 1 of 256 5.0 and 7.5, 4 of 1024 6.0
+// and 9.7, 12 of 2048 12.9 and 17.7, 16 of 2048 14.1 and 18.3, 64 of 256 8.9 and 12.8, 64 of 2048
+// to 4096 77.7 and 58.8, 160 of 1000 67.7 and 50.3; 512 of 20 to 40 19.7 and, as chosen, 21.0).
 // float32 rows are computed one by one: with 1, 4 and 8 of them a stage takes 0.93, 1.13 and
 // 1.50 us (one head a CTA), 0.66, 0.87 and 1.35 (8 heads).  Nothing is chosen that leaves the
 // ring a single stage (8 such heads of 8 rows in clusters: 130 us, where 2 stages take 90).
