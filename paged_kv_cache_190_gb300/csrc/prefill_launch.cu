@@ -51,6 +51,13 @@ __device__ __forceinline__ int block_before(int x, int* sums, int& all) {
   return before;
 }
 
+// Sum of a warp's numbers, or `cap` if that is less.
+__device__ __forceinline__ uint32_t capped_sum(uint32_t x, uint32_t cap) {
+  const uint32_t high = __reduce_add_sync(0xffffffffu, x >> 16), low = __reduce_add_sync(0xffffffffu, x & 0xffffu);
+  const uint64_t sum = (static_cast<uint64_t>(high) << 16) + low;
+  return sum < cap ? static_cast<uint32_t>(sum) : cap;
+}
+
 // One block: the tiles of all sequences, sorted by how many steps they take (a counting
 // sort over 256 lengths), the longest first: dealt out in turns they then end together.
 //   header: [0] tiles, [1] whether there are shares
@@ -75,7 +82,7 @@ constexpr int kLeastShare = 4;                             // steps: less is not
 template <int KEYS, int THREADS>
 __global__ void __launch_bounds__(THREADS) prefill_plan_kernel(const PrefillParams p, int tile_rows) {
   __shared__ int most, count[kPlanBuckets], next[kPlanBuckets], sums[THREADS / 32], busiest;
-  __shared__ unsigned long long claimed;                   // tiles of all sequences
+  __shared__ uint32_t claimed[THREADS / 32];               // tiles of the sequences of each warp
   __shared__ int item_from[THREADS];
   __shared__ PrefillSeq seqs[kPlanSeqs];
   __shared__ int2 unsorted[kPlanTiles];
@@ -83,16 +90,14 @@ __global__ void __launch_bounds__(THREADS) prefill_plan_kernel(const PrefillPara
   allow_next_grid();
   const int me = threadIdx.x, warp = me >> 5, lane = me & 31;
   const int tokens = tile_rows >> p.group_log2;
-  if (me == 0) {
-    most = 1;
-    claimed = 0;
-  }
+  if (me == 0) most = 1;
   if (me < kPlanBuckets) count[me] = 0;
   wait_prior_grids();
   __syncthreads();
   bool bad = false;
   int longest = 1;
-  unsigned long long claims = 0;
+  const uint32_t too_many = static_cast<uint32_t>(p.room) + 1;   // (below 2^31: where sums stop)
+  uint32_t claims = 0;
   for (int b = me; b < p.num_seqs; b += THREADS) {
     const int a = p.starts[b], e = p.starts[b + 1], len = p.lens[b];
     const PrefillSeq s = prefill_seq(p, a, e, len);
@@ -100,20 +105,17 @@ __global__ void __launch_bounds__(THREADS) prefill_plan_kernel(const PrefillPara
     bad |= prefill_bad(p, a, e, len);
     // (a sequence's last tile has the most steps, but for one more at a window's border)
     if (s.n > 0) longest = max(longest, prefill_tile<KEYS>(p, s, (s.n - 1) / tokens, tokens).steps);
-    claims += static_cast<unsigned long long>((s.n + tokens - 1) / tokens);
+    claims = min(claims + static_cast<uint32_t>((s.n + tokens - 1) / tokens), too_many);
   }
   if (bad) report(p.device_errors, PA_DEVERR_BAD_LENGTH);
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-    claims += __shfl_xor_sync(0xffffffffu, claims, o);
-  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  claims = capped_sum(claims, too_many);
   if (lane == 0) {
     atomicMax(&most, longest);
-    atomicAdd(&claimed, claims);
+    claimed[warp] = claims;
   }
   __syncthreads();
-  if (claimed > static_cast<unsigned long long>(p.room)) {
+  if (capped_sum(lane < THREADS / 32 ? claimed[lane] : 0u, too_many) == too_many) {
     if (me < 2) p.header[me] = 0;
     return;
   }
