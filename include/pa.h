@@ -543,8 +543,8 @@ int pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cach
  * up to 3.76 us each; 0: at once, for a prompt with its first copies in flight) and
  * reports PA_DEVERR_TIMEOUT; the kernel then waits for its own copies in flight
  * (with the normal bound) and returns, leaving the context usable.  polls < 0
- * restores the normal bound (15.8 s, of a prompt's waits in which its copies stand still).
- * Process-wide; meant for tests, not for concurrent use.
+ * restores the normal bound (15.8 s).  Process-wide; meant for tests, not for
+ * concurrent use.
  */
 int pa_debug_set_wait_limit(int polls);
 

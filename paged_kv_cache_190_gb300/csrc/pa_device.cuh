@@ -12,7 +12,7 @@ namespace pa {
 // Upper bound on mbarrier polls before a wait gives up and reports PA_DEVERR_TIMEOUT.  A poll
 // itself blocks for up to 3.76 us (64 polls of a barrier that never completes took 240.9 us, 256
 // 963.0), so a stuck wait gives up after 15.8 s; a wait of one pipeline stage takes microseconds.
-// (Waits that may last as long as a whole call have to follow its progress.)
+// (A wait that may rightly last as long as a whole call needs another end.)
 constexpr uint32_t kMaxPolls = 1u << 22;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {

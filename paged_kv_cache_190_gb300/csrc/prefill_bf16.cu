@@ -12,9 +12,9 @@
 // MFLOP (2048 clocks of the tensor cores), 64 KiB of K and V and 32768 exponentials (1024
 // clocks).  On a GB300 (1990 TFLOP/s of bf16 products measured, 1738 in a long run), 32 query
 // and 8 kv heads of 128, first in a graph of a few calls and then among calls that keep the GPU
-// busy for longer: one prompt of 16384 tokens 1325 to 1360 us and 1406 to 1440, 1530 to 1660
-// TFLOP/s of what causality leaves; 12 ragged prompts, 17569 tokens, 233 and 241 to 243, 1180 to
-// 1230; 6 chunks of 200 to 512 tokens behind up to 15000 251 and 258 to 261, 1230 to 1280; one
+// busy for longer: one prompt of 16384 tokens 1327 to 1360 us and 1415 to 1440, 1530 to 1660
+// TFLOP/s of what causality leaves; 12 ragged prompts, 17569 tokens, 235 and 243 to 247, 1160 to
+// 1220; 6 chunks of 200 to 512 tokens behind up to 15000 253 and 259 to 263, 1220 to 1270; one
 // prompt of 37 tokens 6.5.  Heads of 64 have the same exponentials for half the products, and
 // their steps take about as long: 4 prompts of 4096 tokens of 16 heads 171 us, 806 TFLOP/s; 4
 // prompts, 12802 tokens, in windows of 1024 117.
@@ -42,9 +42,8 @@
 //     step come to more than 2^16 (bf16 has float32's range, so they may pass 1), so O is
 //     hardly ever rescaled, and the other steps take no maximum: 128 keys of 32 rows cost a
 //     warp alone 750 clocks instead of 1030.
-//   * Every wait is bounded, by polls or by polls in which the ring stands still; on expiry the
-//     kernel reports PA_DEVERR_TIMEOUT, waits for its own copies and products, frees its tensor
-//     memory and returns.
+//   * Every wait is bounded; on expiry the kernel reports PA_DEVERR_TIMEOUT, waits for its
+//     own copies and products, frees its tensor memory and returns.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -62,6 +61,7 @@ constexpr int kProducer = 8, kIssuer = 9, kCleaner = 10, kIssuerStep = 2;   // i
 constexpr int kThreadsPrefill = 12 * 32;
 constexpr float kMostSum = 65536.f;                        // of a row's weights in one step
 constexpr int kBadRing = 8;
+constexpr uint32_t kPatientPolls = 1u << 28;               // a quarter of an hour
 constexpr uint32_t kTmemO = 256;                           // column of O0; S0 is column 0
 
 template <int D>
@@ -126,32 +126,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // The lowest n bits of a word, n of any size.
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
 
-// The ring's words, one for each of the last kBadRing steps: the step's number, from 1, and below it
-// a bit for each 16 of its keys whose page is none.  Their sum says whether the ring has moved on.
-constexpr uint32_t kBadKeys = 0xff;
-constexpr int kStepBits = 24;
-__device__ __forceinline__ uint32_t ring_sum(const volatile uint32_t* words) {
-  uint32_t x = 0;
-  for (int i = 0; i < kBadRing; ++i) x += words[i];
-  return x;
-}
-
 // Two kinds of waits may rightly last as long as whole items take: the clearing warp's, and those of
-// the second half's softmax behind items that have no rows for it.  They are given up after `limit`
-// polls in which the ring has not moved on; it moves as often as there are steps, so they end.
-// This one: until step number `step` has begun, or `bar` has completed the phase.  (Not inlined, for
-// the registers of the softmax loop beside it; and every wait this way would cost 2 to 4 %.)
-__device__ __noinline__ void follow_ring(const volatile uint32_t* words, uint32_t step, uint64_t* bar, uint32_t parity,
-                                         volatile int* abort_flag, uint32_t limit) {
-  uint32_t seen = 0;
-  for (uint32_t polls = 0; polls < limit && !*abort_flag; ++polls) {
-    // (numbers are compared modulo 2^24)
-    const uint32_t ahead = (words[(step - 1) % kBadRing] >> (32 - kStepBits)) - step;
-    if (static_cast<int32_t>(ahead << (32 - kStepBits)) >= 0 || mbar_try_wait(bar, parity)) return;
-    const uint32_t now = ring_sum(words);
-    if (now != seen) polls = 0;
-    seen = now;
+// the second half's softmax behind items that have no rows for it.  They end with the wait of some
+// other warp, for nothing stands still without one of the producer's or the issuers' waits, which
+// are of one stage, running out and raising the flag.  (In every wait of the softmax this costs 1 to
+// 2 % of windows; going along with the ring's steps instead costs up to 5 % of many short chunks.)
+__device__ __forceinline__ bool patient_wait(uint64_t* bar, uint32_t parity, const volatile int* abort_flag) {
+  for (uint32_t i = 0; i < kPatientPolls; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
   }
+  return false;
 }
 
 template <int D>
@@ -194,7 +179,6 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
     }
     mbar_init(end, 2);
     *abort_flag = 0;
-    for (int i = 0; i < kBadRing; ++i) bad_ring[i] = 0;
     fence_mbar_init();
   }
   if (warp == kIssuer) {
@@ -219,14 +203,6 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     // (the flag is not looked at where the first poll says yes, as it nearly always does)
     return mbar_try_wait(bar, parity) || (!*abort_flag && mbar_wait(bar, parity, p.wait_limit));
-  };
-  auto patient_wait = [&](uint64_t* bar, uint32_t parity) {   // (see follow_ring)
-    for (uint32_t seen = ring_sum(bad_ring);;) {
-      if (wait(bar, parity)) return true;
-      const uint32_t now = ring_sum(bad_ring);
-      if (now == seen || *abort_flag) return false;
-      seen = now;
-    }
   };
   PrefillWalk<kPrefillKeys> walk(p, tile_tokens);
   PrefillItem it;
@@ -275,7 +251,10 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
           return page >= 0 && page < p.num_blocks ? page * p.num_kv_heads + it.h : -1;
         };
         int ahead = look(it.v0);
-        for (int v = it.v0; v < it.v1; ++v, ++steps) {
+        // (no polls: given up for certain, behind a step whose copies are in flight.  Asked in the
+        // first poll of every wait this would cost 2 to 3 %, and for each step 0.6.)
+        const int v_end = p.wait_limit != 0 ? it.v1 : it.v0 + 1;
+        for (int v = it.v0; v < v_end; ++v, ++steps) {
           const int z = ahead;
           ahead = look(v + 1);
           const int t0 = (v + (v >= it.t.ns ? it.t.shift : 0)) * kPrefillKeys, hi = min(it.t.end, t0 + kPrefillKeys);
@@ -294,7 +273,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
               for (int i = 0; i < 4; ++i)
                 if ((gone >> i) & 1) word |= 3u << (2 * i);
             }
-            bad_ring[steps % kBadRing] = ((steps + 1) << (32 - kStepBits)) | word;
+            bad_ring[steps % kBadRing] = word;
             mbar_arrive_expect_tx(&full[slot], bytes);
           }
           raw_used &= ~(1u << slot);
@@ -319,13 +298,8 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
           if (z >= -1)
             tma_load_4d(smem + Ly::OFF_RING + slot * Ly::TILE + lane * bs * D * 2, &p.map_v, 0, 0, z, 0, bar);
           ++c;
-          // (no polls: a wait that expires for certain, with a step's copies in flight.  In the first
-          // poll of every wait the question would cost 2 to 3 %.)
-          if (p.wait_limit == 0) {
-            ok = false;
-            break;
-          }
         }
+        ok = ok && p.wait_limit != 0;
       }
       if (!ok && lane == 0) fail();
       // the copies still in flight must land before the shared memory is released
@@ -349,7 +323,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
           int x, y;
           const bool behind = hidden(it.t, t0, hi, x, y);
           if ((hi & 15) == 0 && !behind) continue;
-          ok = patient_wait(&raw[slot], (raw_parity >> slot) & 1);
+          ok = patient_wait(&raw[slot], (raw_parity >> slot) & 1, abort_flag);
           ok = __all_sync(kFull, ok);
           if (!ok) break;
           raw_parity ^= 1u << slot;
@@ -504,7 +478,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
         // nothing may be in flight when the columns are released
         if (issues) {
           umma_commit(end);
-          mbar_wait(end, 0);
+          if (!mbar_wait(end, 0)) fail();
         }
         __syncwarp();
       }
@@ -523,8 +497,6 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
       const PrefillTile& t = it.t;
       if (half == 1 && (t.tokens << p.group_log2) <= 128) {
         steps += t.steps > 0 ? it.v1 - it.v0 : 0;
-        // (whether the ring stands still is a later wait's to say)
-        if (t.steps > 0) follow_ring(bad_ring, steps, &s_full[1], n & 1, abort_flag, p.wait_limit);
         continue;
       }
       const int j = r >> p.group_log2;
@@ -532,6 +504,8 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
       const int first_pos = t.pos0 + ((r & ~31) >> p.group_log2);
       const int last_pos = t.pos0 + min((r | 31) >> p.group_log2, t.tokens - 1);
       float m = kNoScore, l = 0.f;
+      // (behind items that this half had no rows of; if nothing comes, the first step says so)
+      if (n != steps && t.steps > 0) patient_wait(&s_full[half], n & 1, abort_flag);
       for (int v = it.v0; v < (t.steps > 0 ? it.v1 : it.v0); ++v, ++n, ++steps) {
         const int t0 = (v + (v >= t.ns ? t.shift : 0)) * kPrefillKeys;
         // does every row of this warp see every key of the step?
@@ -542,7 +516,7 @@ __global__ void __launch_bounds__(kThreadsPrefill, 1) prefill_bf16_kernel(const 
         float s[128];
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s + 32 * i);
-        const uint32_t bad = bad_ring[steps % kBadRing] & kBadKeys;
+        const uint32_t bad = bad_ring[steps % kBadRing];
         tmem_landed(s);
         if (!sees_all || bad != 0) {
           const int last = pos - t0, first = pos - p.window + 1 - t0, sinks = p.sinks - t0;
